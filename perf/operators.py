@@ -470,15 +470,17 @@ def _dispatch_exact(s):
         if s["weighted"]:
             rows = rows * s["weights"].double().reshape(-1)[v][:, None]
         x[at : at + v.numel()] = rows
-    if s["recipe"] == "mx":  # bytes and powers of two: held to the plain form's
-        return {"codes": None, "scales": None, "codes_t": None, "scales_t": None}
-    most = FP8[s["fmt"]][1]
+    kind, most, _ = FP8[s["fmt"]]
 
     def of(v):
-        b = _blocks(v, 128)
+        """The codes' values, each the nearest to its quotient, and what they are multiplied by to stand for v."""
+        b = _blocks(v, 128 if s["recipe"] == "block" else 32)
         top = b.abs().amax(-1)
-        inv = torch.where(top > 0, top / most, 1.0)
-        return (b / inv[..., None]).flatten(-2)[..., : v.shape[-1]], inv
+        if s["recipe"] == "block":
+            inv = scales = torch.where(top > 0, top / most, 1.0)
+        else:  # bytes: whole numbers, held to the plain form's
+            inv, scales = 2.0 ** torch.where(top > 0, torch.ceil(torch.log2(top / most)), 0.0), None
+        return (b / inv[..., None]).clamp(-most, most).to(kind).double().flatten(-2)[..., : v.shape[-1]], scales
 
     q, si = of(x)
     qt, st = of(x.t())
