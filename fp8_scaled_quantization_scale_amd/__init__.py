@@ -35,12 +35,18 @@ GEMM_TENSOR, GEMM_BLOCK_1x128_128x128, GEMM_BLOCK_1x128_1x128, GEMM_MX_1x32 = 0,
 GEMM_BLOCK_128x128_128x128, GEMM_CHANNEL = 4, 5
 LAYOUT_TN = 0
 AMAX_SLOTS = 1024  # floats in the amax array of a per-tensor cast
+EXPERT_ALIGN, MAX_EXPERTS = 128, 1024
+IDX_I32, IDX_I64 = 0, 1
+GROUP_ROWS, GROUP_CONTRACT = 0, 1
 
 FMT = {"e4m3": E4M3, "e5m2": E5M2}
 TORCH_FP8 = {E4M3: torch.float8_e4m3fn, E5M2: torch.float8_e5m2}
 
 EXPORTS = ("fp8_quantize", "fp8_quantize_static_scratch", "fp8_amax_history_update", "fp8_gemm_scaled",
-           "fp8_bf16_gemm", "fp8_status_string", "fp8_version")
+           "fp8_bf16_gemm", "fp8_status_string", "fp8_version",
+           "fp8_layer_norm_forward", "fp8_layer_norm_workspace", "fp8_layer_norm_backward",
+           "fp8_moe_rows", "fp8_moe_sort_workspace", "fp8_moe_sort", "fp8_moe_dispatch", "fp8_moe_quantize",
+           "fp8_moe_combine", "fp8_moe_combine_backward", "fp8_gemm_grouped")
 
 
 class Fp8Error(RuntimeError):
@@ -71,6 +77,32 @@ def load(path: str = LIB_PATH):
                                     vp, i32, i64, vp]
     lib.fp8_bf16_gemm.restype = i32
     lib.fp8_bf16_gemm.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i32, i64, vp]
+    f32 = ctypes.c_float
+    lib.fp8_layer_norm_forward.restype = i32
+    lib.fp8_layer_norm_forward.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, i64, vp, vp, vp]
+    lib.fp8_layer_norm_workspace.restype = i64
+    lib.fp8_layer_norm_workspace.argtypes = [i64, i64]
+    lib.fp8_layer_norm_backward.restype = i32
+    lib.fp8_layer_norm_backward.argtypes = [vp, i64, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i64, vp, vp, vp, i64, vp]
+    lib.fp8_moe_rows.restype = i64
+    lib.fp8_moe_rows.argtypes = [i64, i64, i64]
+    lib.fp8_moe_sort_workspace.restype = i64
+    lib.fp8_moe_sort_workspace.argtypes = [i64, i64, i64]
+    lib.fp8_moe_sort.restype = i32
+    lib.fp8_moe_sort.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, vp, i64, vp, vp, i64, vp]
+    lib.fp8_moe_dispatch.restype = i32
+    lib.fp8_moe_dispatch.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, i64, vp, i64, i64, vp]
+    lib.fp8_moe_quantize.restype = i32
+    lib.fp8_moe_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i64, i64, i32, i32, i32, i32,
+                                     vp, i64, vp, vp, i64, vp, vp, vp]
+    lib.fp8_moe_combine.restype = i32
+    lib.fp8_moe_combine.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp]
+    lib.fp8_moe_combine_backward.restype = i32
+    lib.fp8_moe_combine_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, vp, i64, i64,
+                                             vp, vp]
+    lib.fp8_gemm_grouped.restype = i32
+    lib.fp8_gemm_grouped.argtypes = [vp, i32, vp, i64, vp, i32, vp, i64, i64, i64, i64, i32, i32, vp, i64, i64, i64,
+                                     i64, i64, vp, i32, i64, i64, vp]
     lib.fp8_status_string.restype = ctypes.c_char_p
     lib.fp8_status_string.argtypes = [i32]
     lib.fp8_version.restype = i32
@@ -168,9 +200,106 @@ def fp8_bf16_gemm(a, lda, b, ldb, M, N, K, c, c_dtype, ldc, stream=None) -> int:
     return load().fp8_bf16_gemm(_p(a), lda, _p(b), ldb, M, N, K, _p(c), c_dtype, ldc, _stream(stream))
 
 
+def fp8_layer_norm_forward(x, x_dtype, rows, cols, ld_x, weight, bias, w_dtype, eps, y, ld_y, mean, rstd,
+                           stream=None) -> int:
+    return load().fp8_layer_norm_forward(_p(x), x_dtype, rows, cols, ld_x, _p(weight), _p(bias), w_dtype, eps,
+                                         _p(y), ld_y, _p(mean), _p(rstd), _stream(stream))
+
+
+def fp8_layer_norm_workspace(rows, cols) -> int:
+    return load().fp8_layer_norm_workspace(rows, cols)
+
+
+def fp8_layer_norm_backward(dy, ld_dy, x, x_dtype, rows, cols, ld_x, weight, w_dtype, mean, rstd, dx, ld_dx,
+                            dweight, dbias, workspace, workspace_bytes, stream=None) -> int:
+    return load().fp8_layer_norm_backward(_p(dy), ld_dy, _p(x), x_dtype, rows, cols, ld_x, _p(weight), w_dtype,
+                                          _p(mean), _p(rstd), _p(dx), ld_dx, _p(dweight), _p(dbias), _p(workspace),
+                                          workspace_bytes, _stream(stream))
+
+
+def fp8_moe_rows(tokens, topk, experts) -> int:
+    return load().fp8_moe_rows(tokens, topk, experts)
+
+
+def fp8_moe_sort_workspace(tokens, topk, experts) -> int:
+    return load().fp8_moe_sort_workspace(tokens, topk, experts)
+
+
+def fp8_moe_sort(expert, idx_dtype, tokens, topk, ld_expert, experts, offsets, counts, row_slot, rows, slot_row,
+                 workspace, workspace_bytes, stream=None) -> int:
+    return load().fp8_moe_sort(_p(expert), idx_dtype, tokens, topk, ld_expert, experts, _p(offsets), _p(counts),
+                               _p(row_slot), rows, _p(slot_row), _p(workspace), workspace_bytes, _stream(stream))
+
+
+def fp8_moe_dispatch(x, dtype, tokens, cols, ld_x, topk, weights, slot_row, offsets, counts, experts, y, rows, ld_y,
+                     stream=None) -> int:
+    return load().fp8_moe_dispatch(_p(x), dtype, tokens, cols, ld_x, topk, _p(weights), _p(slot_row), _p(offsets),
+                                   _p(counts), experts, _p(y), rows, ld_y, _stream(stream))
+
+
+def fp8_moe_quantize(x, x_dtype, x_rows, cols, ld_x, row_slot, topk, weights, offsets, experts, rows, recipe, fmt,
+                     orient, margin, q_row, ld_q_row, s_row, q_col, ld_q_col, s_col, nonfinite, stream=None) -> int:
+    return load().fp8_moe_quantize(_p(x), x_dtype, x_rows, cols, ld_x, _p(row_slot), topk, _p(weights), _p(offsets),
+                                   experts, rows, recipe, fmt, orient, margin, _p(q_row), ld_q_row, _p(s_row),
+                                   _p(q_col), ld_q_col, _p(s_col), _p(nonfinite), _stream(stream))
+
+
+def fp8_moe_combine(ys, dtype, rows, cols, ld_ys, slot_row, tokens, topk, weights, y, ld_y, stream=None) -> int:
+    return load().fp8_moe_combine(_p(ys), dtype, rows, cols, ld_ys, _p(slot_row), tokens, topk, _p(weights), _p(y),
+                                  ld_y, _stream(stream))
+
+
+def fp8_moe_combine_backward(dy, dtype, tokens, cols, ld_dy, ys, ld_ys, slot_row, offsets, counts, experts, topk,
+                             weights, dys, rows, ld_dys, dweights, stream=None) -> int:
+    return load().fp8_moe_combine_backward(_p(dy), dtype, tokens, cols, ld_dy, _p(ys), ld_ys, _p(slot_row),
+                                           _p(offsets), _p(counts), experts, topk, _p(weights), _p(dys), rows, ld_dys,
+                                           _p(dweights), _stream(stream))
+
+
+def fp8_gemm_grouped(a, fmt_a, s_a, lda, b, fmt_b, s_b, ldb, stride_b, ld_sb, stride_sb, recipe, group, offsets,
+                     experts, rows, M, N, K, c, c_dtype, ldc, stride_c, stream=None) -> int:
+    return load().fp8_gemm_grouped(_p(a), fmt_a, _p(s_a), lda, _p(b), fmt_b, _p(s_b), ldb, stride_b, ld_sb, stride_sb,
+                                   recipe, group, _p(offsets), experts, rows, M, N, K, _p(c), c_dtype, ldc, stride_c,
+                                   _stream(stream))
+
+
 # ---------------------------------------------------------------------------
 # conveniences: allocate outputs with torch, call the entry points above
+# (norm.py and moe.py hold those of the layer norm and of the experts)
 # ---------------------------------------------------------------------------
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *_):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _scope(device: torch.device, stream):
+    """Where a call allocates and launches: on `stream` (a torch stream or a
+    raw handle), else on the current stream of the tensors' device.  What is
+    allocated inside belongs to that stream, so a workspace that is freed when
+    the call returns is not handed to another stream's work before its own."""
+    if stream is None:
+        return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _one_device(first: torch.Tensor, *others) -> None:
+    for t in others:
+        _need(t is None or t.device == first.device, "all tensors must be on one device")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension of a 2-D tensor (of one row, any stride will do)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
 
 def _ceil(a: int, b: int) -> int:
     return (a + b - 1) // b

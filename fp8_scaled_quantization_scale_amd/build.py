@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8mi.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["api.cpp", "quantize.hip", "history.hip", "gemm.hip"]
+SOURCES = ["gemm.hip", "quantize.hip", "norm.hip", "moe.hip", "history.hip", "api.cpp", "api_moe.cpp", "api_norm.cpp"]
 PROBE_LIB = os.path.join(HERE, "libfp8mi_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
@@ -65,7 +65,7 @@ def _link(objs, lib: str):
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = SOURCES + PROBE_SOURCES
-    with ThreadPoolExecutor(max_workers=min(5, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = dict(zip(srcs, ex.map(_compile, srcs)))
     _link([objs[s] for s in SOURCES], LIB)
     _link([objs[s] for s in PROBE_SOURCES], PROBE_LIB)

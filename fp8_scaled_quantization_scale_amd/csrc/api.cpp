@@ -10,14 +10,16 @@
 #include "launch.hpp"
 
 namespace {
-
 thread_local char g_hip_msg[256] = "no HIP error recorded";
+}  // namespace
 
-int hip_status(hipError_t e) {
+int fp8mi::hip_status(hipError_t e) {
   if (e == hipSuccess) return FP8MI_OK;
   std::snprintf(g_hip_msg, sizeof(g_hip_msg), "HIP error %d: %s", (int)e, hipGetErrorString(e));
   return FP8MI_ERR_HIP;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -112,7 +114,7 @@ int fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t
   fp8mi::QuantParams p{x,      x_dtype,  rows,  cols,  ld_x,     recipe, fmt,      orient, margin,
                        q_row,  ld_q_row, s_row, q_col, ld_q_col, s_col,  scale,    scale_inv,
                        amax,   nonfinite};
-  return hip_status(fp8mi::launch_quantize(p, (hipStream_t)stream));
+  return fp8mi::hip_status(fp8mi::launch_quantize(p, (hipStream_t)stream));
 }
 
 int fp8_quantize_static_scratch(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x, int recipe,
@@ -126,7 +128,7 @@ int fp8_quantize_static_scratch(const void* x, int x_dtype, int64_t rows, int64_
   fp8mi::QuantParams p{x,      x_dtype,  rows,  cols,  ld_x,     recipe, fmt,      orient, margin,
                        q_row,  ld_q_row, s_row, q_col, ld_q_col, s_col,  scale,    scale_inv,
                        amax,   nonfinite};
-  return hip_status(fp8mi::launch_quantize_static_scratch(p, (hipStream_t)stream));
+  return fp8mi::hip_status(fp8mi::launch_quantize_static_scratch(p, (hipStream_t)stream));
 }
 
 int fp8_amax_history_update(float* history, int32_t* head, int64_t len, float* amax, int fmt, int margin,
@@ -134,7 +136,7 @@ int fp8_amax_history_update(float* history, int32_t* head, int64_t len, float* a
   if (fmt != FP8MI_E4M3 && fmt != FP8MI_E5M2) return FP8MI_ERR_ENUM;
   if (!history || !head || !amax || !scale || !scale_inv) return FP8MI_ERR_NULL;
   if (len < 1 || len > 65536 || margin < 0 || margin > 64) return FP8MI_ERR_SHAPE;
-  return hip_status(fp8mi::launch_history(history, head, (int)len, amax, fmt, margin, scale, scale_inv,
+  return fp8mi::hip_status(fp8mi::launch_history(history, head, (int)len, amax, fmt, margin, scale, scale_inv,
                                           nonfinite, (hipStream_t)stream));
 }
 
@@ -145,7 +147,7 @@ int fp8_gemm_scaled(const uint8_t* a, int fmt_a, const void* s_a, int64_t lda, c
   if (st != FP8MI_OK) return st;
   if (M == 0 || N == 0) return FP8MI_OK;
   fp8mi::GemmParams p{a, fmt_a, s_a, lda, b, fmt_b, s_b, ldb, recipe, M, N, K, c, c_dtype, ldc};
-  return hip_status(fp8mi::launch_gemm(p, (hipStream_t)stream));
+  return fp8mi::hip_status(fp8mi::launch_gemm(p, (hipStream_t)stream));
 }
 
 int fp8_bf16_gemm(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
@@ -167,7 +169,7 @@ int fp8_bf16_gemm(const void* a, int64_t lda, const void* b, int64_t ldb, int64_
   if (!tile_count_ok(M, N)) return FP8MI_ERR_UNSUPPORTED;
   fp8mi::GemmParams p{reinterpret_cast<const uint8_t*>(a), 0, nullptr, lda, reinterpret_cast<const uint8_t*>(b), 0,
                       nullptr, ldb, FP8MI_GEMM_TENSOR, M, N, K, c, c_dtype, ldc};
-  return hip_status(fp8mi::launch_gemm_bf16(p, (hipStream_t)stream));
+  return fp8mi::hip_status(fp8mi::launch_gemm_bf16(p, (hipStream_t)stream));
 }
 
 const char* fp8_status_string(int status) {

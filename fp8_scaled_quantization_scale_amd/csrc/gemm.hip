@@ -58,6 +58,7 @@
 // BF16 GEMM FP8's speedup is measured against ("Mastering FP8 LLM training",
 // Fig. 1): a 128-byte K step is 64 BF16 elements, the two 16-byte halves of a
 // fragment feed two 32-deep products, and everything else is shared.
+#include <type_traits>
 #include <utility>
 
 #include "device.hpp"
@@ -177,6 +178,17 @@ __device__ __forceinline__ void wait_vmcnt() {
 }
 __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
+// Grouped products (one B or one contraction range per expert, see
+// fp8_gemm_grouped): the same kernel, whose tiles are cut from segments of
+// the rows [0, R) that a device array of offsets gives.
+//   kGrpRows      C[r] = A[r] . B_e^T for the rows r of segment e: an output
+//                 tile lies in one segment, its rows end where that does
+//   kGrpContract  C_e = A[:, seg e] . B[:, seg e]^T: every expert has all the
+//                 output tiles, and a K loop of its own length
+// Segments start on multiples of 128, so a K window starts on a 16-byte chunk
+// and on a scale block, and a row tile on whole scale words.
+constexpr int kGrpNone = 0, kGrpRows = 1, kGrpContract = 2;
+
 struct GArgs {
   const uint8_t* a;
   const uint8_t* b;
@@ -187,6 +199,14 @@ struct GArgs {
   int nkb;  // scale entries per operand row: K blocks of 128 (FP32 words) or of 32 (MX bytes)
   void* c;
   int tiles_m, tiles_n;
+};
+struct GroupArgs : GArgs {
+  const int32_t* offsets;  // [experts + 1]
+  int experts, R;          // R: rows of A (kGrpRows) / columns of A and B (kGrpContract)
+  int64_t stride_b;        // bytes from one expert's B to the next one's
+  int64_t stride_sb;       // scale entries from one expert's B scales to the next one's
+  int nkb_b;               // scale entries from one row (or 128-row tile) of B to the next
+  int64_t stride_c;        // elements from one expert's C to the next one's
 };
 
 // What each recipe stages per K step.
@@ -205,8 +225,8 @@ struct Scl {
   static constexpr bool kHoistDma = !kRowB && !kMx && REC != kGemmChannel && REC != kGemmBlock128x128;
 };
 
-template <int FA, int FB, int REC, int OUT>
-__global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
+template <int FA, int FB, int REC, int OUT, int GRP>
+__global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == kGrpNone, GArgs, GroupArgs> p) {
   using S = Scl<REC>;
   constexpr bool kScl = S::kSclAny;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kTileBytes];
@@ -233,43 +253,123 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
   const uint32_t fb_lo = (uint32_t)(kBM * kBK + brow0 * kBK + ((lg ^ swb) << 4));
   const uint32_t fb_hi = (uint32_t)(kBM * kBK + brow0 * kBK + (((4 + lg) ^ swb) << 4));
 
+  // grouped: the segments' bounds, and for kGrpRows each segment's first tile
+  // (at most 64 KB tiles + 8 KB: the 160 KB of LDS hold them beside the stages)
+  __shared__ int seg_at[GRP == kGrpNone ? 1 : kMaxExperts + 1];
+  __shared__ int seg_tile[GRP == kGrpRows ? kMaxExperts + 1 : 1];
+  if constexpr (GRP != kGrpNone) {
+    // whatever the array holds, every segment lies in [0, R) on multiples of 128
+    for (int e = tid; e <= p.experts; e += 512) seg_at[e] = min(max(p.offsets[e], 0), p.R) & ~127;
+    __syncthreads();
+  }
+  if constexpr (GRP == kGrpRows) {
+    if (wave == 0) {
+      int before = 0;
+      for (int e0 = 0; e0 < p.experts; e0 += 64) {
+        const int e = e0 + lane;
+        int n = e < p.experts ? (max(seg_at[e + 1] - seg_at[e], 0) + kBM - 1) / kBM * p.tiles_n : 0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {  // inclusive scan over the wave
+          const int o = __shfl_up(n, off, 64);
+          if (lane >= off) n += o;
+        }
+        if (e < p.experts) seg_tile[e + 1] = before + n;
+        before += __shfl(n, 63, 64);
+      }
+      if (lane == 0) seg_tile[0] = 0;
+    }
+    __syncthreads();
+  }
 
-  const int total = p.tiles_m * p.tiles_n;
+  int total = p.tiles_m * p.tiles_n;
+  if constexpr (GRP == kGrpRows) total = __builtin_amdgcn_readfirstlane(seg_tile[p.experts]);
+  if constexpr (GRP == kGrpContract) total *= p.experts;
 #pragma unroll 1
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     __syncthreads();  // every wave is done with the previous tile's LDS
     // ---- tile assignment: XCD-contiguous ranges of the tile index (tiles t and
     // t + gridDim.x stay on one XCD when gridDim.x % 8 == 0), grouped 8 tile-rows deep
     int pid = tile;
-    if ((total & 7) == 0) pid = (pid & 7) * (total >> 3) + (pid >> 3);
+    if constexpr (GRP == kGrpNone) {
+      if ((total & 7) == 0) pid = (pid & 7) * (total >> 3) + (pid >> 3);
+    } else {
+      // any total: the first total % 8 XCDs take one tile more
+      pid = (tile & 7) * (total >> 3) + min(tile & 7, total & 7) + (tile >> 3);
+    }
+    // grouped: the tile's expert, its segment [s0, s1), and the tile's number among the expert's
+    int ex = 0, s0 = 0, s1 = 0, tiles_m = p.tiles_m;
+    if constexpr (GRP == kGrpRows) {
+      // segments that end at or before the tile, 64 at a time
+      for (int e0 = 0; e0 < p.experts; e0 += 64) {
+        const int e = e0 + lane;
+        ex += __popcll(__ballot(e < p.experts && seg_tile[min(e, p.experts - 1) + 1] <= pid));
+      }
+      pid -= __builtin_amdgcn_readfirstlane(seg_tile[ex]);
+    } else if constexpr (GRP == kGrpContract) {
+      ex = pid / (p.tiles_m * p.tiles_n);
+      pid -= ex * (p.tiles_m * p.tiles_n);
+    }
+    if constexpr (GRP != kGrpNone) {
+      s0 = __builtin_amdgcn_readfirstlane(seg_at[ex]);
+      s1 = max(__builtin_amdgcn_readfirstlane(seg_at[ex + 1]), s0);
+    }
+    if constexpr (GRP == kGrpRows) tiles_m = (s1 - s0 + kBM - 1) / kBM;
     constexpr int GROUP_M = 8;
     const int in_group = GROUP_M * p.tiles_n;
     const int first_m = (pid / in_group) * GROUP_M;
-    const int gsize = min(p.tiles_m - first_m, GROUP_M);
+    const int gsize = min(tiles_m - first_m, GROUP_M);
     const int pm = first_m + (pid % in_group) % gsize;
     const int pn = (pid % in_group) / gsize;
-    const int m0 = pm * kBM, n0 = pn * kBN;
-    const int rows_a = min(kBM, p.M - m0), rows_b = min(kBN, p.N - n0);
-    const int KT = (p.K + kBK - 1) / kBK;
+    const int m0 = (GRP == kGrpRows ? s0 : 0) + pm * kBM, n0 = pn * kBN;
+    const int m_end = GRP == kGrpRows ? s1 : p.M;  // the tile's rows end here
+    const int K = GRP == kGrpContract ? s1 - s0 : p.K;
+    const int rows_a = min(kBM, m_end - m0), rows_b = min(kBN, p.N - n0);
+    const int KT = (K + kBK - 1) / kBK;
+    // grouped: bytes before the operands' K windows, the expert's B and its
+    // scales; scale entries between two rows of A and of B.  The ranges end
+    // with the last row's window, so that no read leaves the operands however
+    // far apart their rows lie.
+    const int k_at = GRP == kGrpContract ? s0 : 0;
+    const uint8_t* b_ex = p.b;
+    int64_t sb_ex = 0;
+    int nkb_b = p.nkb;
+    if constexpr (GRP == kGrpRows) {
+      b_ex += ex * p.stride_b;
+      sb_ex = ex * p.stride_sb;
+      nkb_b = p.nkb_b;
+    }
+    const int nblk = GRP == kGrpContract ? K / (S::kMx ? 32 : 128) : p.nkb;  // scale blocks along K
+    auto span = [&](int rows, int64_t ld, int64_t n) __attribute__((always_inline)) -> int64_t {
+      return GRP == kGrpNone ? rows * ld : (rows - 1) * ld + n;
+    };
 
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (int64_t)m0 * p.lda, (uint32_t)(rows_a * p.lda));
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + (int64_t)n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (int64_t)m0 * p.lda + k_at, (uint32_t)span(rows_a, p.lda, K));
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(b_ex + (int64_t)n0 * p.ldb + k_at, (uint32_t)span(rows_b, p.ldb, K));
     // scale rows of this tile (range-checked: rows past the matrix read as zero)
     __amdgpu_buffer_rsrc_t rsa = make_rsrc(nullptr, 0), rsb = make_rsrc(nullptr, 0);
     if constexpr (S::kRowA)
-      rsa = make_rsrc(static_cast<const uint32_t*>(p.sa) + (int64_t)m0 * p.nkb, (uint32_t)(rows_a * p.nkb * 4));
+      rsa = make_rsrc(static_cast<const uint32_t*>(p.sa) + (int64_t)m0 * p.nkb + k_at / 128,
+                      (uint32_t)(span(rows_a, p.nkb, nblk) * 4));
     if constexpr (S::kTileA)
       rsa = make_rsrc(static_cast<const uint32_t*>(p.sa) + (int64_t)(m0 / 128) * p.nkb,
                       (uint32_t)(((rows_a + 127) / 128) * p.nkb * 4));
     if constexpr (S::kMx)
-      rsa = make_rsrc(static_cast<const uint8_t*>(p.sa) + (int64_t)m0 * p.nkb, (uint32_t)((rows_a * p.nkb + 3) & ~3));
+      rsa = make_rsrc(static_cast<const uint8_t*>(p.sa) + (int64_t)m0 * p.nkb + k_at / 32,
+                      (uint32_t)((span(rows_a, p.nkb, nblk) + 3) & ~3));
     if constexpr (S::kRowB)
-      rsb = make_rsrc(static_cast<const uint32_t*>(p.sb) + (int64_t)n0 * p.nkb, (uint32_t)(rows_b * p.nkb * 4));
+      rsb = make_rsrc(static_cast<const uint32_t*>(p.sb) + (int64_t)n0 * p.nkb + k_at / 128,
+                      (uint32_t)(span(rows_b, p.nkb, nblk) * 4));
     if constexpr (S::kTileB)
-      rsb = make_rsrc(static_cast<const uint32_t*>(p.sb) + (int64_t)(n0 / 128) * p.nkb,
-                      (uint32_t)(((rows_b + 127) / 128) * p.nkb * 4));
-    if constexpr (S::kMx)
-      rsb = make_rsrc(static_cast<const uint8_t*>(p.sb) + (int64_t)n0 * p.nkb, (uint32_t)((rows_b * p.nkb + 3) & ~3));
+      rsb = make_rsrc(static_cast<const uint32_t*>(p.sb) + sb_ex + (int64_t)(n0 / 128) * nkb_b,
+                      (uint32_t)(span((rows_b + 127) / 128, nkb_b, nblk) * 4));
+    // (an expert's E8M0 bytes may start inside a dword: sb_mis bytes in)
+    int sb_mis = 0;
+    if constexpr (S::kMx) {
+      const int64_t at = sb_ex + (int64_t)n0 * nkb_b + k_at / 32;
+      if constexpr (GRP == kGrpRows) sb_mis = (int)(at & 3);
+      rsb = make_rsrc(static_cast<const uint8_t*>(p.sb) + at - sb_mis,
+                      (uint32_t)((sb_mis + span(rows_b, nkb_b, nblk) + 3) & ~3));
+    }
 
     // One 1 KB tile segment (8 rows): segments 0..31 are A rows 8s.., 32..63
     // B rows 8(s-32)...  Lane l fetches chunk (l % 8) ^ swizzle of row 8s + l / 8: for an A row
@@ -311,7 +411,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
         vo = (is_a ? base_a : ((seg & 2) ? base_b1 : base_b0)) + (uint32_t)(8 * (seg & 31)) * ld;
       }
       if constexpr (decltype(Tail)::value) {
-        if (k0 + chunk(is_a, seg) >= p.K) vo = kOOB;
+        if (k0 + chunk(is_a, seg) >= K) vo = kOOB;
       }
       uint32_t lb = __builtin_amdgcn_readfirstlane(lds_base + (kt & 1) * kTileBytes);
       asm volatile("" : "+s"(lb));
@@ -327,8 +427,9 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
     auto dma_scl = [&](int kt, bool a_side, __amdgpu_buffer_rsrc_t rs) __attribute__((always_inline)) {
       uint32_t sb = __builtin_amdgcn_readfirstlane(scl_base + ((kt / kSG) & 1) * kSclBytes);
       asm volatile("" : "+s"(sb));
+      const int nkb = a_side ? p.nkb : nkb_b, mis = a_side ? 0 : sb_mis;
       auto first = [&](int row) -> uint32_t {  // aligned start of a row's group window
-        return S::kMx ? ((((uint32_t)(row * p.nkb)) & ~3u) + 4u * kt) : (uint32_t)((row * p.nkb + kt) * 4);
+        return S::kMx ? ((((uint32_t)(mis + row * nkb)) & ~3u) + 4u * kt) : (uint32_t)((row * nkb + kt) * 4);
       };
       if (a_side) {
         if constexpr (S::kTileA) {
@@ -340,7 +441,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
         }
       } else {
         if constexpr (S::kTileB) {
-          if (q == 0) dma16(rs, sb + kSclBLo, lane < 2 ? (uint32_t)((lane * p.nkb + kt) * 4) : kOOB, 0);
+          if (q == 0) dma16(rs, sb + kSclBLo, lane < 2 ? (uint32_t)((lane * nkb_b + kt) * 4) : kOOB, 0);
         } else {
           dma16(rs, sb + kSclBLo + 16 * 64 * q, first(64 * q + lane), 0);
           if constexpr (S::kMx) dma4(rs, sb + kSclBHi + 4 * 64 * q, first(64 * q + lane) + 16u);
@@ -365,7 +466,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
       }
     };
     auto issue = [&](int kt) __attribute__((always_inline)) {
-      if (kt * kBK + kBK <= p.K) issue_set(kt, std::false_type{});
+      if (kt * kBK + kBK <= K) issue_set(kt, std::false_type{});
       else issue_set(kt, std::true_type{});
     };
 
@@ -415,8 +516,9 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
     // dword after them); mis is ((lr % 4) nkb) % 4 for every row a lane reads
     // (tiles start on multiples of 4 rows), so the lane's byte of step kt is
     // window byte b = mis + lg + 4 (kt % kSG), the same for all its rows.
-    auto mx_b = [&](int kt) __attribute__((always_inline)) -> int {
-      return (((lr & 3) * p.nkb) & 3) + lg + 4 * (kt % kSG);
+    // (grouped: B's rows may lie another number of bytes apart, and start inside a dword)
+    auto mx_b = [&](int kt, int nkb, int mis) __attribute__((always_inline)) -> int {
+      return ((mis + (lr & 3) * nkb) & 3) + lg + 4 * (kt % kSG);
     };
     // where row `row`'s byte b sits: in its 16 bytes at LO, or in the dword after at HI
     auto mx_at = [&](const uint8_t* sc, int lo, int hi, int row, int b) __attribute__((always_inline)) -> const uint8_t* {
@@ -483,12 +585,13 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
       // multiply phase opens with MFMAs
       if constexpr (S::kTileA) stile *= *reinterpret_cast<const float*>(sc + kSclALo + 1024 * wm + ks);
       if constexpr (S::kMx) {
-        const int b = mx_b(kt);
+        const int b = mx_b(kt, p.nkb, 0);
+        const int bb = GRP == kGrpRows ? mx_b(kt, nkb_b, sb_mis) : b;  // the B rows' byte
         if (kt % kSG < kSG - 1) {
           // b <= 14: every lane's byte is among its rows' 16 staged bytes,
           // at a constant distance from its first row's
           uint32_t xa = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclALo + 16 * arow + b);
-          uint32_t xb = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclBLo + 16 * brow0 + b);
+          uint32_t xb = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclBLo + 16 * brow0 + bb);
           asm volatile("" : "+v"(xa), "+v"(xb));
 #pragma unroll
           for (int i = 0; i < kMT; ++i) sax[i] = lds_u8(xa + (uint32_t)(16 * 16 * i));
@@ -498,7 +601,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
 #pragma unroll
           for (int i = 0; i < kMT; ++i) sax[i] = mx_byte(mx_at(sc, kSclALo, kSclAHi, wm * kWM + i * 16 + lr, b));
 #pragma unroll
-          for (int j = 0; j < kNT; ++j) sbx[j] = mx_byte(mx_at(sc, kSclBLo, kSclBHi, wn * kWN + brow(j), b));
+          for (int j = 0; j < kNT; ++j) sbx[j] = mx_byte(mx_at(sc, kSclBLo, kSclBHi, wn * kWN + brow(j), bb));
         }
       }
 #pragma unroll
@@ -511,8 +614,8 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
       // MX: blocks past K (last step only) take byte 0, 2^-127, times their
       // zero codes, whatever E8M0 bytes follow a row's last
       if constexpr (S::kMx) {
-        if (p.nkb - 4 * kt < 4) {
-          const bool in_k = lg < p.nkb - 4 * kt;
+        if (nblk - 4 * kt < 4) {
+          const bool in_k = lg < nblk - 4 * kt;
 #pragma unroll
           for (int i = 0; i < kMT; ++i) sax[i] = in_k ? sax[i] : 0;
 #pragma unroll
@@ -587,7 +690,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
 #pragma unroll
       for (int i = 0; i < kMT; ++i) {
         const int row = m0 + wm * kWM + i * 16 + lr;
-        csa[i] = (KT > 0 && row < p.M) ? sap[row] : 0.0f;
+        csa[i] = (KT > 0 && row < m_end) ? sap[row] : 0.0f;
       }
     }
     wait_vmcnt<0>();
@@ -627,11 +730,13 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
       if (KT > 0) alpha = *reinterpret_cast<const float*>(p.sa) * *reinterpret_cast<const float*>(p.sb);
     }
     constexpr int ESIZE = OUT == kOutBf16 ? 2 : 4;
-    const bool vec_ok = ((p.ldc * ESIZE) % 16 == 0) && ((reinterpret_cast<uintptr_t>(p.c) & 15) == 0);
+    void* c_ex = p.c;
+    if constexpr (GRP == kGrpContract) c_ex = static_cast<uint8_t*>(p.c) + ex * p.stride_c * ESIZE;
+    const bool vec_ok = ((p.ldc * ESIZE) % 16 == 0) && ((reinterpret_cast<uintptr_t>(c_ex) & 15) == 0);
 #pragma unroll
     for (int i = 0; i < kMT; ++i) {
       const int row = m0 + wm * kWM + i * 16 + lr;
-      if (row >= p.M) continue;
+      if (row >= m_end) continue;
       float v[kCPL];
       if constexpr (REC == kGemmChannel) {
 #pragma unroll
@@ -645,7 +750,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
           for (int r = 0; r < 4; ++r) v[4 * j + r] = (REC == kGemmTensor) ? acc[i][j][r] * alpha : acc[i][j][r];
       }
       if constexpr (OUT == kOutBf16) {
-        __bf16* dst = reinterpret_cast<__bf16*>(p.c) + (int64_t)row * p.ldc + cbase;
+        __bf16* dst = reinterpret_cast<__bf16*>(c_ex) + (int64_t)row * p.ldc + cbase;
         if (vec_ok && cbase + kCPL <= p.N) {
 #pragma unroll
           for (int qq = 0; qq < kCPL / 8; ++qq) {
@@ -663,7 +768,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(GArgs p) {
             if (cbase + c < p.N) dst[c] = (__bf16)v[c];
         }
       } else {
-        float* dst = reinterpret_cast<float*>(p.c) + (int64_t)row * p.ldc + cbase;
+        float* dst = reinterpret_cast<float*>(c_ex) + (int64_t)row * p.ldc + cbase;
         if (vec_ok && cbase + kCPL <= p.N) {
 #pragma unroll
           for (int qq = 0; qq < kCPL / 4; ++qq)
@@ -700,7 +805,7 @@ hipError_t launch4(const GemmParams& g, hipStream_t st) {
   const unsigned tiles = (unsigned)a.tiles_m * (unsigned)a.tiles_n;
   const unsigned cus = (unsigned)cu_count(stream_device(st));
   const unsigned blocks = tiles < cus ? tiles : cus;
-  gemm_kernel<FA, FB, REC, OUT><<<blocks, 512, 0, st>>>(a);
+  gemm_kernel<FA, FB, REC, OUT, kGrpNone><<<blocks, 512, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -726,7 +831,66 @@ hipError_t launch_fmt(const GemmParams& g, hipStream_t st) {
   return hipErrorInvalidValue;
 }
 
+// Grouped: which tiles there are is on the device, so the grid is the most
+// workgroups that can have one (at most one per compute unit).
+template <int FA, int FB, int REC, int OUT, int GRP>
+hipError_t launch_grouped4(const GroupedGemmParams& g, hipStream_t st) {
+  GroupArgs a;
+  a.a = g.a;
+  a.b = g.b;
+  a.sa = g.s_a;
+  a.sb = g.s_b;
+  a.lda = g.lda;
+  a.ldb = g.ldb;
+  a.ldc = g.ldc;
+  a.offsets = g.offsets;
+  a.experts = (int)g.experts;
+  a.R = (int)g.R;
+  a.M = (int)g.M;
+  a.N = (int)g.N;
+  a.K = (int)g.K;
+  constexpr int kPer = REC == kGemmMx ? 32 : 128;
+  a.nkb = (int)(((GRP == kGrpContract ? g.R : g.K) + kPer - 1) / kPer);
+  a.nkb_b = (int)g.ld_sb;
+  a.stride_b = g.stride_b;
+  a.stride_sb = g.stride_sb;
+  a.stride_c = g.stride_c;
+  a.c = g.c;
+  a.tiles_m = (int)((g.M + kBM - 1) / kBM);
+  a.tiles_n = (int)((g.N + kBN - 1) / kBN);
+  const int64_t tiles =
+      GRP == kGrpRows ? (g.R / kBM + g.experts) * a.tiles_n : (int64_t)a.tiles_m * a.tiles_n * g.experts;
+  const int64_t cus = cu_count(stream_device(st));
+  // (a multiple of 8: tiles t and t + grid stay on one XCD)
+  const unsigned blocks = (unsigned)((tiles < cus ? tiles : cus) + 7) / 8 * 8;
+  gemm_kernel<FA, FB, REC, OUT, GRP><<<blocks, 512, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int FA, int FB>
+hipError_t launch_grouped_fmt(const GroupedGemmParams& g, hipStream_t st) {
+  const bool bf = g.c_dtype == kOutBf16;
+  if (g.contract) {
+    if (g.recipe == kGemmMx)
+      return bf ? launch_grouped4<FA, FB, kGemmMx, kOutBf16, kGrpContract>(g, st)
+                : launch_grouped4<FA, FB, kGemmMx, kOutFp32, kGrpContract>(g, st);
+    return bf ? launch_grouped4<FA, FB, kGemmBlock1x128, kOutBf16, kGrpContract>(g, st)
+              : launch_grouped4<FA, FB, kGemmBlock1x128, kOutFp32, kGrpContract>(g, st);
+  }
+  if (g.recipe == kGemmMx)
+    return bf ? launch_grouped4<FA, FB, kGemmMx, kOutBf16, kGrpRows>(g, st)
+              : launch_grouped4<FA, FB, kGemmMx, kOutFp32, kGrpRows>(g, st);
+  return bf ? launch_grouped4<FA, FB, kGemmBlock128x128, kOutBf16, kGrpRows>(g, st)
+            : launch_grouped4<FA, FB, kGemmBlock128x128, kOutFp32, kGrpRows>(g, st);
+}
+
 }  // namespace
+
+hipError_t launch_gemm_grouped(const GroupedGemmParams& g, hipStream_t st) {
+  if (g.fmt_a == kE4M3)
+    return g.fmt_b == kE4M3 ? launch_grouped_fmt<kE4M3, kE4M3>(g, st) : launch_grouped_fmt<kE4M3, kE5M2>(g, st);
+  return g.fmt_b == kE4M3 ? launch_grouped_fmt<kE5M2, kE4M3>(g, st) : launch_grouped_fmt<kE5M2, kE5M2>(g, st);
+}
 
 hipError_t launch_gemm_bf16(const GemmParams& g, hipStream_t st) {
   // BF16 operands through the byte-addressed kernel: K and the leading

@@ -45,6 +45,10 @@ constexpr int kGemmTensor = 0, kGemmBlock128x128 = 1, kGemmBlock1x128 = 2, kGemm
 constexpr int kGemmBf16 = 16;
 // slots of a delayed-scaling amax accumulator (FP8MI_AMAX_SLOTS)
 constexpr int kAmaxSlots = 1024;
+// experts a sort, a dispatch or a grouped GEMM takes (FP8MI_MAX_EXPERTS), and
+// the multiple of rows their segments start on (FP8MI_EXPERT_ALIGN)
+constexpr int kMaxExperts = 1024;
+constexpr int kExpertAlign = 128;
 
 struct QuantParams {
   const void* x;
@@ -82,6 +86,77 @@ struct GemmParams {
   int64_t ldc;
 };
 
+// fp8_gemm_grouped (contract: one product per expert over its own rows;
+// else each expert's rows times its own B)
+struct GroupedGemmParams {
+  bool contract;
+  const uint8_t* a;
+  int fmt_a;
+  const void* s_a;
+  int64_t lda;
+  const uint8_t* b;
+  int fmt_b;
+  const void* s_b;
+  int64_t ldb, stride_b, ld_sb, stride_sb;
+  int recipe;
+  const int32_t* offsets;
+  int64_t experts, R, M, N, K;
+  void* c;
+  int c_dtype;
+  int64_t ldc, stride_c;
+};
+
+// fp8_moe_quantize: q.rows is the sorted buffer's row capacity
+struct MoeQuantParams {
+  QuantParams q;
+  const int32_t* offsets;
+  const int32_t* row_slot;
+  const float* weights;
+  int64_t experts, topk, x_rows;
+};
+
+struct MoeSortParams {
+  const void* expert;
+  int idx_dtype;
+  int64_t tokens, topk, ld_expert, experts;
+  int32_t *offsets, *counts, *row_slot, *slot_row;
+  int64_t rows;
+  int32_t* workspace;
+};
+
+// dispatch, combine and combine's backward pass
+struct MoeRowsParams {
+  int dtype;
+  int64_t tokens, topk, experts, cols, rows;
+  const int32_t *offsets, *counts, *row_slot, *slot_row;
+  const float* weights;
+  const void* token_rows;  // x / dy
+  int64_t ld_token;
+  const void* expert_rows;  // ys
+  int64_t ld_expert;
+  void* out;                // dispatch: sorted rows; combine: token rows; backward: sorted rows
+  int64_t ld_out;
+  float* dweights;
+};
+
+struct NormParams {
+  const void* x;
+  const void* dy;
+  int x_dtype, w_dtype;
+  int64_t rows, cols, ld_x, ld_dy, ld_out;
+  const void* weight;
+  const void* bias;
+  float eps;
+  float *mean, *rstd;
+  void* out;  // y / dx
+  void *dweight, *dbias;
+  float* workspace;
+  int64_t workspace_floats;
+};
+
+// FP8MI_OK, or FP8MI_ERR_HIP with the error's text kept for fp8_status_string
+int hip_status(hipError_t e);
+
 hipError_t launch_quantize(const QuantParams& p, hipStream_t st);
 // fp8_quantize with current scaling's partial maxima in the library's static
 // device scratch instead of amax[1 ..] (see quantize.hip)
@@ -92,5 +167,15 @@ hipError_t launch_history(float* history, int32_t* head, int len, float* amax, i
 hipError_t launch_gemm(const GemmParams& p, hipStream_t st);
 // a, b BF16 [M x K], [N x K]; K, lda, ldb in elements
 hipError_t launch_gemm_bf16(const GemmParams& p, hipStream_t st);
+hipError_t launch_gemm_grouped(const GroupedGemmParams& p, hipStream_t st);
+hipError_t launch_moe_quantize(const MoeQuantParams& p, hipStream_t st);
+hipError_t launch_moe_sort(const MoeSortParams& p, hipStream_t st);
+int64_t moe_sort_blocks(int64_t slots);
+hipError_t launch_moe_dispatch(const MoeRowsParams& p, hipStream_t st);
+hipError_t launch_moe_combine(const MoeRowsParams& p, hipStream_t st);
+hipError_t launch_moe_combine_backward(const MoeRowsParams& p, hipStream_t st);
+hipError_t launch_norm_forward(const NormParams& p, hipStream_t st);
+hipError_t launch_norm_backward(const NormParams& p, hipStream_t st);
+int64_t norm_partials(int64_t rows);
 
 }  // namespace fp8mi

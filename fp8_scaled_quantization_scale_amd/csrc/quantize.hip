@@ -30,6 +30,7 @@
 // costs as much as the whole cast.
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "device.hpp"
 #include "launch.hpp"
@@ -167,6 +168,18 @@ struct TileArgs {
   const uint32_t* parts;
 };
 
+// Rows sorted by expert (fp8_moe_quantize): row r of the tiles is row
+// row_slot[r] / topk of x, times weights[row_slot[r]], or zero where the slot
+// is negative; without row_slot, row r of x itself.  The rows end where the
+// last expert's segment does, which the device array of offsets says.
+struct MoeTileArgs : TileArgs {
+  const int32_t* offsets;   // [experts + 1], multiples of 128
+  const int32_t* row_slot;  // [rows] or nullptr
+  const float* weights;     // [x rows * topk] or nullptr (1)
+  int experts, topk;
+  int64_t x_rows;
+};
+
 // max |x| key of 8 BF16 values packed in a uint4: packed 16-bit max of the
 // sign-cleared halves (non-negative BF16 orders like its bits, NaN on top).
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -189,6 +202,21 @@ struct Raw<uint16_t> {
   uint4 w[8];
   __device__ __forceinline__ void row(int i, float v[8]) const { unpack_bf16x8(w[i], v); }
   __device__ __forceinline__ uint32_t key(int i, const float*) const { return bf16x8_key(w[i]); }
+  // row i from row rows[g + 16 i].x of x, zeros where that is negative
+  __device__ __forceinline__ void gather(const uint16_t* x, int64_t ld, const int2* rows, int g, int64_t ccol, int64_t nval) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t src = rows[g + 16 * i].x;
+      if (src >= 0 && nval >= 8) {
+        w[i] = ld16(x + src * ld + ccol);
+      } else {
+        uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (src >= 0)
+          for (int e = 0; e < 8 && e < nval; ++e) h[e] = x[src * ld + ccol + e];
+        w[i] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+      }
+    }
+  }
   __device__ __forceinline__ void load(const uint16_t* x, int64_t ld, int64_t rows, int64_t r0, int64_t ccol,
                                        int64_t nval) {
 #pragma unroll
@@ -212,6 +240,25 @@ struct Raw<float> {
   __device__ __forceinline__ void row(int i, float v[8]) const {
     v[0] = w[2 * i].x; v[1] = w[2 * i].y; v[2] = w[2 * i].z; v[3] = w[2 * i].w;
     v[4] = w[2 * i + 1].x; v[5] = w[2 * i + 1].y; v[6] = w[2 * i + 1].z; v[7] = w[2 * i + 1].w;
+  }
+  __device__ __forceinline__ void gather(const float* x, int64_t ld, const int2* rows, int g, int64_t ccol, int64_t nval) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t src = rows[g + 16 * i].x;
+      if (src >= 0 && nval >= 8) {
+        const uint4 lo = ld16(x + src * ld + ccol), hi = ld16(x + src * ld + ccol + 4);
+        w[2 * i] = make_float4(__builtin_bit_cast(float, lo.x), __builtin_bit_cast(float, lo.y),
+                               __builtin_bit_cast(float, lo.z), __builtin_bit_cast(float, lo.w));
+        w[2 * i + 1] = make_float4(__builtin_bit_cast(float, hi.x), __builtin_bit_cast(float, hi.y),
+                                   __builtin_bit_cast(float, hi.z), __builtin_bit_cast(float, hi.w));
+      } else {
+        float h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (src >= 0)
+          for (int e = 0; e < 8 && e < nval; ++e) h[e] = x[src * ld + ccol + e];
+        w[2 * i] = make_float4(h[0], h[1], h[2], h[3]);
+        w[2 * i + 1] = make_float4(h[4], h[5], h[6], h[7]);
+      }
+    }
   }
   __device__ __forceinline__ void load(const float* x, int64_t ld, int64_t rows, int64_t r0, int64_t ccol,
                                        int64_t nval) {
@@ -248,26 +295,68 @@ __device__ __forceinline__ bool fits(uint32_t key, float s) {
 // ... and prefetches the next tile's raw words into registers while the
 // current one is processed, so every workgroup always has a tile in flight.
 // CURRENT: per-tensor scale from the finished amax; otherwise the recipe's own.
-template <typename InT, int FMT, int MODE, bool ROW, bool COL, bool CURRENT>
-__global__ __launch_bounds__(kThreads) void quant_tile_kernel(TileArgs a) {
+// MOE: rows sorted by expert, gathered and weighted as they are read (block
+// recipes only; a row's numbers are read one tile ahead of its elements).
+template <typename InT, int FMT, int MODE, bool ROW, bool COL, bool CURRENT, bool MOE = false>
+__global__ __launch_bounds__(kThreads) void quant_tile_kernel(std::conditional_t<MOE, MoeTileArgs, TileArgs> a) {
   constexpr int kLdsElems = COL ? kTile * kTile : 1;
   __shared__ InT tile[kLdsElems];
   __shared__ uint32_t red4[4];
   __shared__ uint32_t colred[4][kTile];
+  // MOE: each tile row's source row and weight (as bits): of the tile in hand,
+  // of the one whose words are on their way and of the one after it
+  __shared__ int2 rowinfo[MOE ? 3 : 1][kTile];
 
   const int tid = threadIdx.x;
   const int g = tid >> 4;   // row group 0..15
   const int li = tid & 15;  // lane in group
   const InT* x = reinterpret_cast<const InT*>(a.x);
   const int64_t tiles_x = (a.cols + kTile - 1) / kTile;
-  const int64_t tiles = tiles_x * ((a.rows + kTile - 1) / kTile);
+  int64_t tiles = tiles_x * ((a.rows + kTile - 1) / kTile);
+  if constexpr (MOE) {
+    const int64_t end = a.offsets[a.experts];
+    tiles = tiles_x * ((end < 0 ? 0 : (end < a.rows ? end : a.rows)) / kTile);
+  }
+  auto source = [&](int64_t tile_no) __attribute__((always_inline)) -> int2 {
+    int2 info = make_int2(-1, 0x3F800000);  // a row of zeros, weight 1
+    if constexpr (MOE) {
+      if (tid < kTile && tile_no < tiles) {
+        const int64_t r = (tile_no / tiles_x) * kTile + tid;
+        if (!a.row_slot) {
+          info.x = (int)r;
+        } else {
+          const int slot = a.row_slot[r];
+          const int64_t from = slot < 0 ? -1 : (int64_t)((uint32_t)slot / (uint32_t)a.topk);
+          if (from >= 0 && from < a.x_rows) {
+            info.x = (int)from;
+            if (a.weights) info.y = __builtin_bit_cast(int, a.weights[slot]);
+          }
+        }
+      }
+    }
+    return info;
+  };
+  int ring = 0;  // MOE: rowinfo of the tile in hand
+  auto weight = [&](int row) __attribute__((always_inline)) -> float {
+    return __builtin_bit_cast(float, rowinfo[ring][row].y);
+  };
 
   // the first tile's words are in flight while the scale is worked out
   Raw<InT> cur, nxt;
   int64_t t = blockIdx.x;
   if (t < tiles) {
     const int64_t by = t / tiles_x, bx = t - by * tiles_x;
-    cur.load(x, a.ld_x, a.rows, by * kTile + g, bx * kTile + 8 * li, a.cols - (bx * kTile + 8 * li));
+    if constexpr (MOE) {
+      const int2 first = source(t), second = source(t + gridDim.x);
+      if (tid < kTile) {
+        rowinfo[0][tid] = first;
+        rowinfo[1][tid] = second;
+      }
+      __syncthreads();
+      cur.gather(x, a.ld_x, rowinfo[0], g, bx * kTile + 8 * li, a.cols - (bx * kTile + 8 * li));
+    } else {
+      cur.load(x, a.ld_x, a.rows, by * kTile + g, bx * kTile + 8 * li, a.cols - (bx * kTile + 8 * li));
+    }
   }
 
   // ---- per-tensor scale (the same for every tile)
@@ -304,9 +393,16 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(TileArgs a) {
   for (; t < tiles; t += gridDim.x) {
     const int64_t by = t / tiles_x, bx = t - by * tiles_x;
     const int64_t tn = t + gridDim.x;
+    int2 after = make_int2(-1, 0);
+    if constexpr (MOE) after = source(tn + gridDim.x);
     if (tn < tiles) {
       const int64_t byn = tn / tiles_x, bxn = tn - byn * tiles_x;
-      nxt.load(x, a.ld_x, a.rows, byn * kTile + g, bxn * kTile + 8 * li, a.cols - (bxn * kTile + 8 * li));
+      if constexpr (MOE) {
+        nxt.gather(x, a.ld_x, rowinfo[ring == 2 ? 0 : ring + 1], g, bxn * kTile + 8 * li,
+                   a.cols - (bxn * kTile + 8 * li));
+      } else {
+        nxt.load(x, a.ld_x, a.rows, byn * kTile + g, bxn * kTile + 8 * li, a.cols - (bxn * kTile + 8 * li));
+      }
     }
     const int64_t row0 = by * kTile, col0 = bx * kTile;
     const int64_t ccol = col0 + 8 * li;  // first column of this lane's chunk
@@ -350,7 +446,10 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(TileArgs a) {
         for (int i = 0; i < 8; ++i) {
           float v[8];
           cur.row(i, v);
-          kk[i] = group_max_u32<16>(cur.key(i, v));
+          uint32_t key = cur.key(i, v);
+          // (rounding is monotonic: the largest |x w| is the largest |x| times |w|)
+          if constexpr (MOE) key = abs_key(key_to_float(key) * weight(g + 16 * i));
+          kk[i] = group_max_u32<16>(key);
           bad_rows[i] = !is_finite(key_to_float(kk[i]));
         }
         uint32_t kj = kk[0];
@@ -372,13 +471,19 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(TileArgs a) {
         const int64_t r = row0 + g + 16 * i;
         float v[8];
         cur.row(i, v);
+        if constexpr (MOE) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= weight(g + 16 * i);
+        }
         float s = s_t;
         bool safe = safe_t;
         if constexpr (MODE == MODE_B1x128) {
           s = s_rows[i];
           safe = bad_rows[i];
         } else if constexpr (MODE == MODE_MX32 || MODE == MODE_MX32F) {
-          const uint32_t k = group_max_u32<4>(cur.key(i, v));
+          uint32_t key = cur.key(i, v);
+          if constexpr (MOE && sizeof(InT) == 2) key = abs_key(key_to_float(key) * weight(g + 16 * i));  // (FP32: of the products)
+          const uint32_t k = group_max_u32<4>(key);
           const int byte = mx_byte<MODE, FMT>(key_to_float(k));
           // the floor rule lets elements exceed max: saturating encoder
           safe = byte == 0xFF || MODE == MODE_MX32F;
@@ -439,6 +544,10 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(TileArgs a) {
           const float2 pr = reinterpret_cast<const float2*>(tile)[rl * (kTile / 2) + cp];
           w0[j] = pr.x;
           w1[j] = pr.y;
+        }
+        if constexpr (MOE) {
+          w0[j] *= weight(rl);
+          w1[j] *= weight(rl);
         }
         const uint32_t a0 = abs_key(w0[j]), a1 = abs_key(w1[j]);
         k0 = k0 > a0 ? k0 : a0;
@@ -551,6 +660,13 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(TileArgs a) {
       }
     }
     cur = nxt;
+    if constexpr (MOE) {
+      // the slot written is the one no wave reads before the barrier: it held
+      // the tile before the one in hand
+      ring = ring == 2 ? 0 : ring + 1;
+      if (tid < kTile) rowinfo[ring == 2 ? 0 : ring + 1][tid] = after;
+      __syncthreads();
+    }
   }
 
   if constexpr (MODE == MODE_TENSOR && !CURRENT) {
@@ -780,6 +896,44 @@ hipError_t launch_tile(const QuantParams& p, hipStream_t st, int nparts = 0, con
   return launch_tile_k<InT, FMT, MODE, false, true, CURRENT>(a, tiles, st);
 }
 
+template <typename InT, int FMT, int MODE, bool ROW, bool COL>
+hipError_t launch_moe_k(const MoeTileArgs& a, int64_t tiles, hipStream_t st) {
+  static std::atomic<int> occupancy{0};
+  auto k = quant_tile_kernel<InT, FMT, MODE, ROW, COL, false, true>;
+  k<<<persistent_grid(k, tiles, occupancy, st), kThreads, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <typename InT, int FMT, int MODE>
+hipError_t launch_moe(const MoeQuantParams& m, hipStream_t st) {
+  const QuantParams& p = m.q;
+  MoeTileArgs a;
+  static_cast<TileArgs&>(a) = TileArgs{p.x, p.rows, p.cols, p.ld_x, p.q_row, p.ld_q_row, p.s_row, p.q_col, p.ld_q_col,
+                                       p.s_col, nullptr, nullptr, nullptr, p.nonfinite, p.margin, 0, nullptr};
+  a.offsets = m.offsets;
+  a.row_slot = m.row_slot;
+  a.weights = m.weights;
+  a.experts = (int)m.experts;
+  a.topk = (int)m.topk;
+  a.x_rows = m.x_rows;
+  // at most this many: the rows that hold an expert's segment are fewer
+  const int64_t tiles = ((p.cols + kTile - 1) / kTile) * (p.rows / kTile);
+  const bool row = p.orient & 1, col = p.orient & 2;
+  if (row && col) return launch_moe_k<InT, FMT, MODE, true, true>(a, tiles, st);
+  if (row) return launch_moe_k<InT, FMT, MODE, true, false>(a, tiles, st);
+  return launch_moe_k<InT, FMT, MODE, false, true>(a, tiles, st);
+}
+
+template <typename InT, int FMT>
+hipError_t launch_moe_fmt(const MoeQuantParams& m, hipStream_t st) {
+  switch (m.q.recipe) {
+    case kRecipeBlock1x128: return launch_moe<InT, FMT, MODE_B1x128>(m, st);
+    case kRecipeMx1x32: return launch_moe<InT, FMT, MODE_MX32>(m, st);
+    case kRecipeMx1x32Ocp: return launch_moe<InT, FMT, MODE_MX32F>(m, st);
+  }
+  return hipErrorInvalidValue;
+}
+
 template <typename InT, int FMT>
 hipError_t launch_fmt(const QuantParams& p, hipStream_t st) {
   switch (p.recipe) {
@@ -909,6 +1063,12 @@ hipError_t launch_quantize(const QuantParams& p, hipStream_t st) {
     return p.fmt == kE4M3 ? launch_fmt<uint16_t, kE4M3>(p, st) : launch_fmt<uint16_t, kE5M2>(p, st);
   }
   return p.fmt == kE4M3 ? launch_fmt<float, kE4M3>(p, st) : launch_fmt<float, kE5M2>(p, st);
+}
+
+hipError_t launch_moe_quantize(const MoeQuantParams& m, hipStream_t st) {
+  if (m.q.x_dtype == kInBf16)
+    return m.q.fmt == kE4M3 ? launch_moe_fmt<uint16_t, kE4M3>(m, st) : launch_moe_fmt<uint16_t, kE5M2>(m, st);
+  return m.q.fmt == kE4M3 ? launch_moe_fmt<float, kE4M3>(m, st) : launch_moe_fmt<float, kE5M2>(m, st);
 }
 
 hipError_t launch_quantize_static_scratch(const QuantParams& p, hipStream_t st) {

@@ -273,6 +273,143 @@ int fp8_bf16_gemm(const void* a, int64_t lda, const void* b, int64_t ldb,
                   int64_t M, int64_t N, int64_t K,
                   void* c, int c_dtype, int64_t ldc, void* stream);
 
+/* ---- layer norm -------------------------------------------------------------
+ * The layer that stands before an FP8 linear layer.  Statistics and sums are
+ * FP32; each output is rounded once.  Matrices are row-major, leading
+ * dimensions in elements, pointers aligned to their element.  None of the
+ * outputs may overlap an input. */
+
+/* fp8_layer_norm_forward -- over the columns of x [rows x cols]:
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ *   x, y : BF16 or FP32 (x_dtype); weight, bias: [cols] of w_dtype (BF16 or
+ *   FP32), NULL for 1 and 0; mean, rstd: float [rows], which the backward pass
+ *   takes; eps >= 0.  cols >= 1 (at most 2^28); rows == 0 does nothing. */
+int fp8_layer_norm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                           const void* weight, const void* bias, int w_dtype, float eps,
+                           void* y, int64_t ld_y, float* mean, float* rstd, void* stream);
+
+/* fp8_layer_norm_workspace -- bytes of device memory that the gradient of
+ * weight and bias needs (each workgroup's column sums); negative: an error. */
+int64_t fp8_layer_norm_workspace(int64_t rows, int64_t cols);
+
+/* fp8_layer_norm_backward -- with h = (x - mean) rstd, g = dy * weight:
+ *   dx = rstd * (g - sum(g) / cols - h * sum(g h) / cols),
+ *   dweight = sum over rows of dy h, dbias = sum over rows of dy.
+ *   dweight, dbias ([cols] of w_dtype) may each be NULL; with either, workspace
+ *   holds fp8_layer_norm_workspace(rows, cols) bytes, which calls that overlap
+ *   in time may not share.  The sums are added in a fixed order: equal calls
+ *   give equal bits.  rows == 0 writes zero gradients. */
+int fp8_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int x_dtype, int64_t rows, int64_t cols,
+                            int64_t ld_x, const void* weight, int w_dtype, const float* mean, const float* rstd,
+                            void* dx, int64_t ld_dx, void* dweight, void* dbias,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- experts ----------------------------------------------------------------
+ * A router gives token t the experts expert[t][0 .. topk).  Slot s = t * topk +
+ * j is one of these choices; a slot whose expert lies outside [0, experts) is
+ * dropped.  The other slots are sorted by expert, in order within one, into a
+ * buffer of `rows` rows: expert e's segment is [offsets[e], offsets[e + 1]),
+ * starts on a multiple of FP8MI_EXPERT_ALIGN, holds counts[e] slots and then
+ * rows of zeros; the rows behind offsets[experts] belong to nobody, and nothing
+ * here reads or writes them.  The sizes stay on the device: no call waits for
+ * them, and `rows` is the most that any routing needs (fp8_moe_rows). */
+#define FP8MI_EXPERT_ALIGN 128
+#define FP8MI_MAX_EXPERTS 1024
+#define FP8MI_IDX_I32 0
+#define FP8MI_IDX_I64 1
+
+/* Rows of the sorted buffer: the most that tokens * topk slots over `experts`
+ * experts can fill, a multiple of FP8MI_EXPERT_ALIGN; negative: an error. */
+int64_t fp8_moe_rows(int64_t tokens, int64_t topk, int64_t experts);
+
+/* Bytes of device memory that fp8_moe_sort needs (0 for few slots); negative:
+ * an error. */
+int64_t fp8_moe_sort_workspace(int64_t tokens, int64_t topk, int64_t experts);
+
+/* fp8_moe_sort -- segments and row maps of a routing.
+ *   expert   : [tokens x topk] int32 or int64 (idx_dtype), ld_expert >= topk.
+ *   offsets  : int32 [experts + 1]; counts: int32 [experts].
+ *   row_slot : int32 [rows], the slot in each row, -1 in rows without one
+ *              (those behind the last segment too); rows >= fp8_moe_rows.
+ *   slot_row : int32 [tokens x topk], each slot's row, -1 for a dropped one.
+ *   workspace: fp8_moe_sort_workspace bytes; calls that overlap in time may
+ *              not share it.
+ * experts <= FP8MI_MAX_EXPERTS and tokens * topk <= 2^30, else
+ * FP8MI_ERR_UNSUPPORTED (of every entry point below too). */
+int fp8_moe_sort(const void* expert, int idx_dtype, int64_t tokens, int64_t topk, int64_t ld_expert,
+                 int64_t experts, int32_t* offsets, int32_t* counts, int32_t* row_slot, int64_t rows,
+                 int32_t* slot_row, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* fp8_moe_dispatch -- y[slot_row[t][j]] = weights[t][j] * x[t] (weights NULL:
+ * 1), zeros in a segment's rows without a slot.  x [tokens x cols] and y
+ * [rows x cols] BF16 or FP32; weights float [tokens x topk]. */
+int fp8_moe_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, int64_t ld_x, int64_t topk,
+                     const float* weights, const int32_t* slot_row, const int32_t* offsets, const int32_t* counts,
+                     int64_t experts, void* y, int64_t rows, int64_t ld_y, void* stream);
+
+/* fp8_moe_quantize -- fp8_quantize of the sorted rows, read straight from
+ * where they are: row r is x[row_slot[r] / topk] * weights[row_slot[r]] (one
+ * FP32 product; weights NULL: 1), zeros where row_slot[r] < 0.  With row_slot
+ * NULL it is x[r] itself (x_rows >= rows, no weights), rows without a slot
+ * included.  recipe: BLOCK_1x128, MX_1x32 or MX_1x32_OCP (per-tensor and
+ * channel scales would span experts: FP8MI_ERR_UNSUPPORTED).  Outputs, scale
+ * layouts, alignment and nonfinite as for fp8_quantize on a [rows x cols]
+ * matrix; since segments start on multiples of 128, no block of the COL
+ * outputs holds two experts' rows. */
+int fp8_moe_quantize(const void* x, int x_dtype, int64_t x_rows, int64_t cols, int64_t ld_x,
+                     const int32_t* row_slot, int64_t topk, const float* weights, const int32_t* offsets,
+                     int64_t experts, int64_t rows, int recipe, int fmt, int orient, int margin,
+                     uint8_t* q_row, int64_t ld_q_row, void* s_row, uint8_t* q_col, int64_t ld_q_col, void* s_col,
+                     int32_t* nonfinite, void* stream);
+
+/* fp8_moe_combine -- y[t] = sum over j of weights[t][j] * ys[slot_row[t][j]]
+ * (weights NULL: 1), summed in FP32; a dropped slot adds nothing.  It is the
+ * gradient of fp8_moe_dispatch, and the way back from the experts. */
+int fp8_moe_combine(const void* ys, int dtype, int64_t rows, int64_t cols, int64_t ld_ys, const int32_t* slot_row,
+                    int64_t tokens, int64_t topk, const float* weights, void* y, int64_t ld_y, void* stream);
+
+/* fp8_moe_combine_backward -- the gradient of fp8_moe_combine:
+ *   dys[slot_row[t][j]] = weights[t][j] * dy[t], zeros in a segment's rows
+ *   without a slot (dys NULL: left out);
+ *   dweights[t][j] = <dy[t], ys[slot_row[t][j]]>, 0 for a dropped slot, float
+ *   (dweights NULL: left out, and ys is not read). */
+int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t cols, int64_t ld_dy,
+                             const void* ys, int64_t ld_ys, const int32_t* slot_row, const int32_t* offsets,
+                             const int32_t* counts, int64_t experts, int64_t topk, const float* weights,
+                             void* dys, int64_t rows, int64_t ld_dys, float* dweights, void* stream);
+
+/* which index of the products the experts share out (fp8_gemm_grouped) */
+#define FP8MI_GROUP_ROWS 0
+#define FP8MI_GROUP_CONTRACT 1
+
+/* fp8_gemm_grouped -- the experts' products: fp8_gemm_scaled with one B, or
+ * one contraction range, per expert.
+ *   GROUP_ROWS     (fprop, dgrad): for the rows r of segment e,
+ *       C[r] = dequant(A[r]) . dequant(B_e)^T.
+ *       a [rows x K], s_a as fp8_gemm_scaled's with M = rows; B_e = b + e *
+ *       stride_b, [N x K] with ldb; its scales s_b + e * stride_sb entries,
+ *       rows (of 128x128 tiles: tile rows) ld_sb entries apart; c [rows x N].
+ *       recipe GEMM_BLOCK_1x128_128x128 or GEMM_MX_1x32.  M is not used.  Rows
+ *       without a slot are computed like the others; those behind the last
+ *       segment are left as they were.
+ *   GROUP_CONTRACT (wgrad): for every expert, C_e = dequant(A[:, segment e]) .
+ *       dequant(B[:, segment e])^T, zeros for an empty segment.
+ *       a [M x rows], b [N x rows] (the COL outputs of fp8_moe_quantize), s_a
+ *       and s_b their dense grids; C_e = c + e * stride_c, [M x N] with ldc.
+ *       recipe GEMM_BLOCK_1x128_1x128 or GEMM_MX_1x32.  K, stride_b, ld_sb and
+ *       stride_sb are not used.
+ * offsets: int32 [experts + 1] as fp8_moe_sort gives it (read on the device;
+ * values outside [0, rows] are clamped to it, others rounded down to multiples
+ * of 128).  rows % 128 == 0, K % 16 == 0, stride_b % 16 == 0; other
+ * requirements, errors, tolerance and non-finite inputs as for
+ * fp8_gemm_scaled.  GROUP_CONTRACT needs rows <= 4194304. */
+int fp8_gemm_grouped(const uint8_t* a, int fmt_a, const void* s_a, int64_t lda,
+                     const uint8_t* b, int fmt_b, const void* s_b, int64_t ldb, int64_t stride_b,
+                     int64_t ld_sb, int64_t stride_sb, int recipe, int group, const int32_t* offsets,
+                     int64_t experts, int64_t rows, int64_t M, int64_t N, int64_t K,
+                     void* c, int c_dtype, int64_t ldc, int64_t stride_c, void* stream);
+
 /* Human-readable text of a status code; for FP8MI_ERR_HIP the text of the
  * last HIP error seen by this thread.  The string is owned by the library. */
 const char* fp8_status_string(int status);
