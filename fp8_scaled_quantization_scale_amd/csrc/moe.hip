@@ -292,31 +292,48 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
     float dot[kAtOnce];
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) dot[q] = 0.0f;
+    // the group's rows and weights, the same for the whole workgroup
+    int64_t row[kAtOnce];
+    float w[kAtOnce];
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q) {
+      const int64_t slot = t * a.topk + j0 + q;
+      row[q] = j0 + q < a.topk ? a.slot_row[slot] : -1;
+      if (row[q] >= a.rows) row[q] = -1;
+      w[q] = a.weights && j0 + q < a.topk ? a.weights[slot] : 1.0f;
+    }
     for (int64_t c = threadIdx.x * 8; c < a.cols; c += kRowThreads * 8) {
-      Chunk<T> k;
+      Chunk<T> k, y[kAtOnce];  // all on their way together
       float g[8];
       k.load(dy + c, a.cols - c);
-      k.get(g);
+      if (a.dweights) {
 #pragma unroll
-      for (int q = 0; q < kAtOnce; ++q) {
-        if (j0 + q >= a.topk) continue;
-        const int64_t slot = t * a.topk + j0 + q, row = a.slot_row[slot];
-        if (row < 0 || row >= a.rows) continue;
-        if (a.dweights) {
-          Chunk<T> y;
-          float v[8];
-          y.load(static_cast<const T*>(a.expert_rows) + row * a.ld_expert + c, a.cols - c);
-          y.get(v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot[q] += g[e] * v[e];
+        for (int q = 0; q < kAtOnce; ++q) {
+          y[q].fill(0.0f);
+          if (row[q] >= 0) y[q].load(static_cast<const T*>(a.expert_rows) + row[q] * a.ld_expert + c, a.cols - c);
         }
-        if (a.out) {
-          const float w = a.weights ? a.weights[slot] : 1.0f;
+      }
+      k.get(g);
+      if (a.out) {
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+          if (row[q] < 0) continue;
           float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = g[e] * w;
+          for (int e = 0; e < 8; ++e) v[e] = g[e] * w[q];
           k.set(v);
-          k.store(static_cast<T*>(a.out) + row * a.ld_out + c, a.cols - c);
+          k.store(static_cast<T*>(a.out) + row[q] * a.ld_out + c, a.cols - c);
+        }
+      }
+      if (a.dweights) {
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+          float v[8];
+          y[q].get(v);
+          if (row[q] >= 0) {  // (a non-finite dy times no row is nothing)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[q] += g[e] * v[e];
+          }
         }
       }
     }
