@@ -676,6 +676,292 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(std::conditional_t
 }
 
 // ---------------------------------------------------------------------------
+// BF16 rows sorted by expert (fp8_moe_quantize) whose columns are whole tiles:
+// the same casts on the same 128 x 128 tiles, gathered through the sort's row
+// map.
+//
+// With the gather and the weights on top, the tile kernel above has more
+// instructions per element than HBM leaves time for (16384 x 8192 to 4 of 64
+// experts, both orientations: 573 us; the bytes of each row read and of the
+// codes take 415, and 255 if each token came from HBM once).  This one is built
+// for few, and takes 446 us (weighted 461): a workgroup stays on its 128 rows
+// for `chunk` tiles, so that source rows, weights and addresses are worked out
+// once; maxima are taken on packed halves, across a row's 16 lanes with DPP,
+// and the column pass keeps its 64 elements packed until they are scaled.  The
+// tile in flight is not held in registers: three workgroups per CU cover its
+// latency better than two that prefetch (522 us against 573 in the kernel
+// above).  Units run along a row tile's columns, then down; column-major and
+// per-XCD ranges of row tiles were slower for both orientations together (459
+// and 449 us), though the column codes alone liked the former (274, now 294).
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t umax32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// max over the 16 lanes of a DPP row (rotations) / over 4 lanes (quad permutes)
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  v = umax32(v, dpp<0x128>(v));
+  v = umax32(v, dpp<0x124>(v));
+  v = umax32(v, dpp<0x122>(v));
+  return umax32(v, dpp<0x121>(v));
+}
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = umax32(v, dpp<0x4E>(v));         // lanes 2 3 0 1
+  return umax32(v, dpp<0xB1>(v));      // lanes 1 0 3 2
+}
+// lane N of every row of 16, to all of that row
+template <int N>
+__device__ __forceinline__ float row16_lane(float v) {
+  return __builtin_bit_cast(float, dpp<0x150 + N>(__builtin_bit_cast(uint32_t, v)));
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (N > 0) {
+    unrolled<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+template <int FMT, int MODE, bool ROW, bool COL, bool WGT>
+__global__ __launch_bounds__(kThreads, 3) void moe_tile_kernel(MoeTileArgs a, int chunk) {
+  constexpr bool kMx = MODE == MODE_MX32 || MODE == MODE_MX32F;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[COL ? kTile * kTile / 2 + kTile * 4 : 4];  // rows, then codes
+  __shared__ uint32_t colred[COL && !kMx ? 4 : 1][kTile / 2];
+  __shared__ int2 rowinfo[kTile];
+  const int tid = threadIdx.x, g = tid >> 4, li = tid & 15;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
+  const int tiles_x = (int)(a.cols / kTile), chunks = (tiles_x + chunk - 1) / chunk;
+  const int64_t end = a.offsets[a.experts];
+  const int row_tiles = a.x_rows == 0 ? 0 : (int)((end < 0 ? 0 : (end < a.rows ? end : a.rows)) / kTile);
+  const int64_t gr = a.rows / kTile;
+
+  for (int64_t u = blockIdx.x; u < (int64_t)row_tiles * chunks; u += gridDim.x) {
+    const int64_t by = u / chunks, row0 = by * kTile;
+    const int part = (int)(u - by * chunks);
+    __syncthreads();  // rowinfo and the tile of the unit before are done with
+    if (tid < kTile) {
+      int2 info = make_int2(-1, 0x3F800000);  // a row of zeros, weight 1
+      if (!a.row_slot) {
+        info.x = (int)(row0 + tid);
+      } else {
+        const int slot = a.row_slot[row0 + tid];
+        const int64_t from = slot < 0 ? -1 : (int64_t)((uint32_t)slot / (uint32_t)a.topk);
+        if (from >= 0 && from < a.x_rows) {
+          info.x = (int)from;
+          if constexpr (WGT) info.y = __builtin_bit_cast(int, a.weights[slot]);
+        }
+      }
+      rowinfo[tid] = info;
+    }
+    __syncthreads();
+    int src[8];
+    float wr[WGT ? 8 : 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int2 info = rowinfo[g + 16 * i];
+      src[i] = info.x;
+      if constexpr (WGT) wr[i] = __builtin_bit_cast(float, info.y);
+    }
+
+    bool pads = false;  // rows without a slot among this thread's
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pads = pads || src[i] < 0;
+    pads = __any(pads);
+
+    const int bx_end = min(tiles_x, (part + 1) * chunk);
+    for (int bx = part * chunk; bx < bx_end; ++bx) {
+      const int64_t col0 = (int64_t)bx * kTile;
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = ld16(x + (int64_t)max(src[i], 0) * a.ld_x + col0 + 8 * li);
+      if (pads) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (src[i] < 0) w[i] = make_uint4(0, 0, 0, 0);
+      }
+
+      // ---- COL: the raw rows go to LDS first, so that the other waves' wait
+      // for them overlaps the ROW work
+      if constexpr (COL) {
+        if (bx > part * chunk) __syncthreads();  // the tile before is done with
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(tile)[(g + 16 * i) * (kTile / 8) + li] = w[i];
+      }
+
+      // ---- ROW: 16 lanes own a row
+      if constexpr (ROW) {
+        uint32_t key[8];  // max |x w| of the lane's chunk, then of its block
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          key[i] = bf16x8_key(w[i]);
+          // (rounding is monotonic: the largest |x w| is the largest |x| times |w|)
+          if constexpr (WGT) key[i] = abs_key(key_to_float(key[i]) * wr[i]);
+          key[i] = kMx ? quad_max(key[i]) : row16_max(key[i]);
+        }
+        float sj = 1.0f;                   // 1x128: the scale of row li % 8
+        bool bad = MODE == MODE_MX32F;     // an element may need the saturating encoder
+        if constexpr (!kMx) {
+          uint32_t kj = key[0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) kj = ((li & 7) == j) ? key[j] : kj;
+          const float am = key_to_float(kj);
+          sj = scale_from_amax<FMT>(am, a.margin);
+          bad = __any(!is_finite(am));
+          if (li < 8) {
+            reinterpret_cast<float*>(a.s_row)[(row0 + g + 16 * li) * tiles_x + bx] = recip_rn(sj);
+            if (bad && !is_finite(am) && a.nonfinite) atomicAdd(a.nonfinite, 1);
+          }
+        } else {
+          const int64_t gc = (a.cols + 31) / 32;
+          uint8_t* sr = reinterpret_cast<uint8_t*>(a.s_row) + (row0 + g) * gc + (col0 + 8 * li) / 32;
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            key[i] = (uint32_t)mx_byte<MODE, FMT>(key_to_float(key[i]));
+            odd = odd || key[i] == 0xFF;
+            if ((li & 3) == 0) {
+              sr[16 * i * gc] = (uint8_t)key[i];
+              if (key[i] == 0xFF && a.nonfinite) atomicAdd(a.nonfinite, 1);
+            }
+          }
+          bad = bad || __any(odd);
+        }
+        auto rows = [&](auto Safe) __attribute__((always_inline)) {
+          unrolled<8>([&](auto I) __attribute__((always_inline)) {
+            constexpr int i = decltype(I)::value;
+            float s;
+            if constexpr (kMx) s = key[i] == 0xFF ? 1.0f : mx_inv_scale((int)key[i]);
+            else s = row16_lane<i>(sj);
+            float v[8];
+            unpack_bf16x8(w[i], v);
+            if constexpr (WGT) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] *= wr[i];
+            }
+            const uint2 c = encode8<FMT, decltype(Safe)::value>(v, s);
+            uint8_t* q = a.q_row + (row0 + 16 * i) * a.ld_q_row + col0;  // (the same for all lanes)
+            const uint32_t at = (uint32_t)(g * a.ld_q_row + 8 * li);
+            st_stream8(q + at, c);
+            __builtin_amdgcn_sched_barrier(0);  // row by row: registers for one at a time
+          });
+        };
+        if (bad) rows(std::true_type{});
+        else rows(std::false_type{});
+      }
+
+      // ---- COL: thread (cp, rq) has rows 32 rq .. of the column pair 2 cp
+      if constexpr (COL) {
+        __syncthreads();
+        const int cp = tid & 63, rq = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int64_t col = col0 + 2 * cp;
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = tile[(32 * rq + j) * (kTile / 2) + cp];
+        uint32_t k0, k1;  // max |x w| of the columns' blocks
+        if constexpr (!WGT) {
+          u16x2 m = __builtin_bit_cast(u16x2, v[0] & 0x7FFF7FFFu);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[j] & 0x7FFF7FFFu));
+          if constexpr (!kMx) {
+            colred[rq][cp] = __builtin_bit_cast(uint32_t, m);
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, colred[q][cp]));
+          }
+          k0 = (uint32_t)m.x << 16;
+          k1 = (uint32_t)m.y << 16;
+        } else {
+          k0 = k1 = 0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float wt = __builtin_bit_cast(float, rowinfo[32 * rq + j].y);
+            k0 = umax32(k0, abs_key(bf_lo(v[j]) * wt));
+            k1 = umax32(k1, abs_key(bf_hi(v[j]) * wt));
+          }
+          if constexpr (!kMx) {
+            uint32_t* red = tile + kTile * kTile / 2;  // behind the rows
+            red[rq * kTile + cp] = k0;
+            red[rq * kTile + 64 + cp] = k1;
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              k0 = umax32(k0, red[q * kTile + cp]);
+              k1 = umax32(k1, red[q * kTile + 64 + cp]);
+            }
+          }
+        }
+        const float am0 = key_to_float(k0), am1 = key_to_float(k1);
+        float s0, s1;
+        bool bad = MODE == MODE_MX32F;
+        if constexpr (!kMx) {
+          s0 = scale_from_amax<FMT>(am0, a.margin);
+          s1 = scale_from_amax<FMT>(am1, a.margin);
+          bad = __any(!is_finite(am0) || !is_finite(am1));
+          if (rq == 0) {
+            float* sc = reinterpret_cast<float*>(a.s_col) + col * gr + by;
+            sc[0] = recip_rn(s0);
+            sc[gr] = recip_rn(s1);
+            if (bad && a.nonfinite) atomicAdd(a.nonfinite, (int)!is_finite(am0) + (int)!is_finite(am1));
+          }
+        } else {
+          const int b0 = mx_byte<MODE, FMT>(am0), b1 = mx_byte<MODE, FMT>(am1);
+          s0 = b0 == 0xFF ? 1.0f : mx_inv_scale(b0);
+          s1 = b1 == 0xFF ? 1.0f : mx_inv_scale(b1);
+          const bool odd = __any(b0 == 0xFF || b1 == 0xFF);
+          bad = bad || odd;
+          uint8_t* sc = reinterpret_cast<uint8_t*>(a.s_col) + col * (gr * 4) + by * 4 + rq;
+          sc[0] = (uint8_t)b0;
+          sc[gr * 4] = (uint8_t)b1;
+          if (odd && a.nonfinite) atomicAdd(a.nonfinite, (int)(b0 == 0xFF) + (int)(b1 == 0xFF));
+        }
+        // 32 codes of each column, then through LDS to whole 128-byte lines
+        uint32_t pk[2][8];
+        auto encode = [&](auto Safe) __attribute__((always_inline)) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float lo[4], hi[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              lo[e] = bf_lo(v[4 * q + e]);
+              hi[e] = bf_hi(v[4 * q + e]);
+              if constexpr (WGT) {
+                const float wt = __builtin_bit_cast(float, rowinfo[32 * rq + 4 * q + e].y);
+                lo[e] *= wt;
+                hi[e] *= wt;
+              }
+            }
+            pk[0][q] = encode4<FMT, decltype(Safe)::value>(lo[0] * s0, lo[1] * s0, lo[2] * s0, lo[3] * s0);
+            pk[1][q] = encode4<FMT, decltype(Safe)::value>(hi[0] * s1, hi[1] * s1, hi[2] * s1, hi[3] * s1);
+          }
+        };
+        if (bad) encode(std::true_type{});
+        else encode(std::false_type{});
+        __syncthreads();  // every wave has read the rows (and the maxima)
+        uint8_t* ct = reinterpret_cast<uint8_t*>(tile);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint4* d = reinterpret_cast<uint4*>(ct + (2 * cp + half) * kCodeStride + 32 * rq);
+          d[0] = make_uint4(pk[half][0], pk[half][1], pk[half][2], pk[half][3]);
+          d[1] = make_uint4(pk[half][4], pk[half][5], pk[half][6], pk[half][7]);
+        }
+        __syncthreads();
+        const int c = tid >> 3, m = tid & 7;
+        uint8_t* q = a.q_col + (col0 + c) * a.ld_q_col + row0 + 16 * m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(q + 32 * k * a.ld_q_col) =
+              *reinterpret_cast<const uint4*>(ct + (c + 32 * k) * kCodeStride + 16 * m);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Per-tensor amax for current scaling: max |x| over the tensor, NaN-dominant.
 // Each workgroup of the reduction pass stores its partial maximum (a |x| bit
 // pattern) in slot 1 + w of the caller's amax array; every workgroup of the
@@ -904,6 +1190,37 @@ hipError_t launch_moe_k(const MoeTileArgs& a, int64_t tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int FMT, int MODE, bool ROW, bool COL, bool WGT>
+hipError_t launch_moe_bf16(const MoeTileArgs& a, int64_t tiles, hipStream_t st) {
+  static std::atomic<int> occupancy{0};
+  auto k = moe_tile_kernel<FMT, MODE, ROW, COL, WGT>;
+  int per_cu = occupancy.load(std::memory_order_relaxed);
+  if (per_cu <= 0) {
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, k, kThreads, 0) != hipSuccess || per_cu <= 0) per_cu = 1;
+    occupancy.store(per_cu, std::memory_order_relaxed);
+  }
+  const int64_t most = (int64_t)cu_count(stream_device(st)) * per_cu;
+  // tiles a workgroup stays on its rows for: at most 8, fewer where that
+  // would leave compute units without work
+  int64_t chunk = tiles / (2 * most);
+  chunk = chunk < 1 ? 1 : (chunk > 8 ? 8 : chunk);
+  const int64_t units = (tiles + chunk - 1) / chunk;
+  const int64_t grid = units < most ? units : most;
+  k<<<(unsigned)grid, kThreads, 0, st>>>(a, (int)chunk);
+  return hipGetLastError();
+}
+
+template <typename InT, int FMT, int MODE, bool ROW, bool COL>
+hipError_t launch_moe_orient(const MoeTileArgs& a, int64_t tiles, hipStream_t st) {
+  // FP32 rows, and BF16 rows that end inside a tile, take the general kernel
+  if constexpr (sizeof(InT) == 2) {
+    if (a.cols % kTile == 0)
+      return a.weights ? launch_moe_bf16<FMT, MODE, ROW, COL, true>(a, tiles, st)
+                       : launch_moe_bf16<FMT, MODE, ROW, COL, false>(a, tiles, st);
+  }
+  return launch_moe_k<InT, FMT, MODE, ROW, COL>(a, tiles, st);
+}
+
 template <typename InT, int FMT, int MODE>
 hipError_t launch_moe(const MoeQuantParams& m, hipStream_t st) {
   const QuantParams& p = m.q;
@@ -919,9 +1236,9 @@ hipError_t launch_moe(const MoeQuantParams& m, hipStream_t st) {
   // at most this many: the rows that hold an expert's segment are fewer
   const int64_t tiles = ((p.cols + kTile - 1) / kTile) * (p.rows / kTile);
   const bool row = p.orient & 1, col = p.orient & 2;
-  if (row && col) return launch_moe_k<InT, FMT, MODE, true, true>(a, tiles, st);
-  if (row) return launch_moe_k<InT, FMT, MODE, true, false>(a, tiles, st);
-  return launch_moe_k<InT, FMT, MODE, false, true>(a, tiles, st);
+  if (row && col) return launch_moe_orient<InT, FMT, MODE, true, true>(a, tiles, st);
+  if (row) return launch_moe_orient<InT, FMT, MODE, true, false>(a, tiles, st);
+  return launch_moe_orient<InT, FMT, MODE, false, true>(a, tiles, st);
 }
 
 template <typename InT, int FMT>

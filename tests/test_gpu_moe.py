@@ -178,7 +178,7 @@ def test_rows_behind_the_last_segment_are_left_alone():
 
 
 CASTS = [(1, 1, 1, 16, "random", B), (200, 2, 8, 512, "dropped", B), (150, 3, 5, 1000, "half", F), (130, 2, 3, 136, "one", B),
-         (64, 1, 70, 384, "random", F)]
+         (64, 1, 70, 384, "random", F), (64, 1, 70, 384, "random", B), (2500, 4, 9, 1408, "dropped", B)]
 
 
 @pytest.mark.parametrize("tokens,topk,experts,cols,kind,dt", CASTS)
@@ -229,10 +229,20 @@ def test_quantize_sorted_rows_and_nonfinite():
     assert torch.equal(a.q_row[:end], b.q_row[:end]) and torch.equal(a.s_row[:end], b.s_row[:end])
     assert torch.equal(a.q_col[:, :end], b.q_col[:, :end]) and torch.equal(a.s_col[:, :end // 128], b.s_col[:, :end // 128])
     x[7, 3], x[9, 200] = float("nan"), float("inf")
-    count = torch.zeros(1, dtype=torch.int32, device="cuda")
-    q = moe.quantize(x, p, fm.BLOCK_1x128, fm.E4M3, fm.ROW, nonfinite=count)
-    assert int(count) == 4  # two slots each
+    xs = moe.dispatch(x, p)
+    xs[end:] = 0.0
+    for recipe in (fm.BLOCK_1x128, fm.MX_1x32, fm.MX_1x32_OCP):
+        for w_ in (None, torch.ones_like(w)):
+            for cols in (256, 232):  # whole tiles, and rows that end inside one
+                count, ref = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+                q = moe.quantize(x[:, :cols], p, recipe, fm.E5M2, fm.ROW_AND_COL, weights=w_, nonfinite=count)
+                f = fm.quantize(xs[:end, :cols], recipe, fm.E5M2, fm.ROW_AND_COL, nonfinite=ref)
+                assert int(count) == int(ref) > 0
+                n = f.s_col.shape[1]
+                assert torch.equal(q.q_row[:end, :cols], f.q_row[:, :cols]) and torch.equal(q.q_col[:, :end], f.q_col[:, :end])
+                assert torch.equal(q.s_row[:end], f.s_row) and torch.equal(q.s_col[:, :n], f.s_col)
     r = p.slot_row[7, 0]
+    q = moe.quantize(x, p, fm.BLOCK_1x128, fm.E4M3, fm.ROW)
     assert int(q.q_row[r, 3]) == 0x7F and float(q.s_row[r, 0]) == 1.0
 
 
