@@ -13,13 +13,13 @@ step can be captured in a graph and replayed with other routings.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
 from . import (COL, GEMM_MX_1x32, GROUP_CONTRACT, GROUP_ROWS,
-               IDX_I32, IDX_I64, IN_BF16, IN_FP32, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _ceil, _check, _ld,
-               _matrix, _need, _one_device, _pad16, _scope, _vector, fp8_gemm_grouped, fp8_moe_combine,
+               IDX_I32, IDX_I64, IN_BF16, IN_FP32, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _ceil, _check,
+               _is_matrix, _is_vector, _ld, _matrix, _need, _one_device, _pad16, _scope, _vector, fp8_gemm_grouped, fp8_moe_combine,
                fp8_moe_combine_backward, fp8_moe_dispatch, fp8_moe_quantize, fp8_moe_rows, fp8_moe_sort,
                fp8_moe_sort_workspace, load, scale_grid_shape)
 from . import quantize as _quantize_matrix
@@ -30,9 +30,7 @@ _IDX = {torch.int32: IDX_I32, torch.int64: IDX_I64}
 _CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
 
-@dataclass
-class Plan:
-    """A routing's segments and row maps (int32 device tensors)."""
+class _Fields(NamedTuple):
     tokens: int
     topk: int
     experts: int
@@ -43,42 +41,57 @@ class Plan:
     slot_row: torch.Tensor   # [tokens x topk] row of each slot, -1 where it was dropped
 
 
+class Plan(_Fields):
+    """A routing's segments and row maps (int32 device tensors).  It cannot be
+    changed, so its tensors' sizes are looked at once, here."""
+    __slots__ = ()
+
+    def __new__(cls, tokens, topk, experts, rows, offsets, counts, row_slot, slot_row):
+        for name, t, n in (("offsets", offsets, experts + 1), ("counts", counts, experts), ("row_slot", row_slot, rows),
+                           ("slot_row", slot_row, tokens * topk)):
+            if not _is_vector(t, torch.int32, n):
+                _vector("a plan's " + name, t, torch.int32, n)
+        _one_device(offsets, counts, row_slot, slot_row)
+        return super().__new__(cls, tokens, topk, experts, rows, offsets, counts, row_slot, slot_row)
+
+
 def sort(expert: torch.Tensor, experts: int, stream=None) -> Plan:
     """Sort the slots of ``expert`` [tokens x topk] (int32 or int64) by expert,
     stably; numbers outside [0, experts) drop their slot."""
-    _need(isinstance(expert, torch.Tensor) and expert.is_cuda, "expert must be a device tensor")
-    _need(expert.dim() == 2 and expert.dtype in _IDX, "expert must be a 2-D int32 or int64 tensor")
-    _need(expert.shape[1] >= 1, "expert needs at least one choice per token")
-    _need(expert.stride(1) == 1 or expert.shape[1] == 1, "expert must have unit column stride")
+    if not _is_matrix(expert, _IDX):
+        raise Fp8Error("expert must be a 2-D int32 or int64 device tensor with unit column stride")
     tokens, topk = expert.shape
+    if topk < 1:
+        raise Fp8Error("expert needs at least one choice per token")
     rows = fp8_moe_rows(tokens, topk, experts)
-    _check(min(rows, 0), "fp8_moe_rows")
+    if rows < 0:
+        _check(rows, "fp8_moe_rows")
     size = fp8_moe_sort_workspace(tokens, topk, experts)
     dev, i32 = expert.device, torch.int32
     with _scope(dev, stream):
         offsets, counts = torch.empty(experts + 1, dtype=i32, device=dev), torch.empty(experts, dtype=i32, device=dev)
         row_slot, slot_row = torch.empty(rows, dtype=i32, device=dev), torch.empty(tokens, topk, dtype=i32, device=dev)
-        ws = torch.empty(size // 4, dtype=i32, device=dev) if size else None
-        _check(fp8_moe_sort(expert, _IDX[expert.dtype], tokens, topk, _ld(expert), experts, offsets, counts,
-                            row_slot, rows, slot_row, ws, size), "fp8_moe_sort")
-    return Plan(tokens, topk, experts, rows, offsets, counts, row_slot, slot_row)
-
-
-def _check_plan(p: Plan) -> None:
-    for name, n in (("offsets", p.experts + 1), ("counts", p.experts), ("row_slot", p.rows),
-                    ("slot_row", p.tokens * p.topk)):
-        _vector("plan." + name, getattr(p, name), torch.int32, n)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        st = fp8_moe_sort(expert, _IDX[expert.dtype], tokens, topk, _ld(expert), experts, offsets, counts, row_slot,
+                          rows, slot_row, ws, size)
+    _check(st, "fp8_moe_sort")
+    return tuple.__new__(Plan, (tokens, topk, experts, rows, offsets, counts, row_slot, slot_row))
 
 
 def _check_weights(p: Plan, weights) -> None:
     if weights is not None:
-        _vector("weights", weights, torch.float32, p.tokens * p.topk)
-        _need(weights.numel() == p.tokens * p.topk, f"weights is {tuple(weights.shape)}; needs {p.tokens} x {p.topk}")
+        n = p.tokens * p.topk
+        if not _is_vector(weights, torch.float32, n):
+            _vector("weights", weights, torch.float32, n)
+        if weights.numel() != n:
+            raise Fp8Error(f"weights is {tuple(weights.shape)}; needs {p.tokens} x {p.topk}")
 
 
 def _rows_matrix(name: str, t: torch.Tensor, rows: int) -> None:
-    _matrix(name, t, tuple(_DTYPES))
-    _need(t.shape[0] == rows, f"{name} has {t.shape[0]} rows; needs {rows}")
+    if not _is_matrix(t, _DTYPES):
+        _matrix(name, t, tuple(_DTYPES))
+    if t.shape[0] != rows:
+        raise Fp8Error(f"{name} has {t.shape[0]} rows; needs {rows}")
 
 
 # ---------------------------------------------------------------------------
@@ -86,28 +99,28 @@ def _rows_matrix(name: str, t: torch.Tensor, rows: int) -> None:
 # ---------------------------------------------------------------------------
 
 def _dispatch(x, plan, weights, stream):
-    _check_plan(plan)
     _rows_matrix("x", x, plan.tokens)
     _check_weights(plan, weights)
     _one_device(x, plan.slot_row, weights)
     cols = x.shape[1]
     with _scope(x.device, stream):
         y = torch.empty(plan.rows, cols, dtype=x.dtype, device=x.device)
-        _check(fp8_moe_dispatch(x, _DTYPES[x.dtype], plan.tokens, cols, _ld(x), plan.topk, weights, plan.slot_row,
-                                plan.offsets, plan.counts, plan.experts, y, plan.rows, cols), "fp8_moe_dispatch")
+        st = fp8_moe_dispatch(x, _DTYPES[x.dtype], plan.tokens, cols, _ld(x), plan.topk, weights, plan.slot_row,
+                              plan.offsets, plan.counts, plan.experts, y, plan.rows, cols)
+    _check(st, "fp8_moe_dispatch")
     return y
 
 
 def _combine(ys, plan, weights, stream):
-    _check_plan(plan)
     _rows_matrix("ys", ys, plan.rows)
     _check_weights(plan, weights)
     _one_device(ys, plan.slot_row, weights)
     cols = ys.shape[1]
     with _scope(ys.device, stream):
         y = torch.empty(plan.tokens, cols, dtype=ys.dtype, device=ys.device)
-        _check(fp8_moe_combine(ys, _DTYPES[ys.dtype], plan.rows, cols, _ld(ys), plan.slot_row, plan.tokens, plan.topk,
-                               weights, y, cols), "fp8_moe_combine")
+        st = fp8_moe_combine(ys, _DTYPES[ys.dtype], plan.rows, cols, _ld(ys), plan.slot_row, plan.tokens, plan.topk,
+                             weights, y, cols)
+    _check(st, "fp8_moe_combine")
     return y
 
 
@@ -116,21 +129,21 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor | None, plan: Plan, weig
     """The gradient of combine: (dys [plan.rows x cols] with zeros in the rows
     without a slot, dweights [tokens x topk] FP32).  rows=False or dots=False
     leaves one out (None); without dots, ys is not read and may be None."""
-    _check_plan(plan)
     _rows_matrix("dy", dy, plan.tokens)
     _check_weights(plan, weights)
     if dots:
         _rows_matrix("ys", ys, plan.rows)
-        _need(ys.dtype == dy.dtype and ys.shape[1] == dy.shape[1], "dy and ys must have one dtype and width")
+        if ys.dtype != dy.dtype or ys.shape[1] != dy.shape[1]:
+            raise Fp8Error("dy and ys must have one dtype and width")
     _one_device(dy, ys, plan.slot_row, weights)
     cols, dev = dy.shape[1], dy.device
     with _scope(dev, stream):
         dys = torch.empty(plan.rows, cols, dtype=dy.dtype, device=dev) if rows else None
         dw = torch.empty(plan.tokens, plan.topk, dtype=torch.float32, device=dev) if dots else None
-        _check(fp8_moe_combine_backward(dy, _DTYPES[dy.dtype], plan.tokens, cols, _ld(dy), ys if dots else None,
-                                        _ld(ys) if dots else 0, plan.slot_row, plan.offsets, plan.counts,
-                                        plan.experts, plan.topk, weights, dys, plan.rows, cols, dw),
-               "fp8_moe_combine_backward")
+        st = fp8_moe_combine_backward(dy, _DTYPES[dy.dtype], plan.tokens, cols, _ld(dy), ys if dots else None,
+                                      _ld(ys) if dots else 0, plan.slot_row, plan.offsets, plan.counts, plan.experts,
+                                      plan.topk, weights, dys, plan.rows, cols, dw)
+    _check(st, "fp8_moe_combine_backward")
     return dys, dw
 
 
@@ -200,7 +213,6 @@ def quantize(x: torch.Tensor, plan: Plan, recipe: int, fmt: int, orient: int = R
     """FP8 codes and scales of the sorted rows: of x [tokens x cols] read through
     the plan (gather), each row times its slot's weight, or of x [plan.rows x
     cols] itself.  recipe: BLOCK_1x128, MX_1x32 or MX_1x32_OCP."""
-    _check_plan(plan)
     _rows_matrix("x", x, plan.tokens if gather else plan.rows)
     _check_weights(plan, weights)
     if nonfinite is not None:
@@ -218,10 +230,10 @@ def quantize(x: torch.Tensor, plan: Plan, recipe: int, fmt: int, orient: int = R
             out.q_col = torch.empty(cols, ld_c, dtype=torch.uint8, device=dev)
             shp, dt = scale_grid_shape(recipe, rows, cols, COL)
             out.s_col = torch.empty(shp, dtype=dt, device=dev) if shp is not None else None
-        _check(fp8_moe_quantize(x, _DTYPES[x.dtype], x.shape[0], cols, _ld(x), plan.row_slot if gather else None,
-                                plan.topk, weights, plan.offsets, plan.experts, rows, recipe, fmt, orient, margin,
-                                out.q_row, ld_r, out.s_row, out.q_col, ld_c, out.s_col, nonfinite),
-               "fp8_moe_quantize")
+        st = fp8_moe_quantize(x, _DTYPES[x.dtype], x.shape[0], cols, _ld(x), plan.row_slot if gather else None,
+                              plan.topk, weights, plan.offsets, plan.experts, rows, recipe, fmt, orient, margin,
+                              out.q_row, ld_r, out.s_row, out.q_col, ld_c, out.s_col, nonfinite)
+    _check(st, "fp8_moe_quantize")
     return out
 
 
@@ -229,12 +241,21 @@ def quantize(x: torch.Tensor, plan: Plan, recipe: int, fmt: int, orient: int = R
 # the experts' products
 # ---------------------------------------------------------------------------
 
-def _offsets(offsets: torch.Tensor, like: torch.Tensor) -> int:
-    _need(isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.numel() >= 2,
-          "offsets must be a vector of experts + 1 numbers")
-    _vector("offsets", offsets, torch.int32, 2)
-    _one_device(like, offsets)
+def _offsets(offsets: torch.Tensor) -> int:
+    if not (_is_vector(offsets, torch.int32, 2) and offsets.dim() == 1):
+        raise Fp8Error("offsets must be a contiguous int32 device vector of experts + 1 numbers")
     return offsets.numel() - 1
+
+
+def _out_of(c, shape, out_dtype, device) -> torch.Tensor:
+    if c is None:
+        if out_dtype not in _OUT_DTYPES:
+            raise Fp8Error(f"out_dtype must be one of {tuple(_OUT_DTYPES)}")
+        return torch.empty(shape, dtype=out_dtype, device=device)
+    if not (isinstance(c, torch.Tensor) and c.is_cuda and c.dtype in _OUT_DTYPES and tuple(c.shape) == shape
+            and (c.stride(-1) == 1 or shape[-1] <= 1)):
+        raise Fp8Error(f"c must be a BF16 or FP32 device tensor {shape} with unit last stride")
+    return c
 
 
 def gemm(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, fmt_b: int, s_b: torch.Tensor, recipe: int,
@@ -246,32 +267,32 @@ def gemm(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, fmt_b:
     x N x K/32] bytes), each with unit last stride and any others, so that a
     view of transposed codes will do.  Rows behind the last segment are left as
     they were."""
-    _matrix("a", a, _CODES)
-    experts = _offsets(offsets, a)
-    _need(isinstance(b, torch.Tensor) and b.is_cuda and b.dtype in _CODES, "b must be a device tensor of codes")
-    _need(b.dim() == 3 and b.shape[0] == experts and (b.stride(2) == 1 or b.shape[2] <= 1),
-          f"b must be {experts} x N x K with unit last stride")
-    rows, n, k = a.shape[0], b.shape[1], b.shape[2]
-    _need(a.shape[1] >= k, f"a is {tuple(a.shape)}; needs at least {rows} x {k}")
+    if not _is_matrix(a, _CODES):
+        _matrix("a", a, _CODES)
+    experts = _offsets(offsets)
+    if not (isinstance(b, torch.Tensor) and b.is_cuda and b.dtype in _CODES and b.dim() == 3 and b.shape[0] == experts
+            and (b.stride(2) == 1 or b.shape[2] <= 1)):
+        raise Fp8Error(f"b must be a device tensor of codes, {experts} x N x K with unit last stride")
+    rows, (_, n, k) = a.shape[0], b.shape
+    if a.shape[1] < k:
+        raise Fp8Error(f"a is {tuple(a.shape)}; needs at least {rows} x {k}")
     mx = recipe == GEMM_MX_1x32
-    per = 32 if mx else 128
     dtype = torch.uint8 if mx else torch.float32
-    grid = (experts, n if mx else _ceil(n, 128), _ceil(k, per))
-    _vector("s_a", s_a, dtype, rows * grid[2])
-    _need(isinstance(s_b, torch.Tensor) and s_b.is_cuda and s_b.dtype == dtype, f"s_b must be a {dtype} device tensor")
-    _need(tuple(s_b.shape) == grid and (s_b.stride(2) == 1 or grid[2] <= 1), f"s_b is {tuple(s_b.shape)}; needs {grid}")
-    _one_device(a, s_a, b, s_b, c)
-    ldb = b.stride(1) if n > 1 else max(b.stride(1), k)
-    ld_sb = s_b.stride(1) if grid[1] > 1 else max(s_b.stride(1), grid[2])
+    grid = (experts, n if mx else _ceil(n, 128), _ceil(k, 32 if mx else 128))
+    if not _is_vector(s_a, dtype, rows * grid[2]):
+        _vector("s_a", s_a, dtype, rows * grid[2])
+    if not (isinstance(s_b, torch.Tensor) and s_b.is_cuda and s_b.dtype == dtype and tuple(s_b.shape) == grid
+            and (s_b.stride(2) == 1 or grid[2] <= 1)):
+        raise Fp8Error(f"s_b must be a {dtype} device tensor {grid} with unit last stride")
+    _one_device(a, offsets, s_a, b, s_b, c)
     with _scope(a.device, stream):
-        if c is None:
-            _need(out_dtype in _OUT_DTYPES, f"out_dtype must be one of {tuple(_OUT_DTYPES)}")
-            c = torch.empty(rows, n, dtype=out_dtype, device=a.device)
-        _matrix("c", c, tuple(_OUT_DTYPES))
-        _need(c.shape[0] >= rows and c.shape[1] >= n, f"c is {tuple(c.shape)}; needs at least {rows} x {n}")
-        _check(fp8_gemm_grouped(a, fmt_a, s_a, _ld(a), b, fmt_b, s_b, ldb, b.stride(0) if experts > 1 else 0, ld_sb,
-                                s_b.stride(0) if experts > 1 else 0, recipe, GROUP_ROWS, offsets, experts, rows, 0, n,
-                                k, c, _OUT_DTYPES[c.dtype], _ld(c), 0), "fp8_gemm_grouped")
+        c = _out_of(c, (rows, n), out_dtype, a.device)
+        st = fp8_gemm_grouped(a, fmt_a, s_a, _ld(a), b, fmt_b, s_b, b.stride(1) if n > 1 else max(b.stride(1), k),
+                              b.stride(0) if experts > 1 else 0,
+                              s_b.stride(1) if grid[1] > 1 else max(s_b.stride(1), grid[2]),
+                              s_b.stride(0) if experts > 1 else 0, recipe, GROUP_ROWS, offsets, experts, rows, 0, n, k,
+                              c, _OUT_DTYPES[c.dtype], _ld(c), 0)
+    _check(st, "fp8_gemm_grouped")
     return c
 
 
@@ -282,28 +303,27 @@ def gemm_wgrad(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, 
     expert: a [M x rows], b [N x rows] the transposed codes of the sorted rows
     (quantize's COL outputs), s_a and s_b their grids [M x rows/128] and [N x
     rows/128] (GEMM_MX_1x32: rows/32 bytes); c [experts x M x N]."""
-    _matrix("a", a, _CODES)
-    _matrix("b", b, _CODES)
-    experts = _offsets(offsets, a)
-    m, rows = a.shape
-    n = b.shape[0]
-    _need(b.shape[1] == rows, f"a has {rows} columns, b {b.shape[1]}")
+    for name, t in (("a", a), ("b", b)):
+        if not _is_matrix(t, _CODES):
+            _matrix(name, t, _CODES)
+    experts = _offsets(offsets)
+    (m, rows), n = a.shape, b.shape[0]
+    if b.shape[1] != rows:
+        raise Fp8Error(f"a has {rows} columns, b {b.shape[1]}")
     mx = recipe == GEMM_MX_1x32
     dtype = torch.uint8 if mx else torch.float32
-    for name, t, lines in (("s_a", s_a, m), ("s_b", s_b, n)):
-        _vector(name, t, dtype, lines * _ceil(rows, 32 if mx else 128))
-    _one_device(a, s_a, b, s_b, c)
+    for name, t, size in (("s_a", s_a, m * _ceil(rows, 32 if mx else 128)), ("s_b", s_b, n * _ceil(rows, 32 if mx else 128))):
+        if not _is_vector(t, dtype, size):
+            _vector(name, t, dtype, size)
+    _one_device(a, offsets, s_a, b, s_b, c)
     with _scope(a.device, stream):
-        if c is None:
-            _need(out_dtype in _OUT_DTYPES, f"out_dtype must be one of {tuple(_OUT_DTYPES)}")
-            c = torch.empty(experts, m, n, dtype=out_dtype, device=a.device)
-        _need(isinstance(c, torch.Tensor) and c.is_cuda and c.dtype in _OUT_DTYPES, "c must be a BF16 or FP32 device tensor")
-        _need(tuple(c.shape) == (experts, m, n) and (c.stride(2) == 1 or n <= 1),
-              f"c is {tuple(c.shape)}; needs {(experts, m, n)} with unit last stride")
-        _need(experts == 1 or m * n == 0 or c.stride(0) >= (m - 1) * c.stride(1) + n, "c's experts must not overlap")
-        _check(fp8_gemm_grouped(a, fmt_a, s_a, _ld(a), b, fmt_b, s_b, _ld(b), 0, 0, 0, recipe, GROUP_CONTRACT, offsets,
-                                experts, rows, m, n, 0, c, _OUT_DTYPES[c.dtype],
-                                c.stride(1) if m > 1 else max(c.stride(1), n), c.stride(0)), "fp8_gemm_grouped")
+        c = _out_of(c, (experts, m, n), out_dtype, a.device)
+        ldc = c.stride(1) if m > 1 else max(c.stride(1), n)
+        if experts > 1 and m * n > 0 and c.stride(0) < (m - 1) * ldc + n:
+            raise Fp8Error("c's experts must not overlap")
+        st = fp8_gemm_grouped(a, fmt_a, s_a, _ld(a), b, fmt_b, s_b, _ld(b), 0, 0, 0, recipe, GROUP_CONTRACT, offsets,
+                              experts, rows, m, n, 0, c, _OUT_DTYPES[c.dtype], ldc, c.stride(0))
+    _check(st, "fp8_gemm_grouped")
     return c
 
 

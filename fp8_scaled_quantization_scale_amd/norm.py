@@ -9,21 +9,33 @@ from __future__ import annotations
 
 import torch
 
-from . import (IN_BF16, IN_FP32, Fp8Error, _check, _ld, _matrix, _need, _one_device, _scope, _vector,
+from . import (IN_BF16, IN_FP32, Fp8Error, _check, _is_matrix, _is_vector, _ld, _matrix, _one_device, _scope, _vector,
                fp8_layer_norm_backward, fp8_layer_norm_forward, fp8_layer_norm_workspace)
 
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
+
+
+def _check_x(x) -> None:
+    if not _is_matrix(x, _DTYPES):
+        _matrix("x", x, tuple(_DTYPES))
+    if x.shape[1] < 1:
+        raise Fp8Error("x needs at least one column")
 
 
 def _params(cols: int, weight, bias):
     """dtype of the parameters (FP32 where there are none)."""
     dtype = None
     for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _need(isinstance(t, torch.Tensor) and t.dtype in _DTYPES, f"{name} must be a BF16 or FP32 tensor")
-            _need(dtype is None or t.dtype == dtype, "weight and bias must have one dtype")
-            _need(t.dim() == 1 and t.numel() == cols, f"{name} is {tuple(t.shape)}; needs ({cols},)")
-            dtype = t.dtype
+        if t is None:
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype in _DTYPES):
+            raise Fp8Error(f"{name} must be a BF16 or FP32 device tensor")
+        if dtype is not None and t.dtype != dtype:
+            raise Fp8Error("weight and bias must have one dtype")
+        dtype = t.dtype
+        if t.dim() != 1 or t.numel() != cols:
+            raise Fp8Error(f"{name} is {tuple(t.shape)}; needs ({cols},)")
+        if not _is_vector(t, dtype, cols):
             _vector(name, t, dtype, cols)
     return dtype or torch.float32
 
@@ -32,16 +44,18 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, bias
                        eps: float = 1e-5, stream=None):
     """(y, mean, rstd) of the rows of a 2-D x (unit column stride): y as x, the
     FP32 statistics for layer_norm_backward."""
-    _matrix("x", x, tuple(_DTYPES))
+    _check_x(x)
     rows, cols = x.shape
-    _need(cols >= 1, "x needs at least one column")
     w_dtype = _params(cols, weight, bias)
     _one_device(x, weight, bias)
-    with _scope(x.device, stream):
-        y = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
-        mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=x.device).unbind(0)
-        _check(fp8_layer_norm_forward(x, _DTYPES[x.dtype], rows, cols, _ld(x), weight, bias, _DTYPES[w_dtype], eps,
-                                      y, cols, mean, rstd), "fp8_layer_norm_forward")
+    dev = x.device
+    with _scope(dev, stream):
+        y = torch.empty(rows, cols, dtype=x.dtype, device=dev)
+        mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        st = fp8_layer_norm_forward(x, _DTYPES[x.dtype], rows, cols, _ld(x), weight, bias, _DTYPES[w_dtype], eps, y,
+                                    cols, mean, rstd)
+    _check(st, "fp8_layer_norm_forward")
     return y, mean, rstd
 
 
@@ -49,14 +63,16 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor 
                         rstd: torch.Tensor, params: bool = True, stream=None):
     """(dx, dweight, dbias); params=False leaves the last two out (None).  They
     take the weight's dtype, FP32 where there is no weight."""
-    _matrix("x", x, tuple(_DTYPES))
-    _matrix("dy", dy, (x.dtype,))
+    _check_x(x)
+    if not _is_matrix(dy, (x.dtype,)):
+        _matrix("dy", dy, (x.dtype,))
     rows, cols = x.shape
-    _need(cols >= 1, "x needs at least one column")
-    _need(dy.shape == x.shape, f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
+    if dy.shape != x.shape:
+        raise Fp8Error(f"dy is {tuple(dy.shape)}, x {tuple(x.shape)}")
     w_dtype = _params(cols, weight, None)
-    _vector("mean", mean, torch.float32, rows)
-    _vector("rstd", rstd, torch.float32, rows)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if not _is_vector(t, torch.float32, rows):
+            _vector(name, t, torch.float32, rows)
     _one_device(x, dy, weight, mean, rstd)
     dev = x.device
     with _scope(dev, stream):
@@ -64,12 +80,14 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor 
         dw = db = ws = None
         size = 0
         if params:
-            dw, db = torch.empty(2, cols, dtype=w_dtype, device=dev).unbind(0)
+            dw, db = torch.empty(cols, dtype=w_dtype, device=dev), torch.empty(cols, dtype=w_dtype, device=dev)
             size = fp8_layer_norm_workspace(rows, cols)
-            _need(size > 0, f"no layer norm of {rows} x {cols}")
-            ws = torch.empty(size // 4, dtype=torch.float32, device=dev)
-        _check(fp8_layer_norm_backward(dy, _ld(dy), x, _DTYPES[x.dtype], rows, cols, _ld(x), weight, _DTYPES[w_dtype],
-                                       mean, rstd, dx, cols, dw, db, ws, size), "fp8_layer_norm_backward")
+            if size < 0:
+                _check(size, "fp8_layer_norm_workspace")
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        st = fp8_layer_norm_backward(dy, _ld(dy), x, _DTYPES[x.dtype], rows, cols, _ld(x), weight, _DTYPES[w_dtype],
+                                     mean, rstd, dx, cols, dw, db, ws, size)
+    _check(st, "fp8_layer_norm_backward")
     return dx, dw, db
 
 

@@ -183,12 +183,12 @@ def test_gemm_grouped(kw, code):
 def test_bindings_refuse_host_tensors():
     x, e = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int64)
     i = torch.zeros(8, dtype=torch.int32)
-    plan = moe.Plan(4, 2, 7, 8, i, i, i, i)
+    plan = tuple.__new__(moe.Plan, (4, 2, 7, 8, i, i, i, i))
     q, s = torch.zeros(128, 64, dtype=torch.uint8), torch.ones(128)
     for bad in (lambda: norm.layer_norm_forward(x), lambda: norm.layer_norm_backward(x, x, None, s, s), lambda: moe.sort(e, 8),
                 lambda: moe.dispatch(x, plan), lambda: moe.combine(x, plan), lambda: moe.combine_backward(x, x, plan, None),
                 lambda: moe.quantize(x, plan, fm.BLOCK_1x128, fm.E4M3),
                 lambda: moe.gemm(q, 0, s, q.view(1, 128, 64), 0, s, fm.GEMM_MX_1x32, i), lambda: moe.gemm_wgrad(q, 0, s, q, 0, s, 3, i),
-                lambda: norm.LayerNorm(64)(x)):
-        with pytest.raises(fm.Fp8Error, match="device tensor|GPU only"):
+                lambda: moe.Plan(4, 2, 7, 8, i, i, i, i), lambda: norm.LayerNorm(64)(x)):
+        with pytest.raises(fm.Fp8Error, match="device tensor|device vector|GPU only"):
             bad()
