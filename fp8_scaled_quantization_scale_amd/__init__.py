@@ -285,10 +285,20 @@ def _scope(device: torch.device, stream):
     allocated inside belongs to that stream, so a workspace that is freed when
     the call returns is not handed to another stream's work before its own."""
     if stream is None:
-        return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _NOTHING if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
+
+
+def _at(t):
+    """Address of a tensor whose checks are done (None stays None)."""
+    return None if t is None else t.data_ptr()
+
+
+def _here(device: torch.device) -> int:
+    """The current stream of `device`."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _one_device(first: torch.Tensor, *others) -> None:

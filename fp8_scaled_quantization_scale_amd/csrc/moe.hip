@@ -65,9 +65,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
 }
 
-template <typename Idx>
+// PER: slots per lane, whose experts stay in registers from the count to the
+// walk (0: any number, read twice).
+template <typename Idx, int PER>
 __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
   extern __shared__ int cnt[];  // [kSortWaves][experts]: counts, then the next row of each
+  __shared__ int sums[2][kSortThreads];  // parts of the ranges' sums
   __shared__ int at[kMaxExperts + 1];  // segment starts
   __shared__ int total[kMaxExperts];
   __shared__ int wave_total[kSortWaves];
@@ -77,9 +80,33 @@ __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
 
   for (int i = tid; i < kSortWaves * a.experts; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  for (int64_t s = from + lane; s < to; s += 64) {
-    const int e = expert_of<Idx>(a, s);
-    if (e >= 0) atomicAdd(&cnt[wave * a.experts + e], 1);
+  int held[PER ? PER : 1];
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) held[i] = from + 64 * i + lane < to ? expert_of<Idx>(a, from + 64 * i + lane) : -1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (held[i] >= 0) atomicAdd(&cnt[wave * a.experts + held[i]], 1);
+  } else {
+    for (int64_t s = from + lane; s < to; s += 64) {
+      const int e = expert_of<Idx>(a, s);
+      if (e >= 0) atomicAdd(&cnt[wave * a.experts + e], 1);
+    }
+  }
+  // the ranges' counts, added up by as many threads per expert as there are
+  const int wide = a.experts > 1 ? 1 << (32 - __clz(a.experts - 1)) : 1;  // experts, up to a power of two
+  const int groups = min(kSortThreads / wide, 32);
+  if (a.blocks > 1) {
+    const int x = tid & (wide - 1), part = tid / wide;
+    int all = 0, before = 0;
+    if (x < a.experts && part < groups)
+      for (int b = part; b < a.blocks; b += groups) {
+        const int n = a.hist[(int64_t)b * a.experts + x];
+        all += n;
+        before += b < (int)blockIdx.x ? n : 0;
+      }
+    sums[0][tid] = all;
+    sums[1][tid] = before;
   }
   __syncthreads();
 
@@ -92,10 +119,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
     if (a.blocks == 1) {
       all = mine;
     } else {
-      for (int b = 0; b < a.blocks; ++b) {
-        const int n = a.hist[(int64_t)b * a.experts + e];
-        all += n;
-        if (b < (int)blockIdx.x) before += n;
+      for (int g = 0; g < groups; ++g) {
+        all += sums[0][g * wide + e];
+        before += sums[1][g * wide + e];
       }
     }
   }
@@ -136,9 +162,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
   // rows of this wave's slots, in order
   const int bits = 32 - __clz(a.experts);  // of an expert's number plus one
   volatile int* next = cnt + wave * a.experts;
-  for (int64_t s0 = from; s0 < to; s0 += 64) {
-    const int64_t s = s0 + lane;
-    const int k = s < to ? expert_of<Idx>(a, s) : -1;
+  auto walk = [&](int64_t s, int k) __attribute__((always_inline)) {
     uint64_t same = ~0ull;  // lanes with this lane's expert
     for (int b = 0; b < bits; ++b) {
       const bool set = ((k + 1) >> b) & 1;
@@ -155,6 +179,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
       a.slot_row[s] = row;
       if (row >= 0 && row < a.rows) a.row_slot[row] = (int)s;
     }
+  };
+  if constexpr (PER > 0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) walk(from + 64 * i + lane, held[i]);
+  } else {
+    for (int64_t s0 = from; s0 < to; s0 += 64) walk(s0 + lane, s0 + lane < to ? expert_of<Idx>(a, s0 + lane) : -1);
   }
 
   // rows that hold no slot: the segments' ends, and what lies behind the last
@@ -170,10 +200,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
 // Rows to and from the sorted buffer.  All three are bound by memory; a wave
 // works on one token's (or one pad row's) piece of 64 chunks x kPiece, so the
 // token's row numbers and weights are the same for all its lanes.
+//
+// Outputs of dispatch and combine that would fill half the 256 MB Infinity
+// Cache by themselves are written past it (combine 16384 x 8192 of 4: 256 -> 237
+// us; 8192 x 4096 of 2, whose output a next kernel finds there: 36.0 us, past it
+// 38.1), the gradient's sorted rows always are (4095 x 4096 of 8: 125 -> 118 us,
+// 300 x 1024 of 8: 10.1 -> 8.6).  512 threads: the gradient of 4095 x 4096 took
+// 131 us with 256 and 148 with 128, the others the same.
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 2;                       // chunks of 8 elements per lane
 constexpr int kPieceCols = 64 * 8 * kPiece;     // columns of a piece
-constexpr int kRowThreads = 256, kRowWaves = kRowThreads / 64;
+constexpr int kRowThreads = 512, kRowWaves = kRowThreads / 64;
 
 struct RowArgs {
   int64_t tokens, cols, rows, ld_token, ld_expert, ld_out;
@@ -198,7 +235,7 @@ __device__ __forceinline__ void zero_pads(const RowArgs& a, int x) {
 }
 
 // out[row(t, j)] = w_tj x[t]
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a, int64_t token_blocks) {
   if ((int64_t)blockIdx.x >= token_blocks) return zero_pads<T>(a, (int)(blockIdx.x - token_blocks));
   const int lane = threadIdx.x & 63;
@@ -225,13 +262,13 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a, int64_
         for (int e = 0; e < 8; ++e) v[e] *= w;
         o.set(v);
       }
-      o.store(dst + c0 + i * 512, a.cols - (c0 + i * 512));
+      o.template store<NT>(dst + c0 + i * 512, a.cols - (c0 + i * 512));
     }
   }
 }
 
 // y[t] = sum_j w_tj ys[row(t, j)], in FP32
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -275,7 +312,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
   for (int i = 0; i < kPiece; ++i) {
     Chunk<T> o;
     o.set(acc[i]);
-    o.store(static_cast<T*>(a.out) + t * a.ld_out + c0 + i * 512, a.cols - (c0 + i * 512));
+    o.template store<NT>(static_cast<T*>(a.out) + t * a.ld_out + c0 + i * 512, a.cols - (c0 + i * 512));
   }
 }
 
@@ -322,7 +359,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = g[e] * w[q];
           k.set(v);
-          k.store(static_cast<T*>(a.out) + row[q] * a.ld_out + c, a.cols - c);
+          k.template store<true>(static_cast<T*>(a.out) + row[q] * a.ld_out + c, a.cols - c);
         }
       }
       if (a.dweights) {
@@ -365,6 +402,11 @@ RowArgs args_of(const MoeRowsParams& p) {
                  p.out,          p.dweights};
 }
 
+// whether `rows` rows of output are written past the caches
+bool past_caches(int64_t rows, const MoeRowsParams& p) {
+  return rows * p.cols * (p.dtype == kInBf16 ? 2 : 4) > (128LL << 20);
+}
+
 int64_t sort_range(int64_t slots) {
   const int64_t least = (slots + kSortMaxBlocks - 1) / kSortMaxBlocks;
   const int64_t range = least > kSortRange ? least : kSortRange;
@@ -392,7 +434,9 @@ hipError_t sort_any(const MoeSortParams& p, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  sort_rows_kernel<Idx><<<(unsigned)a.blocks, kSortThreads, kSortWaves * a.experts * sizeof(int), st>>>(a);
+  const size_t lds = kSortWaves * a.experts * sizeof(int);
+  if (a.range == kSortRange) sort_rows_kernel<Idx, kSortRange / kSortThreads><<<(unsigned)a.blocks, kSortThreads, lds, st>>>(a);
+  else sort_rows_kernel<Idx, 0><<<(unsigned)a.blocks, kSortThreads, lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -411,16 +455,26 @@ hipError_t launch_moe_dispatch(const MoeRowsParams& p, hipStream_t st) {
   const RowArgs a = args_of(p);
   const int64_t blocks = (p.tokens * a.pieces + kRowWaves - 1) / kRowWaves;
   const unsigned grid = (unsigned)(blocks + p.experts);
-  if (p.dtype == kInBf16) dispatch_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(a, blocks);
-  else dispatch_kernel<float><<<grid, kRowThreads, 0, st>>>(a, blocks);
+  const bool past = past_caches(p.tokens * p.topk, p);
+  if (p.dtype == kInBf16)
+    past ? dispatch_kernel<uint16_t, true><<<grid, kRowThreads, 0, st>>>(a, blocks)
+         : dispatch_kernel<uint16_t, false><<<grid, kRowThreads, 0, st>>>(a, blocks);
+  else
+    past ? dispatch_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a, blocks)
+         : dispatch_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a, blocks);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const MoeRowsParams& p, hipStream_t st) {
   const RowArgs a = args_of(p);
   const unsigned grid = (unsigned)((p.tokens * a.pieces + kRowWaves - 1) / kRowWaves);
-  if (p.dtype == kInBf16) combine_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(a);
-  else combine_kernel<float><<<grid, kRowThreads, 0, st>>>(a);
+  const bool past = past_caches(p.tokens, p);
+  if (p.dtype == kInBf16)
+    past ? combine_kernel<uint16_t, true><<<grid, kRowThreads, 0, st>>>(a)
+         : combine_kernel<uint16_t, false><<<grid, kRowThreads, 0, st>>>(a);
+  else
+    past ? combine_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a)
+         : combine_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 

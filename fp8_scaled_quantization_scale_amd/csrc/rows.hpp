@@ -14,6 +14,14 @@ namespace fp8mi {
 typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 
+// NT: written past the caches, for output that nothing reads before it would
+// have left them anyway
+template <bool NT, typename V>
+__device__ __forceinline__ void put(V v, V* p) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 // the 8 elements as they lie in memory (BF16: 16 bytes, FP32: 32)
 template <typename T>
 struct Chunk;
@@ -48,10 +56,11 @@ struct Chunk<uint16_t> {
     }
     w = make_uint4(p[0], p[1], p[2], p[3]);
   }
+  template <bool NT = false>
   __device__ __forceinline__ void store(uint16_t* p, int64_t n) const {
     if (n >= 8) {
       const u32x4a2 v = {w.x, w.y, w.z, w.w};
-      *reinterpret_cast<u32x4a2*>(p) = v;
+      put<NT>(v, reinterpret_cast<u32x4a2*>(p));
     } else {
       const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -89,10 +98,11 @@ struct Chunk<float> {
     lo = make_float4(v[0], v[1], v[2], v[3]);
     hi = make_float4(v[4], v[5], v[6], v[7]);
   }
+  template <bool NT = false>
   __device__ __forceinline__ void store(float* p, int64_t n) const {
     if (n >= 8) {
-      reinterpret_cast<f32x4a4*>(p)[0] = f32x4a4{lo.x, lo.y, lo.z, lo.w};
-      reinterpret_cast<f32x4a4*>(p)[1] = f32x4a4{hi.x, hi.y, hi.z, hi.w};
+      put<NT>(f32x4a4{lo.x, lo.y, lo.z, lo.w}, reinterpret_cast<f32x4a4*>(p));
+      put<NT>(f32x4a4{hi.x, hi.y, hi.z, hi.w}, reinterpret_cast<f32x4a4*>(p) + 1);
     } else {
       if (n > 0) p[0] = lo.x;
       if (n > 1) p[1] = lo.y;

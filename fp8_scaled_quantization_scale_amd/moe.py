@@ -17,16 +17,15 @@ from typing import NamedTuple
 
 import torch
 
-from . import (COL, GEMM_MX_1x32, GROUP_CONTRACT, GROUP_ROWS,
-               IDX_I32, IDX_I64, IN_BF16, IN_FP32, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _ceil, _check,
-               _is_matrix, _is_vector, _ld, _matrix, _need, _one_device, _pad16, _scope, _vector, fp8_gemm_grouped, fp8_moe_combine,
-               fp8_moe_combine_backward, fp8_moe_dispatch, fp8_moe_quantize, fp8_moe_rows, fp8_moe_sort,
-               fp8_moe_sort_workspace, load, scale_grid_shape)
+from . import (BLOCK_1x128, COL, GEMM_MX_1x32, GROUP_CONTRACT, GROUP_ROWS, IDX_I32, IDX_I64, IN_BF16, IN_FP32,
+               MX_1x32, MX_1x32_OCP, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _at, _ceil, _check, _here, _is_matrix,
+               _is_vector, _ld, _matrix, _need, _one_device, _pad16, _scope, _vector, load, scale_grid_shape)
 from . import quantize as _quantize_matrix
 
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
 _OUT_DTYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
 _IDX = {torch.int32: IDX_I32, torch.int64: IDX_I64}
+_RECIPES = (BLOCK_1x128, MX_1x32, MX_1x32_OCP)
 _CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
 
@@ -63,17 +62,19 @@ def sort(expert: torch.Tensor, experts: int, stream=None) -> Plan:
     tokens, topk = expert.shape
     if topk < 1:
         raise Fp8Error("expert needs at least one choice per token")
-    rows = fp8_moe_rows(tokens, topk, experts)
+    lib = load()
+    rows = lib.fp8_moe_rows(tokens, topk, experts)
     if rows < 0:
         _check(rows, "fp8_moe_rows")
-    size = fp8_moe_sort_workspace(tokens, topk, experts)
+    size = lib.fp8_moe_sort_workspace(tokens, topk, experts)
     dev, i32 = expert.device, torch.int32
     with _scope(dev, stream):
         offsets, counts = torch.empty(experts + 1, dtype=i32, device=dev), torch.empty(experts, dtype=i32, device=dev)
         row_slot, slot_row = torch.empty(rows, dtype=i32, device=dev), torch.empty(tokens, topk, dtype=i32, device=dev)
         ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-        st = fp8_moe_sort(expert, _IDX[expert.dtype], tokens, topk, _ld(expert), experts, offsets, counts, row_slot,
-                          rows, slot_row, ws, size)
+        st = lib.fp8_moe_sort(expert.data_ptr(), _IDX[expert.dtype], tokens, topk, _ld(expert), experts,
+                              offsets.data_ptr(), counts.data_ptr(), row_slot.data_ptr(), rows, slot_row.data_ptr(),
+                              _at(ws), size, _here(dev))
     _check(st, "fp8_moe_sort")
     return tuple.__new__(Plan, (tokens, topk, experts, rows, offsets, counts, row_slot, slot_row))
 
@@ -105,8 +106,9 @@ def _dispatch(x, plan, weights, stream):
     cols = x.shape[1]
     with _scope(x.device, stream):
         y = torch.empty(plan.rows, cols, dtype=x.dtype, device=x.device)
-        st = fp8_moe_dispatch(x, _DTYPES[x.dtype], plan.tokens, cols, _ld(x), plan.topk, weights, plan.slot_row,
-                              plan.offsets, plan.counts, plan.experts, y, plan.rows, cols)
+        st = load().fp8_moe_dispatch(x.data_ptr(), _DTYPES[x.dtype], plan.tokens, cols, _ld(x), plan.topk, _at(weights),
+                                     plan.slot_row.data_ptr(), plan.offsets.data_ptr(), plan.counts.data_ptr(),
+                                     plan.experts, y.data_ptr(), plan.rows, cols, _here(x.device))
     _check(st, "fp8_moe_dispatch")
     return y
 
@@ -118,8 +120,8 @@ def _combine(ys, plan, weights, stream):
     cols = ys.shape[1]
     with _scope(ys.device, stream):
         y = torch.empty(plan.tokens, cols, dtype=ys.dtype, device=ys.device)
-        st = fp8_moe_combine(ys, _DTYPES[ys.dtype], plan.rows, cols, _ld(ys), plan.slot_row, plan.tokens, plan.topk,
-                             weights, y, cols)
+        st = load().fp8_moe_combine(ys.data_ptr(), _DTYPES[ys.dtype], plan.rows, cols, _ld(ys), plan.slot_row.data_ptr(),
+                                    plan.tokens, plan.topk, _at(weights), y.data_ptr(), cols, _here(ys.device))
     _check(st, "fp8_moe_combine")
     return y
 
@@ -140,9 +142,11 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor | None, plan: Plan, weig
     with _scope(dev, stream):
         dys = torch.empty(plan.rows, cols, dtype=dy.dtype, device=dev) if rows else None
         dw = torch.empty(plan.tokens, plan.topk, dtype=torch.float32, device=dev) if dots else None
-        st = fp8_moe_combine_backward(dy, _DTYPES[dy.dtype], plan.tokens, cols, _ld(dy), ys if dots else None,
-                                      _ld(ys) if dots else 0, plan.slot_row, plan.offsets, plan.counts, plan.experts,
-                                      plan.topk, weights, dys, plan.rows, cols, dw)
+        st = load().fp8_moe_combine_backward(dy.data_ptr(), _DTYPES[dy.dtype], plan.tokens, cols, _ld(dy),
+                                             ys.data_ptr() if dots else None, _ld(ys) if dots else 0,
+                                             plan.slot_row.data_ptr(), plan.offsets.data_ptr(), plan.counts.data_ptr(),
+                                             plan.experts, plan.topk, _at(weights), _at(dys), plan.rows, cols, _at(dw),
+                                             _here(dev))
     _check(st, "fp8_moe_combine_backward")
     return dys, dw
 
@@ -218,6 +222,8 @@ def quantize(x: torch.Tensor, plan: Plan, recipe: int, fmt: int, orient: int = R
     if nonfinite is not None:
         _vector("nonfinite", nonfinite, torch.int32, 1)
     _one_device(x, plan.offsets, weights, nonfinite)
+    if recipe not in _RECIPES:
+        raise Fp8Error("experts take the recipes BLOCK_1x128, MX_1x32 and MX_1x32_OCP: other scales would span experts")
     rows, cols, dev = plan.rows, x.shape[1], x.device
     out = Quantized(fmt=fmt, recipe=recipe, nonfinite=nonfinite)
     ld_r, ld_c = _pad16(cols), _pad16(rows)
@@ -225,14 +231,16 @@ def quantize(x: torch.Tensor, plan: Plan, recipe: int, fmt: int, orient: int = R
         if orient & ROW:
             out.q_row = torch.empty(rows, ld_r, dtype=torch.uint8, device=dev)
             shp, dt = scale_grid_shape(recipe, rows, cols, ROW)
-            out.s_row = torch.empty(shp, dtype=dt, device=dev) if shp is not None else None
+            out.s_row = torch.empty(shp, dtype=dt, device=dev)
         if orient & COL:
             out.q_col = torch.empty(cols, ld_c, dtype=torch.uint8, device=dev)
             shp, dt = scale_grid_shape(recipe, rows, cols, COL)
-            out.s_col = torch.empty(shp, dtype=dt, device=dev) if shp is not None else None
-        st = fp8_moe_quantize(x, _DTYPES[x.dtype], x.shape[0], cols, _ld(x), plan.row_slot if gather else None,
-                              plan.topk, weights, plan.offsets, plan.experts, rows, recipe, fmt, orient, margin,
-                              out.q_row, ld_r, out.s_row, out.q_col, ld_c, out.s_col, nonfinite)
+            out.s_col = torch.empty(shp, dtype=dt, device=dev)
+        st = load().fp8_moe_quantize(x.data_ptr(), _DTYPES[x.dtype], x.shape[0], cols, _ld(x),
+                                     plan.row_slot.data_ptr() if gather else None, plan.topk, _at(weights),
+                                     plan.offsets.data_ptr(), plan.experts, rows, recipe, fmt, orient, margin,
+                                     _at(out.q_row), ld_r, _at(out.s_row), _at(out.q_col), ld_c, _at(out.s_col),
+                                     _at(nonfinite), _here(dev))
     _check(st, "fp8_moe_quantize")
     return out
 
@@ -287,11 +295,12 @@ def gemm(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, fmt_b:
     _one_device(a, offsets, s_a, b, s_b, c)
     with _scope(a.device, stream):
         c = _out_of(c, (rows, n), out_dtype, a.device)
-        st = fp8_gemm_grouped(a, fmt_a, s_a, _ld(a), b, fmt_b, s_b, b.stride(1) if n > 1 else max(b.stride(1), k),
-                              b.stride(0) if experts > 1 else 0,
-                              s_b.stride(1) if grid[1] > 1 else max(s_b.stride(1), grid[2]),
-                              s_b.stride(0) if experts > 1 else 0, recipe, GROUP_ROWS, offsets, experts, rows, 0, n, k,
-                              c, _OUT_DTYPES[c.dtype], _ld(c), 0)
+        st = load().fp8_gemm_grouped(a.data_ptr(), fmt_a, s_a.data_ptr(), _ld(a), b.data_ptr(), fmt_b, s_b.data_ptr(),
+                                     b.stride(1) if n > 1 else max(b.stride(1), k), b.stride(0) if experts > 1 else 0,
+                                     s_b.stride(1) if grid[1] > 1 else max(s_b.stride(1), grid[2]),
+                                     s_b.stride(0) if experts > 1 else 0, recipe, GROUP_ROWS, offsets.data_ptr(),
+                                     experts, rows, 0, n, k, c.data_ptr(), _OUT_DTYPES[c.dtype], _ld(c), 0,
+                                     _here(a.device))
     _check(st, "fp8_gemm_grouped")
     return c
 
@@ -321,8 +330,9 @@ def gemm_wgrad(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, 
         ldc = c.stride(1) if m > 1 else max(c.stride(1), n)
         if experts > 1 and m * n > 0 and c.stride(0) < (m - 1) * ldc + n:
             raise Fp8Error("c's experts must not overlap")
-        st = fp8_gemm_grouped(a, fmt_a, s_a, _ld(a), b, fmt_b, s_b, _ld(b), 0, 0, 0, recipe, GROUP_CONTRACT, offsets,
-                              experts, rows, m, n, 0, c, _OUT_DTYPES[c.dtype], ldc, c.stride(0))
+        st = load().fp8_gemm_grouped(a.data_ptr(), fmt_a, s_a.data_ptr(), _ld(a), b.data_ptr(), fmt_b, s_b.data_ptr(),
+                                     _ld(b), 0, 0, 0, recipe, GROUP_CONTRACT, offsets.data_ptr(), experts, rows, m, n,
+                                     0, c.data_ptr(), _OUT_DTYPES[c.dtype], ldc, c.stride(0), _here(a.device))
     _check(st, "fp8_gemm_grouped")
     return c
 

@@ -9,8 +9,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (IN_BF16, IN_FP32, Fp8Error, _check, _is_matrix, _is_vector, _ld, _matrix, _one_device, _scope, _vector,
-               fp8_layer_norm_backward, fp8_layer_norm_forward, fp8_layer_norm_workspace)
+from . import (IN_BF16, IN_FP32, Fp8Error, _at, _check, _here, _is_matrix, _is_vector, _ld, _matrix, _one_device,
+               _scope, _vector, load)
 
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
 
@@ -53,8 +53,9 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, bias
         y = torch.empty(rows, cols, dtype=x.dtype, device=dev)
         mean = torch.empty(rows, dtype=torch.float32, device=dev)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        st = fp8_layer_norm_forward(x, _DTYPES[x.dtype], rows, cols, _ld(x), weight, bias, _DTYPES[w_dtype], eps, y,
-                                    cols, mean, rstd)
+        st = load().fp8_layer_norm_forward(x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x), _at(weight), _at(bias),
+                                           _DTYPES[w_dtype], eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
+                                           _here(dev))
     _check(st, "fp8_layer_norm_forward")
     return y, mean, rstd
 
@@ -81,12 +82,13 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor 
         size = 0
         if params:
             dw, db = torch.empty(cols, dtype=w_dtype, device=dev), torch.empty(cols, dtype=w_dtype, device=dev)
-            size = fp8_layer_norm_workspace(rows, cols)
+            size = load().fp8_layer_norm_workspace(rows, cols)
             if size < 0:
                 _check(size, "fp8_layer_norm_workspace")
             ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        st = fp8_layer_norm_backward(dy, _ld(dy), x, _DTYPES[x.dtype], rows, cols, _ld(x), weight, _DTYPES[w_dtype],
-                                     mean, rstd, dx, cols, dw, db, ws, size)
+        st = load().fp8_layer_norm_backward(dy.data_ptr(), _ld(dy), x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x),
+                                            _at(weight), _DTYPES[w_dtype], mean.data_ptr(), rstd.data_ptr(),
+                                            dx.data_ptr(), cols, _at(dw), _at(db), _at(ws), size, _here(dev))
     _check(st, "fp8_layer_norm_backward")
     return dx, dw, db
 
