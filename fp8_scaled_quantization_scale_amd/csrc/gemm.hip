@@ -207,6 +207,16 @@ struct GroupArgs : GArgs {
   int64_t stride_sb;       // scale entries from one expert's B scales to the next one's
   int nkb_b;               // scale entries from one row (or 128-row tile) of B to the next
   int64_t stride_c;        // elements from one expert's C to the next one's
+  // kGrpRows: column tiles 2 n and 2 n + 1 start their K loop kSG n steps in
+  // and wrap around (where K is whole groups of kSG steps).  The workgroups of
+  // an XCD then ask for different parts of B's rows at a time instead of the
+  // same 128 bytes of thousands of rows, which lie on few memory channels when
+  // the rows are a large power of two apart (64 experts' transposed codes, 128
+  // KB: 4096 x 2048 each, 16384 rows MX 304 -> 225 us; 128 rows to 4 of 64 203
+  // -> 157 us; rows 4 KB apart, 16384 x 14336 x 4096: 883 us either way; 8 x
+  // 4096 x 16384, 8192 rows 650 -> 628 us).  By every column tile rather than
+  // every second, A tiles were shared less: 893 us on the third of these.
+  int turn;
 };
 
 // What each recipe stages per K step.
@@ -331,6 +341,14 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     const int K = GRP == kGrpContract ? s1 - s0 : p.K;
     const int rows_a = min(kBM, m_end - m0), rows_b = min(kBN, p.N - n0);
     const int KT = (K + kBK - 1) / kBK;
+    // kGrpRows: the step of K that loop step kt works on (see GroupArgs::turn)
+    int rot = 0;
+    if constexpr (GRP == kGrpRows) rot = p.turn ? (pn >> 1) * kSG % KT : 0;
+    auto step_of = [&](int kt) __attribute__((always_inline)) -> int {
+      if constexpr (GRP != kGrpRows) return kt;
+      const int k = kt + rot;
+      return k >= KT ? k - KT : k;
+    };
     // grouped: bytes before the operands' K windows, the expert's B and its
     // scales; scale entries between two rows of A and of B.  The ranges end
     // with the last row's window, so that no read leaves the operands however
@@ -402,7 +420,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     // addresses and keep them in private memory)
     auto dma_tile = [&](int seg, int kt, bool is_a, __amdgpu_buffer_rsrc_t rs, int stride, auto Tail, int i)
         __attribute__((always_inline)) {
-      const int k0 = kt * kBK;
+      const int k0 = step_of(kt) * kBK;
       // the segment's offset: from the registers set above, or the lane's
       // base plus the wave-uniform row offset 8 s ld (formed on the scalar
       // unit; ld passes through an empty asm so that it is formed at each
@@ -434,12 +452,13 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
       uint32_t sb = __builtin_amdgcn_readfirstlane(scl_base + ((kt / kSG) & 1) * kSclBytes);
       asm volatile("" : "+s"(sb));
       const int nkb = a_side ? p.nkb : nkb_b, mis = a_side ? 0 : sb_mis;
+      const int ks = step_of(kt);
       auto first = [&](int row) -> uint32_t {  // aligned start of a row's group window
-        return S::kMx ? ((((uint32_t)(mis + row * nkb)) & ~3u) + 4u * kt) : (uint32_t)((row * nkb + kt) * 4);
+        return S::kMx ? ((((uint32_t)(mis + row * nkb)) & ~3u) + 4u * ks) : (uint32_t)((row * nkb + ks) * 4);
       };
       if (a_side) {
         if constexpr (S::kTileA) {
-          if (q == 0) dma16(rs, sb + kSclALo + 1024 * grp, lane == 0 ? (uint32_t)((grp * p.nkb + kt) * 4) : kOOB, 0);
+          if (q == 0) dma16(rs, sb + kSclALo + 1024 * grp, lane == 0 ? (uint32_t)((grp * p.nkb + ks) * 4) : kOOB, 0);
         } else {
           if (q < 2) dma16(rs, sb + kSclALo + 16 * (128 * grp + 64 * q), first(128 * grp + 64 * q + lane), 0);
           if constexpr (S::kMx)
@@ -447,7 +466,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
         }
       } else {
         if constexpr (S::kTileB) {
-          if (q == 0) dma16(rs, sb + kSclBLo, lane < 2 ? (uint32_t)((lane * nkb_b + kt) * 4) : kOOB, 0);
+          if (q == 0) dma16(rs, sb + kSclBLo, lane < 2 ? (uint32_t)((lane * nkb_b + ks) * 4) : kOOB, 0);
         } else {
           dma16(rs, sb + kSclBLo + 16 * 64 * q, first(64 * q + lane), 0);
           if constexpr (S::kMx) dma4(rs, sb + kSclBHi + 4 * 64 * q, first(64 * q + lane) + 16u);
@@ -472,7 +491,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
       }
     };
     auto issue = [&](int kt) __attribute__((always_inline)) {
-      if (kt * kBK + kBK <= K) issue_set(kt, std::false_type{});
+      if (step_of(kt) * kBK + kBK <= K) issue_set(kt, std::false_type{});
       else issue_set(kt, std::true_type{});
     };
 
@@ -620,8 +639,9 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
       // MX: blocks past K (last step only) take byte 0, 2^-127, times their
       // zero codes, whatever E8M0 bytes follow a row's last
       if constexpr (S::kMx) {
-        if (nblk - 4 * kt < 4) {
-          const bool in_k = lg < nblk - 4 * kt;
+        const int left = nblk - 4 * step_of(kt);
+        if (left < 4) {
+          const bool in_k = lg < left;
 #pragma unroll
           for (int i = 0; i < kMT; ++i) sax[i] = in_k ? sax[i] : 0;
 #pragma unroll
@@ -862,6 +882,7 @@ hipError_t launch_grouped4(const GroupedGemmParams& g, hipStream_t st) {
   a.stride_sb = g.stride_sb;
   a.stride_c = g.stride_c;
   a.c = g.c;
+  a.turn = GRP == kGrpRows && g.K > 0 && g.K % (kSG * kBK) == 0;
   a.tiles_m = (int)((g.M + kBM - 1) / kBM);
   a.tiles_n = (int)((g.N + kBN - 1) / kBN);
   const int64_t tiles =

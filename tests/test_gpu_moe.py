@@ -296,6 +296,27 @@ def test_gemm_rows(tokens, topk, experts, n, k, kind, mx, fa, fb, out):
             _check_product(c[lo:hi], _values(a[lo:hi], fa, s_a[lo:hi], mx), _values(b[-1], fb, s_b[-1], mx, not mx))
 
 
+@pytest.mark.parametrize("tokens,topk,experts,n,k", [(300, 2, 3, 1300, 1024), (900, 1, 2, 2100, 512), (130, 2, 5, 1030, 2048)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_gemm_rows_of_whole_step_groups(tokens, topk, experts, n, k, mx):
+    """K a multiple of 512: the column tiles start at different steps of K, so
+    the sums are in another order than fp8_gemm_scaled's; the same in two calls."""
+    need_gpu()
+    p = moe.sort(_routing(tokens, topk, experts, 47)[0], experts)
+    off = host(p.offsets)
+    per = 32 if mx else 128
+    kb, nb = k // per, n if mx else -(-n // 128)
+    a, b = _codes((p.rows, k), fm.E5M2, 1), _codes((experts, n, k), fm.E4M3, 2)
+    s_a, s_b = _scales((p.rows, kb), mx, 3), _scales((experts, nb, kb), mx, 4)
+    recipe = fm.GEMM_MX_1x32 if mx else fm.GEMM_BLOCK_1x128_128x128
+    c = moe.gemm(a, fm.E5M2, s_a, b, fm.E4M3, s_b, recipe, p.offsets, F)
+    assert torch.equal(c[:off[-1]], moe.gemm(a, fm.E5M2, s_a, b, fm.E4M3, s_b, recipe, p.offsets, F)[:off[-1]])
+    for e in range(experts):
+        lo, hi = off[e], off[e + 1]
+        if lo < hi:
+            _check_product(c[lo:hi], _values(a[lo:hi], fm.E5M2, s_a[lo:hi], mx), _values(b[e], fm.E4M3, s_b[e], mx, not mx))
+
+
 def _values(codes, fmt, scales, mx, tiles=False):
     v = codes.view(fm.TORCH_FP8[fmt]).float().double()
     s = 2.0 ** (scales.double() - 127) if mx else scales.double()
