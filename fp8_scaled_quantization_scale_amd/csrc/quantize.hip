@@ -1212,9 +1212,10 @@ hipError_t launch_moe_bf16(const MoeTileArgs& a, int64_t tiles, hipStream_t st) 
 
 template <typename InT, int FMT, int MODE, bool ROW, bool COL>
 hipError_t launch_moe_orient(const MoeTileArgs& a, int64_t tiles, hipStream_t st) {
-  // FP32 rows, and BF16 rows that end inside a tile, take the general kernel
+  // FP32 rows, BF16 rows that end inside a tile, and codes so far apart that
+  // 15 rows of them pass 32 bits take the general kernel
   if constexpr (sizeof(InT) == 2) {
-    if (a.cols % kTile == 0)
+    if (a.cols % kTile == 0 && (!ROW || a.ld_q_row <= (1 << 28)))
       return a.weights ? launch_moe_bf16<FMT, MODE, ROW, COL, true>(a, tiles, st)
                        : launch_moe_bf16<FMT, MODE, ROW, COL, false>(a, tiles, st);
   }

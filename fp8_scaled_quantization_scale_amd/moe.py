@@ -16,15 +16,17 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (BLOCK_1x128, COL, GEMM_MX_1x32, GROUP_CONTRACT, GROUP_ROWS, IDX_I32, IDX_I64, IN_BF16, IN_FP32,
-               MX_1x32, MX_1x32_OCP, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _at, _ceil, _check, _here, _is_matrix,
+               MAX_EXPERTS, MX_1x32, MX_1x32_OCP, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _at, _ceil, _check, _here, _is_matrix,
                _is_vector, _ld, _matrix, _need, _one_device, _pad16, _scope, _vector, load, scale_grid_shape)
 from . import quantize as _quantize_matrix
 
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
 _OUT_DTYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
 _IDX = {torch.int32: IDX_I32, torch.int64: IDX_I64}
+_MOST_LD = 1 << 22  # leading dimension of a product's operands
 _RECIPES = (BLOCK_1x128, MX_1x32, MX_1x32_OCP)
 _CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
@@ -62,7 +64,7 @@ def sort(expert: torch.Tensor, experts: int, stream=None) -> Plan:
     tokens, topk = expert.shape
     if topk < 1:
         raise Fp8Error("expert needs at least one choice per token")
-    lib = load()
+    lib = load()  # (raises if the library is not built)
     rows = lib.fp8_moe_rows(tokens, topk, experts)
     if rows < 0:
         _check(rows, "fp8_moe_rows")
@@ -163,6 +165,7 @@ class _DispatchFn(torch.autograd.Function):
         return _dispatch(x, plan, weights, None)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weights = ctx.saved_tensors
         dy, dx, dw = _row_major(dy), None, None
@@ -181,6 +184,7 @@ class _CombineFn(torch.autograd.Function):
         return _combine(ys, plan, weights, None)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         ys, weights = ctx.saved_tensors
         dys, dw = combine_backward(_row_major(dy), ys, ctx.plan, weights, ctx.needs_input_grad[0],
@@ -363,6 +367,7 @@ class _GroupedLinearFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         qxt, sxt, qwt, swt = ctx.saved_tensors
         p, mplan, (e, n, k), (need_dx, need_dw) = ctx.p, ctx.mplan, ctx.shape, ctx.need
@@ -393,13 +398,17 @@ class GroupedLinear(torch.nn.Module):
     zeros in a segment's rows without a slot (as dispatch, combine's gradient
     and this layer itself leave them); ``gather=True`` takes x [tokens x
     in_features] and dispatches it as it is cast.  in_features and out_features
-    are multiples of 128, so that no block holds two experts' weights."""
+    are multiples of 128, so that no block holds two experts' weights; experts *
+    out_features is at most 4194304, and so are plan.rows where the weight needs
+    a gradient (the leading dimensions that the products take)."""
 
     def __init__(self, experts: int, in_features: int, out_features: int, recipe=None, device=None,
                  dtype=torch.bfloat16):
         super().__init__()
         if experts < 1 or in_features < 128 or out_features < 128 or in_features % 128 or out_features % 128:
             raise Fp8Error("experts must be positive, in_features and out_features multiples of 128")
+        if experts > MAX_EXPERTS or experts * out_features > _MOST_LD or in_features > _MOST_LD:
+            raise Fp8Error(f"at most {MAX_EXPERTS} experts, and at most {_MOST_LD} features in all")
         self.experts, self.in_features, self.out_features, self.recipe = experts, in_features, out_features, recipe
         self.weight = torch.nn.Parameter(torch.empty(experts, out_features, in_features, device=device, dtype=dtype))
         torch.nn.init.uniform_(self.weight, -in_features ** -0.5, in_features ** -0.5)
@@ -421,7 +430,8 @@ class GroupedLinear(torch.nn.Module):
             raise Fp8Error(f"the plan has {plan.experts} experts, the layer {self.experts}")
         if x.dtype not in _DTYPES or self.weight.dtype not in _DTYPES:
             raise Fp8Error("inputs and weights are BF16 or FP32")
-        load()
         grad = torch.is_grad_enabled()
+        if grad and self.weight.requires_grad and plan.rows > _MOST_LD:
+            raise Fp8Error(f"the weight's gradient takes at most {_MOST_LD} sorted rows; the plan has {plan.rows}")
         return _GroupedLinearFn.apply(x.contiguous(), self.weight.contiguous(), plan, p, gather,
                                       grad and x.requires_grad, grad and self.weight.requires_grad)

@@ -8,6 +8,7 @@ statistics and sums.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (IN_BF16, IN_FP32, Fp8Error, _at, _check, _here, _is_matrix, _is_vector, _ld, _matrix, _one_device,
                _scope, _vector, load)
@@ -25,18 +26,14 @@ def _check_x(x) -> None:
 def _params(cols: int, weight, bias):
     """dtype of the parameters (FP32 where there are none)."""
     dtype = None
-    for name, t in (("weight", weight), ("bias", bias)):
+    for t in (weight, bias):
         if t is None:
             continue
-        if not (isinstance(t, torch.Tensor) and t.dtype in _DTYPES):
-            raise Fp8Error(f"{name} must be a BF16 or FP32 device tensor")
-        if dtype is not None and t.dtype != dtype:
-            raise Fp8Error("weight and bias must have one dtype")
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _DTYPES and t.is_contiguous()):
+            raise Fp8Error("weight and bias must be contiguous BF16 or FP32 device tensors")
+        if t.dim() != 1 or t.numel() != cols or t.dtype != (dtype or t.dtype):
+            raise Fp8Error(f"weight and bias must have one dtype and {cols} elements each")
         dtype = t.dtype
-        if t.dim() != 1 or t.numel() != cols:
-            raise Fp8Error(f"{name} is {tuple(t.shape)}; needs ({cols},)")
-        if not _is_vector(t, dtype, cols):
-            _vector(name, t, dtype, cols)
     return dtype or torch.float32
 
 
@@ -102,6 +99,7 @@ class _LayerNormFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         if dy.dtype != x.dtype or dy.stride(-1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):

@@ -317,6 +317,25 @@ def test_gemm_rows_of_whole_step_groups(tokens, topk, experts, n, k, mx):
             _check_product(c[lo:hi], _values(a[lo:hi], fm.E5M2, s_a[lo:hi], mx), _values(b[e], fm.E4M3, s_b[e], mx, not mx))
 
 
+def test_gemm_of_nothing_is_zero():
+    """K = 0 writes zeros to the segments' rows; no rows, nothing."""
+    need_gpu()
+    p = moe.sort(_routing(100, 1, 2, 5)[0], 2)
+    end = int(p.offsets[-1])
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    c = torch.full((p.rows, 40), 7.0, device="cuda")
+    moe.gemm(torch.empty(p.rows, 0, **u8), 0, torch.empty(p.rows, 0, device="cuda"), torch.empty(2, 40, 0, **u8), 0,
+             torch.empty(2, 1, 0, device="cuda"), fm.GEMM_BLOCK_1x128_128x128, p.offsets, c=c)
+    assert not c[:end].any() and (c[end:] == 7).all()
+    p = moe.sort(torch.empty(0, 2, dtype=torch.int64, device="cuda"), 3)
+    q = moe.quantize(torch.empty(0, 128, dtype=B, device="cuda"), p, fm.BLOCK_1x128, fm.E4M3, fm.ROW_AND_COL)
+    y = moe.gemm(q.q_row, 0, q.s_row, torch.zeros(3, 64, 128, **u8), 0, torch.ones(3, 1, 1, device="cuda"),
+                 fm.GEMM_BLOCK_1x128_128x128, p.offsets)
+    assert y.shape == (0, 64) and moe.combine(y, p).shape == (0, 64)
+    g = moe.gemm_wgrad(q.q_col[:, :0], 0, q.s_col, q.q_col[:, :0], 0, q.s_col, fm.GEMM_BLOCK_1x128_1x128, p.offsets)
+    assert g.shape == (3, 128, 128) and not g.any()
+
+
 def _values(codes, fmt, scales, mx, tiles=False):
     v = codes.view(fm.TORCH_FP8[fmt]).float().double()
     s = 2.0 ** (scales.double() - 127) if mx else scales.double()
@@ -483,6 +502,20 @@ def test_run_of_the_operators_captured_and_replayed():
         assert all(t.isfinite().all() for t in want)
 
 
+def test_no_second_derivative():
+    """The backward passes are kernels of their own: asking for their gradient
+    raises instead of giving none."""
+    need_gpu()
+    e, w = _routing(40, 2, 3, 1)
+    p = moe.sort(e, 3)
+    x = torch.randn(40, 128, device="cuda", requires_grad=True)
+    ln = norm.LayerNorm(128, device="cuda", dtype=F)
+    for f in (lambda: moe.dispatch(x, p), lambda: moe.combine(moe.dispatch(x, p), p, w), lambda: ln(x)):
+        g, = torch.autograd.grad(f().square().sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.sum().backward()
+
+
 def test_side_stream():
     """On a stream of its own, as an argument and as the current one."""
     need_gpu()
@@ -500,6 +533,46 @@ def test_side_stream():
         s.synchronize()
         assert torch.equal(got, want) and torch.equal(q.row_slot, p.row_slot)
         assert torch.equal(y, norm.layer_norm_forward(x)[0])
+
+
+def test_offsets_past_32_bits():
+    """Sorted buffers of more than 4 GiB: the last expert's rows lie behind 2^32
+    bytes of codes, rows and products."""
+    need_gpu()
+    tokens, topk, experts, cols, n = 66000, 8, 3, 8192, 256
+    e = torch.full((tokens, topk), 1, device="cuda")
+    e[-100:] = 2
+    e[0] = 0
+    p = moe.sort(e, experts)
+    last = int(p.offsets[2])
+    assert last * cols > 1 << 32
+    x = torch.randn(tokens, cols, generator=_gen(1), device="cuda").bfloat16()
+    w = torch.rand(tokens, topk, generator=_gen(2), device="cuda")
+    src = x[-100:].repeat_interleave(topk, 0)  # the last segment's rows
+    q = moe.quantize(x, p, fm.BLOCK_1x128, fm.E4M3, fm.ROW_AND_COL)
+    want = fm.quantize(src, fm.BLOCK_1x128, fm.E4M3, fm.ROW)
+    assert torch.equal(q.q_row[last:last + 800], want.q_row) and torch.equal(q.s_row[last:last + 800], want.s_row)
+    pad = torch.nn.functional.pad(src, (0, 0, 0, 96))
+    want = fm.quantize(pad, fm.BLOCK_1x128, fm.E4M3, fm.COL)
+    assert torch.equal(q.q_col[:, last:last + 896], want.q_col)
+    assert torch.equal(q.s_col[:, last // 128:last // 128 + 7], want.s_col)
+    wq = fm.quantize(torch.randn(experts * n, cols, generator=_gen(3), device="cuda"), fm.BLOCK_128x128, fm.E4M3)
+    b, s_b = wq.q_row.view(experts, n, cols), wq.s_row.view(experts, 2, -1)
+    c = moe.gemm(q.q_row, fm.E4M3, q.s_row, b, fm.E4M3, s_b, fm.GEMM_BLOCK_1x128_128x128, p.offsets)
+    for rows in (slice(last, last + 800), slice(last - 256, last)):
+        a = _values(q.q_row[rows], fm.E4M3, q.s_row[rows], False)
+        _check_product(c[rows], a, _values(b[2 if rows.start == last else 1], fm.E4M3, s_b[2 if rows.start == last else 1], False, True))
+    del q, wq, b, s_b, c
+    xs = moe.dispatch(x, p)
+    assert torch.equal(xs[last:last + 800], src) and torch.equal(xs[:topk], x[:1].expand(topk, -1))
+    y = moe.combine(xs, p, w)
+    ref = src.view(100, topk, cols).double() * w[-100:].double()[..., None]
+    _within(y[-100:], ref.sum(1), (topk + 2) * E32 * ref.abs().sum(1), "combine")
+    dys, dw = moe.combine_backward(x, xs, p, w)
+    ref = (src.double() * w[-100:].reshape(-1, 1).double())
+    _within(dys[last:last + 800], ref, E32 * ref.abs(), "dys")
+    dots = x[-100:].double().square()
+    _within(dw[-100:], dots.sum(1, keepdim=True).expand(-1, topk), (cols + 2) * E32 * dots.sum(1, keepdim=True), "dweights")
 
 
 def test_refusals():
@@ -530,6 +603,7 @@ def test_refusals():
                 lambda: moe.gemm(a, 0, sa, b, 0, sb, fm.GEMM_BLOCK_1x128_1x128, p.offsets),
                 lambda: moe.gemm_wgrad(a.t().contiguous(), 0, sa, a.t().contiguous(), 0, sa, rec, p.offsets),
                 lambda: moe.gemm_wgrad(a.t(), 0, sa, a.t(), 0, sa, fm.GEMM_BLOCK_1x128_1x128, p.offsets),
+                lambda: moe.GroupedLinear(256, 128, 1 << 15), lambda: moe.GroupedLinear(1025, 128, 128),
                 lambda: layer(xs, p), lambda: moe.GroupedLinear(4, 100, 128), lambda: moe.GroupedLinear(0, 128, 128),
                 lambda: moe.GroupedLinear(3, 128, 128, linear.Float8BlockScaling(), device="cuda")(xs, p),
                 lambda: moe.GroupedLinear(4, 128, 128, linear.Float8CurrentScaling(), device="cuda")(xs, p),

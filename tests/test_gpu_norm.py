@@ -195,6 +195,29 @@ def test_gradient_against_differences():
         assert abs(slope - (grad.double() * d).sum()) <= 1e-5 * (grad.double() * d).abs().sum() + 1e-8
 
 
+def test_offsets_past_32_bits():
+    """x, y, dy and dx of more than 4 GiB each; the last rows and the sums over all."""
+    need_gpu()
+    rows, cols = 540000, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(rows, cols, generator=g, device="cuda", dtype=B)
+    w, b = torch.rand(cols, generator=g, device="cuda") + 0.5, torch.rand(cols, generator=g, device="cuda")
+    y, mean, rstd = norm.layer_norm_forward(x, w, b)
+    few, m, r = norm.layer_norm_forward(x[-3:].clone(), w, b)
+    assert torch.equal(y[-3:], few) and torch.equal(mean[-3:], m) and torch.equal(rstd[-3:], r)
+    dy = y
+    dx, dw, db = norm.layer_norm_backward(dy, x, w, mean, rstd)
+    few, _, _ = norm.layer_norm_backward(dy[-3:].clone(), x[-3:].clone(), w, m, r)
+    assert torch.equal(dx[-3:], few)
+    sdb, adb, sdw, adw = (torch.zeros(cols, dtype=torch.float64, device="cuda") for _ in range(4))
+    for i in range(0, rows, 60000):
+        d = dy[i:i + 60000].double()
+        t = d * (x[i:i + 60000].double() - mean[i:i + 60000, None].double()) * rstd[i:i + 60000, None].double()
+        sdb, adb, sdw, adw = sdb + d.sum(0), adb + d.abs().sum(0), sdw + t.sum(0), adw + t.abs().sum(0)
+    _within(db, sdb, (rows + 8) * E32 * adb, "dbias")
+    _within(dw, sdw, (rows + 8) * E32 * 3 * adw, "dweight")
+
+
 def test_refusals():
     need_gpu()
     x, w, b, dy = _inputs(8, 64, 64, B, F)
