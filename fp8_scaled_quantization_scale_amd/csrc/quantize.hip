@@ -684,15 +684,18 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(std::conditional_t
 // instructions per element than HBM leaves time for (16384 x 8192 to 4 of 64
 // experts, both orientations: 573 us; the bytes of each row read and of the
 // codes take 415, and 255 if each token came from HBM once).  This one is built
-// for few, and takes 446 us (weighted 461): a workgroup stays on its 128 rows
-// for `chunk` tiles, so that source rows, weights and addresses are worked out
+// for few, and takes 416 us (weighted 431, ROW alone 247, COL alone 293), 640
+// VALU instructions per wave and tile: a workgroup stays on its 128 rows for
+// `chunk` tiles, so that source rows, weights and addresses are worked out
 // once; maxima are taken on packed halves, across a row's 16 lanes with DPP,
 // and the column pass keeps its 64 elements packed until they are scaled.  The
 // tile in flight is not held in registers: three workgroups per CU cover its
 // latency better than two that prefetch (522 us against 573 in the kernel
-// above).  Units run along a row tile's columns, then down; column-major and
-// per-XCD ranges of row tiles were slower for both orientations together (459
-// and 449 us), though the column codes alone liked the former (274, now 294).
+// above).  It is bound by what it moves; the ROW scales leave in pieces of a
+// whole chunk, 32 bytes instead of 4 (444 us, ROW alone 313 without).  Units
+// run along a row tile's columns, then down; column-major and per-XCD ranges of
+// row tiles were slower for both orientations together (by 3% and 1%), though
+// the column codes alone liked the former (274).
 // ---------------------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
@@ -727,12 +730,18 @@ __device__ __forceinline__ void unrolled(F&& f) {
   }
 }
 
+typedef unsigned int u32x4a4_t __attribute__((ext_vector_type(4), aligned(4)));
+constexpr int kMaxChunk = 8;  // tiles a workgroup stays on its rows for, at most
+
 template <int FMT, int MODE, bool ROW, bool COL, bool WGT>
 __global__ __launch_bounds__(kThreads, 3) void moe_tile_kernel(MoeTileArgs a, int chunk) {
   constexpr bool kMx = MODE == MODE_MX32 || MODE == MODE_MX32F;
   __shared__ __attribute__((aligned(16))) uint32_t tile[COL ? kTile * kTile / 2 + kTile * 4 : 4];  // rows, then codes
   __shared__ uint32_t colred[COL && !kMx ? 4 : 1][kTile / 2];
   __shared__ int2 rowinfo[kTile];
+  // ROW scales of the unit's tiles, a word per tile (1x128: the scale; MX: the
+  // four blocks' bytes): they leave as whole 32-byte pieces of a row of scales
+  __shared__ __attribute__((aligned(16))) uint32_t rowscl[ROW ? kTile : 1][kMaxChunk];
   const int tid = threadIdx.x, g = tid >> 4, li = tid & 15;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
   const int tiles_x = (int)(a.cols / kTile), chunks = (tiles_x + chunk - 1) / chunk;
@@ -813,19 +822,17 @@ __global__ __launch_bounds__(kThreads, 3) void moe_tile_kernel(MoeTileArgs a, in
           sj = scale_from_amax<FMT>(am, a.margin);
           bad = __any(!is_finite(am));
           if (li < 8) {
-            reinterpret_cast<float*>(a.s_row)[(row0 + g + 16 * li) * tiles_x + bx] = recip_rn(sj);
+            rowscl[g + 16 * li][bx - part * chunk] = __builtin_bit_cast(uint32_t, recip_rn(sj));
             if (bad && !is_finite(am) && a.nonfinite) atomicAdd(a.nonfinite, 1);
           }
         } else {
-          const int64_t gc = (a.cols + 31) / 32;
-          uint8_t* sr = reinterpret_cast<uint8_t*>(a.s_row) + (row0 + g) * gc + (col0 + 8 * li) / 32;
           bool odd = false;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             key[i] = (uint32_t)mx_byte<MODE, FMT>(key_to_float(key[i]));
             odd = odd || key[i] == 0xFF;
             if ((li & 3) == 0) {
-              sr[16 * i * gc] = (uint8_t)key[i];
+              reinterpret_cast<uint8_t*>(&rowscl[g + 16 * i][bx - part * chunk])[li >> 2] = (uint8_t)key[i];
               if (key[i] == 0xFF && a.nonfinite) atomicAdd(a.nonfinite, 1);
             }
           }
@@ -956,6 +963,18 @@ __global__ __launch_bounds__(kThreads, 3) void moe_tile_kernel(MoeTileArgs a, in
         for (int k = 0; k < 4; ++k)
           *reinterpret_cast<uint4*>(q + 32 * k * a.ld_q_col) =
               *reinterpret_cast<const uint4*>(ct + (c + 32 * k) * kCodeStride + 16 * m);
+      }
+    }
+    if constexpr (ROW) {
+      __syncthreads();
+      // (a row of scales has tiles_x words in both recipes)
+      const int r = tid >> 1, j0 = 4 * (tid & 1), left = bx_end - part * chunk - j0;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.s_row) + (row0 + r) * tiles_x + part * chunk + j0;
+      if (left >= 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&rowscl[r][j0]);
+        *reinterpret_cast<u32x4a4_t*>(dst) = u32x4a4_t{v.x, v.y, v.z, v.w};
+      } else {
+        for (int j = 0; j < left; ++j) dst[j] = rowscl[r][j0 + j];
       }
     }
   }
@@ -1200,10 +1219,9 @@ hipError_t launch_moe_bf16(const MoeTileArgs& a, int64_t tiles, hipStream_t st) 
     occupancy.store(per_cu, std::memory_order_relaxed);
   }
   const int64_t most = (int64_t)cu_count(stream_device(st)) * per_cu;
-  // tiles a workgroup stays on its rows for: at most 8, fewer where that
-  // would leave compute units without work
+  // fewer tiles per unit where 8 would leave compute units without work
   int64_t chunk = tiles / (2 * most);
-  chunk = chunk < 1 ? 1 : (chunk > 8 ? 8 : chunk);
+  chunk = chunk < 1 ? 1 : (chunk > kMaxChunk ? kMaxChunk : chunk);
   const int64_t units = (tiles + chunk - 1) / chunk;
   const int64_t grid = units < most ? units : most;
   k<<<(unsigned)grid, kThreads, 0, st>>>(a, (int)chunk);
