@@ -22,7 +22,9 @@ namespace {
 // counts into first rows, and every wave then walks its part in order, 64
 // slots at a time: equal experts among the 64 lanes find each other with one
 // ballot per bit of the number.  No atomic decides an order: those on LDS
-// only count.
+// only count.  Bound by latency: 256 slots over 8 experts 4.1 us (one launch),
+// 65536 over 64 in 4.9 + 6.2 us (13.5 for the second with the ranges' counts
+// added up by one thread per expert and the experts read twice).
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortRange = 2048;   // slots per workgroup, until there would be
@@ -197,7 +199,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_rows_kernel(SortArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows to and from the sorted buffer.  All three are bound by memory; a wave
+// Rows to and from the sorted buffer.  All three are bound by memory (16384 x
+// 8192 to 4 experts each: dispatch 286 us, 4.9 TB/s; combine 237 us, 5.7 TB/s;
+// the gradient of 4095 x 4096 to 8: 117 us, 4.8 TB/s and 33 MB of pads); a wave
 // works on one token's (or one pad row's) piece of 64 chunks x kPiece, so the
 // token's row numbers and weights are the same for all its lanes.
 //
