@@ -321,13 +321,19 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
 }
 
 // out[row(t, j)] = w_tj dy[t] (if out), dweights_tj = <dy[t], ys[row(t, j)]>
-// (if dweights): a workgroup per token, so that each dot product ends inside it.
-template <typename T>
-__global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a) {
-  if ((int64_t)blockIdx.x >= a.tokens) return zero_pads<T>(a, (int)(blockIdx.x - a.tokens));
+// (if dweights): NT threads per token, so that each dot product ends inside a
+// wave (NT 64) or a workgroup.  Up to kWaveCols columns a wave: a workgroup would
+// be mostly idle (8192 tokens, 512 columns to 2: 13 us against 77; 1024 to 8: 60
+// against 109; 2048 to 4: 74 against 100; but 4095 x 4096 to 8: 139 against 120).
+constexpr int kWaveCols = 2048;
+template <typename T, int NT>
+__global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a, int64_t token_blocks) {
+  if ((int64_t)blockIdx.x >= token_blocks) return zero_pads<T>(a, (int)(blockIdx.x - token_blocks));
   constexpr int kAtOnce = 8;
   __shared__ float red[kRowWaves][kAtOnce];
-  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x % NT;
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / NT) + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  if (t >= a.tokens) return;  // (whole waves; a workgroup of one token has it)
   const T* dy = static_cast<const T*>(a.token_rows) + t * a.ld_token;
   for (int j0 = 0; j0 < a.topk; j0 += kAtOnce) {
     float dot[kAtOnce];
@@ -343,7 +349,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
       if (row[q] >= a.rows) row[q] = -1;
       w[q] = a.weights && j0 + q < a.topk ? a.weights[slot] : 1.0f;
     }
-    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kRowThreads * 8) {
+    for (int64_t c = tid * 8; c < a.cols; c += NT * 8) {
       Chunk<T> k, y[kAtOnce];  // all on their way together
       float g[8];
       k.load(dy + c, a.cols - c);
@@ -378,15 +384,21 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
         }
       }
     }
-    if (a.dweights) {
-      __syncthreads();  // red is read below before the next group's sums
+    if (!a.dweights) continue;
 #pragma unroll
-      for (int q = 0; q < kAtOnce; ++q) {
-        dot[q] = wave_sum(dot[q]);
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][q] = dot[q];
+    for (int q = 0; q < kAtOnce; ++q) dot[q] = wave_sum(dot[q]);
+    if constexpr (NT == 64) {
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        if (tid == 0 && j0 + q < a.topk) a.dweights[t * a.topk + j0 + q] = dot[q];
+    } else {
+      __syncthreads();  // red is read below before the next group's sums
+      if ((tid & 63) == 0) {
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) red[tid >> 6][q] = dot[q];
       }
       __syncthreads();
-      const int q = threadIdx.x;
+      const int q = tid;
       if (q < kAtOnce && j0 + q < a.topk) {
         float s = 0.0f;
 #pragma unroll
@@ -484,9 +496,15 @@ hipError_t launch_moe_combine(const MoeRowsParams& p, hipStream_t st) {
 
 hipError_t launch_moe_combine_backward(const MoeRowsParams& p, hipStream_t st) {
   const RowArgs a = args_of(p);
-  const unsigned grid = (unsigned)(p.tokens + (p.out ? p.experts : 0));
-  if (p.dtype == kInBf16) combine_backward_kernel<uint16_t><<<grid, kRowThreads, 0, st>>>(a);
-  else combine_backward_kernel<float><<<grid, kRowThreads, 0, st>>>(a);
+  const bool wave = p.cols <= kWaveCols;
+  const int64_t blocks = wave ? (p.tokens + kRowWaves - 1) / kRowWaves : p.tokens;
+  const unsigned grid = (unsigned)(blocks + (p.out ? p.experts : 0));
+  if (p.dtype == kInBf16)
+    wave ? combine_backward_kernel<uint16_t, 64><<<grid, kRowThreads, 0, st>>>(a, blocks)
+         : combine_backward_kernel<uint16_t, kRowThreads><<<grid, kRowThreads, 0, st>>>(a, blocks);
+  else
+    wave ? combine_backward_kernel<float, 64><<<grid, kRowThreads, 0, st>>>(a, blocks)
+         : combine_backward_kernel<float, kRowThreads><<<grid, kRowThreads, 0, st>>>(a, blocks);
   return hipGetLastError();
 }
 
