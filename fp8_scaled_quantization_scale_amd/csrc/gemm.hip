@@ -194,8 +194,7 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (
 // hold slots (68 row tiles in 15 rounds; one 16384-row product, 64 row tiles in
 // 14 rounds: 797 us); its weight gradient 1155 us, 1.66 PFLOP/s (28 tiles of 8
 // to 45 steps per workgroup; one product with K = 16384: 1006 us).  With few
-// rows per expert it streams the weights: 128 rows to 4 of 64 experts, 4096 x
-// 2048 each, 157 us, 3.4 TB/s.
+// rows per expert it streams the weights, in 128 x 128 tiles (gemm_few_kernel).
 constexpr int kGrpNone = 0, kGrpRows = 1, kGrpContract = 2;
 
 struct GArgs {
@@ -220,11 +219,12 @@ struct GroupArgs : GArgs {
   // and wrap around (where K is whole groups of kSG steps).  The workgroups of
   // an XCD then ask for different parts of B's rows at a time instead of the
   // same 128 bytes of thousands of rows, which lie on few memory channels when
-  // the rows are a large power of two apart (64 experts' transposed codes, 128
-  // KB: 4096 x 2048 each, 16384 rows MX 304 -> 225 us; 128 rows to 4 of 64 203
-  // -> 157 us; rows 4 KB apart, 16384 x 14336 x 4096: 883 us either way; 8 x
-  // 4096 x 16384, 8192 rows 650 -> 628 us).  By every column tile rather than
-  // every second, A tiles were shared less: 893 us on the third of these.
+  // the rows are a large power of two apart.  In 256 x 256 tiles: 64 experts'
+  // transposed codes, rows 128 KB apart, 4096 x 2048 each, 16384 rows MX 304 ->
+  // 225 us; 128 rows to 4 of 64 203 -> 157 us; rows 4 KB apart, 16384 x 14336 x
+  // 4096: 883 us either way; 8 x 4096 x 16384, 8192 rows 650 -> 628 us.  By every
+  // column tile rather than every second, A tiles were shared less: 893 us on
+  // the third of these.
   int turn;
 };
 
@@ -819,6 +819,244 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
   }  // tile loop
 }
 
+// ---------------------------------------------------------------------------
+// Grouped rows of few rows per expert: 128 x 128 tiles.
+//
+// There a product streams its weights: C has a row tile or two per expert, and
+// the 256 x 256 kernel spends half of it (or more) on rows that are not there,
+// takes one tile per compute unit, and has at most one K step of one tile on
+// its way.  Here 4 waves compute 128 x 128 (64 x 64 each) from two 32 KB
+// stages, and two workgroups share a compute unit: while one waits for its
+// step or writes its tile, the other multiplies.  One barrier per step: it
+// publishes the step that landed and frees the other stage, whose next step
+// goes out before the products.  Fragments, swizzles, scale windows and the
+// order of every sum are those of the kernel above.
+//
+// Bound by the weights' stream: 128 rows to 4 of 64 experts, 4096 x 2048 each,
+// 136 us, 3.9 TB/s of the 537 MB that its codes hold; 391 rows to 4 of 6, 128 x
+// 4480, MX, 32 us.  launch_grouped4 has the rule between the two and both sides.
+// ---------------------------------------------------------------------------
+constexpr int kFM = 128, kFN = 128, kFThreads = 256;
+constexpr int kFStage = (kFM + kFN) * kBK;
+constexpr int kFMT = 4;  // 16-row sub-tiles of a wave
+// scale window of a row at 16 row, MX: the dword after it at HI + 4 row; B's behind A's
+constexpr int kFSclHi = 2048, kFSclB = 2560, kFScl = 2 * kFSclB;
+
+template <int FA, int FB, int REC, int OUT>
+__global__ __launch_bounds__(kFThreads, 2) void gemm_few_kernel(GroupArgs p) {
+  constexpr bool kMx = REC == kGemmMx;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kFStage];
+  __shared__ __attribute__((aligned(16))) uint8_t sscl[2 * kFScl];
+  __shared__ int seg_at[kMaxExperts + 1];
+  const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_void*)smem;
+  const uint32_t scl_base = (uint32_t)(uintptr_t)(lds_void*)sscl;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int q = __builtin_amdgcn_readfirstlane(tid >> 6), wm = q >> 1, wn = q & 1;
+  const int lr = lane & 15, lg = lane >> 4;
+  const int arow = wm * 64 + lr, brow0 = wn * 64 + (lr >> 2) * kCPL + (lr & 3);
+  const int swa = swz_a(arow), swb = swz_b(brow0);
+  const uint32_t fa_lo = (uint32_t)(arow * kBK + ((lg ^ swa) << 4));
+  const uint32_t fa_hi = (uint32_t)(arow * kBK + (((4 + lg) ^ swa) << 4));
+  const uint32_t fb_lo = (uint32_t)(kFM * kBK + brow0 * kBK + ((lg ^ swb) << 4));
+  const uint32_t fb_hi = (uint32_t)(kFM * kBK + brow0 * kBK + (((4 + lg) ^ swb) << 4));
+
+  for (int e = tid; e <= p.experts; e += kFThreads) seg_at[e] = min(max(p.offsets[e], 0), p.R) & ~127;
+  __syncthreads();
+  // a segment that would begin before an earlier one ends begins there: row
+  // tiles are numbered through, whatever the array holds
+  if (q == 0) {
+    int top = 0;
+    for (int e0 = 0; e0 <= p.experts; e0 += 64) {
+      const int e = e0 + lane;
+      int v = e <= p.experts ? seg_at[e] : 0;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(v, off, 64);
+        if (lane >= off) v = max(v, o);
+      }
+      v = max(v, top);
+      if (e <= p.experts) seg_at[e] = v;
+      top = __shfl(v, 63, 64);
+    }
+  }
+  __syncthreads();
+  const int tiles_n = (p.N + kFN - 1) / kFN;
+  const int total = __builtin_amdgcn_readfirstlane(seg_at[p.experts]) / kFM * tiles_n;
+  const int KT = (p.K + kBK - 1) / kBK;
+
+#pragma unroll 1
+  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    __syncthreads();  // every wave is done with the tile before
+    const int pid = (tile & 7) * (total >> 3) + min(tile & 7, total & 7) + (tile >> 3);
+    // the expert: segments whose tiles all come before (the last one's end after)
+    int ex = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 64) {
+      const int e = e0 + lane;
+      ex += __popcll(__ballot(e < p.experts && seg_at[min(e, p.experts - 1) + 1] / kFM * tiles_n <= pid));
+    }
+    const int s0 = __builtin_amdgcn_readfirstlane(seg_at[ex]), s1 = __builtin_amdgcn_readfirstlane(seg_at[ex + 1]);
+    const int local = max(pid - s0 / kFM * tiles_n, 0), blocks = max((s1 - s0) / kFM, 1);
+    const int pm = local % blocks, pn = local / blocks;  // an expert's row tiles share B in turn
+    const int m0 = s0 + pm * kFM, n0 = pn * kFN;
+    const int rows_b = min(kFN, p.N - n0);
+    const int rot = p.turn ? (pn >> 1) * kSG % KT : 0;
+    auto step_of = [&](int kt) __attribute__((always_inline)) -> int {
+      const int k = kt + rot;
+      return k >= KT ? k - KT : k;
+    };
+    const int64_t sb_at = ex * p.stride_sb + (int64_t)(kMx ? n0 : n0 / 128) * p.nkb_b;
+    const int sb_mis = kMx ? (int)(sb_at & 3) : 0;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (int64_t)m0 * p.lda, (uint32_t)((kFM - 1) * p.lda + p.K));
+    const __amdgpu_buffer_rsrc_t rb =
+        make_rsrc(p.b + ex * p.stride_b + (int64_t)n0 * p.ldb, (uint32_t)((rows_b - 1) * p.ldb + p.K));
+    __amdgpu_buffer_rsrc_t rsa, rsb;
+    if constexpr (kMx) {
+      rsa = make_rsrc(static_cast<const uint8_t*>(p.sa) + (int64_t)m0 * p.nkb, (uint32_t)((kFM * p.nkb + 3) & ~3));
+      rsb = make_rsrc(static_cast<const uint8_t*>(p.sb) + sb_at - sb_mis,
+                      (uint32_t)((sb_mis + (rows_b - 1) * p.nkb_b + p.nkb + 3) & ~3));
+    } else {
+      rsa = make_rsrc(static_cast<const uint32_t*>(p.sa) + (int64_t)m0 * p.nkb, (uint32_t)(kFM * p.nkb * 4));
+      rsb = make_rsrc(static_cast<const uint32_t*>(p.sb) + sb_at, (uint32_t)(p.nkb * 4));
+    }
+
+    // step kt: wave q brings segments 4 q .. 4 q + 3 (8 rows each) of A and of
+    // B, and with the first step of each group of kSG the group's scales
+    auto issue = [&](int kt) __attribute__((always_inline)) {
+      const int ks = step_of(kt), k0 = ks * kBK;
+      const uint32_t lb = lds_base + (uint32_t)((kt & 1) * kFStage);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int seg = 4 * q + i, ca = 16 * ((lane & 7) ^ (lane >> 3));
+        uint32_t vo = (uint32_t)((8 * seg + (lane >> 3)) * (int)p.lda + ca);
+        if (k0 + ca >= p.K) vo = kOOB;
+        dma16(ra, lb + seg * 1024, vo, (uint32_t)k0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int seg = 4 * q + i, cb = 16 * ((lane & 7) ^ (((lane >> 3) & 3) | ((seg & 2) << 1)));
+        uint32_t vo = (uint32_t)((8 * seg + (lane >> 3)) * (int)p.ldb + cb);
+        if (k0 + cb >= p.K) vo = kOOB;
+        dma16(rb, lb + kFM * kBK + seg * 1024, vo, (uint32_t)k0);
+      }
+      if (kt % kSG) return;
+      const uint32_t sb = scl_base + (uint32_t)(((kt / kSG) & 1) * kFScl);
+      const int row = 64 * (q & 1) + lane;
+      if constexpr (kMx) {
+        const uint32_t wa = (uint32_t)(row * p.nkb & ~3) + 4u * ks, wb = (uint32_t)((sb_mis + row * p.nkb_b) & ~3) + 4u * ks;
+        if (q < 2) {
+          dma16(rsa, sb + 16 * 64 * q, wa, 0);
+          dma16(rsb, sb + kFSclB + 16 * 64 * q, row < rows_b ? wb : kOOB, 0);
+        } else {
+          dma4(rsa, sb + kFSclHi + 4 * 64 * (q - 2), wa + 16u);
+          dma4(rsb, sb + kFSclB + kFSclHi + 4 * 64 * (q - 2), row < rows_b ? wb + 16u : kOOB);
+        }
+      } else {
+        if (q < 2) dma16(rsa, sb + 16 * 64 * q, (uint32_t)((row * p.nkb + ks) * 4), 0);
+        else if (q == 2) dma16(rsb, sb + kFSclB, lane == 0 ? (uint32_t)(ks * 4) : kOOB, 0);
+      }
+    };
+
+    v4f acc[kFMT][kNT];
+#pragma unroll
+    for (int i = 0; i < kFMT; ++i)
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto frag = [&](uint32_t lo_addr, uint32_t hi_addr) __attribute__((always_inline)) -> v8i {
+      const uint4 lo = lds_u4(lo_addr), hi = lds_u4(hi_addr);
+      return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+
+    if (KT > 0) issue(0);
+#pragma unroll 1
+    for (int kt = 0; kt < KT; ++kt) {
+      wait_vmcnt<0>();
+      __syncthreads();
+      if (kt + 1 < KT) issue(kt + 1);
+      const uint32_t stage = lds_base + (uint32_t)((kt & 1) * kFStage);
+      const uint32_t sc = scl_base + (uint32_t)(((kt / kSG) & 1) * kFScl);
+      v8i fb[kNT];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) fb[j] = frag(stage + fb_lo + 4 * j * kBK, stage + fb_hi + 4 * j * kBK);
+      if constexpr (kMx) {
+        const int left = p.nkb - 4 * step_of(kt);  // K blocks from this step on; lanes past them take 2^-127 x 0
+        auto byte_of = [&](int base, int row, int mis, int nkb) __attribute__((always_inline)) -> int {
+          const int b = ((mis + (lr & 3) * nkb) & 3) + lg + 4 * (kt % kSG);
+          const uint32_t at = sc + (uint32_t)(base + (b < 16 ? 16 * row + b : kFSclHi + 4 * row + b - 16));
+          return lg < left ? lds_u8(at) : 0;
+        };
+        int sbx[kNT];
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) sbx[j] = byte_of(kFSclB, brow0 + 4 * j, sb_mis, p.nkb_b);
+#pragma unroll
+        for (int i = 0; i < kFMT; ++i) {
+          const v8i fa = frag(stage + fa_lo + 16 * i * kBK, stage + fa_hi + 16 * i * kBK);
+          const int sax = byte_of(0, arow + 16 * i, 0, p.nkb);
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) acc[i][j] = mfma_mx<FB, FA>(fb[j], fa, acc[i][j], sbx[j], sax);
+        }
+      } else {
+        const float stile = lds_f32(sc + kFSclB + 4 * (kt % kSG));
+#pragma unroll
+        for (int i = 0; i < kFMT; ++i) {
+          const v8i fa = frag(stage + fa_lo + 16 * i * kBK, stage + fa_hi + 16 * i * kBK);
+          const float s = lds_f32(sc + 16 * (arow + 16 * i) + 4 * (kt % kSG)) * stile;
+          v4f part[kNT];
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) part[j] = mfma<FB, FA>(fb[j], fa, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[j][r], s, acc[i][j][r]);
+        }
+      }
+      wait_lgkm0();  // done reading the stage that the next step but one takes
+    }
+
+    constexpr int ESIZE = OUT == kOutBf16 ? 2 : 4;
+    const bool vec_ok = ((p.ldc * ESIZE) % 16 == 0) && ((reinterpret_cast<uintptr_t>(p.c) & 15) == 0);
+    const int cbase = n0 + wn * 64 + lg * kCPL;
+#pragma unroll
+    for (int i = 0; i < kFMT; ++i) {
+      const int64_t row = m0 + wm * 64 + i * 16 + lr;
+      float v[kCPL];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[4 * j + r] = acc[i][j][r];
+      if constexpr (OUT == kOutBf16) {
+        __bf16* dst = reinterpret_cast<__bf16*>(p.c) + row * p.ldc + cbase;
+        if (vec_ok && cbase + kCPL <= p.N) {
+#pragma unroll
+          for (int qq = 0; qq < kCPL / 8; ++qq) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __bf16 lo = (__bf16)v[8 * qq + 2 * e], hi = (__bf16)v[8 * qq + 2 * e + 1];
+              w[e] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+            }
+            reinterpret_cast<uint4*>(dst)[qq] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCPL; ++c)
+            if (cbase + c < p.N) dst[c] = (__bf16)v[c];
+        }
+      } else {
+        float* dst = reinterpret_cast<float*>(p.c) + row * p.ldc + cbase;
+        if (vec_ok && cbase + kCPL <= p.N) {
+#pragma unroll
+          for (int qq = 0; qq < kCPL / 4; ++qq)
+            reinterpret_cast<float4*>(dst)[qq] = make_float4(v[4 * qq], v[4 * qq + 1], v[4 * qq + 2], v[4 * qq + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCPL; ++c)
+            if (cbase + c < p.N) dst[c] = v[c];
+        }
+      }
+    }
+  }
+}
+
 template <int FA, int FB, int REC, int OUT>
 hipError_t launch4(const GemmParams& g, hipStream_t st) {
   GArgs a;
@@ -894,6 +1132,23 @@ hipError_t launch_grouped4(const GroupedGemmParams& g, hipStream_t st) {
   a.turn = GRP == kGrpRows && g.K > 0 && g.K % (kSG * kBK) == 0;
   a.tiles_m = (int)((g.M + kBM - 1) / kBM);
   a.tiles_n = (int)((g.N + kBN - 1) / kBN);
+  if constexpr (GRP == kGrpRows) {
+    // 128 x 128 tiles where they all run at once, where the experts have 256
+    // rows each at most, and where C is no wider than one of them.  256 x 256
+    // -> 128 x 128 in us; one round: 128 rows to 2 of 8 experts, 256 x 512,
+    // 11.5 -> 7.0; 1000 to 2 of 2, 2048 x 4096, 48 -> 29; 1024 to 2 of 8,
+    // 2048 x 2048, 29 -> 22.  Few rows: 128 to 4 of 64, 4096 x 2048, 159 -> 136;
+    // 1000 to 8 of 128, 2048 x 2048, 170 -> 146; 8192 to 1 of 64, 4096 x 4096,
+    // 304 -> 301.  Narrow: 9010 to 6 of 6, 16 x 2592, 48 -> 33.  Beyond them the
+    // small tiles lose: 2048 to 2 of 8, 4096 x 4096, 105 -> 116; 12288 to 1 of
+    // 64, the same, 354 -> 360; 8192 to 2 of 8, 16384 x 4096, 871 -> 1151.
+    const int64_t few = g.R / kFM * ((g.N + kFN - 1) / kFN), room = 2 * (int64_t)cu_count(stream_device(st));
+    if (few <= room || g.R <= 256 * g.experts || g.N <= kFN) {
+      const unsigned blocks = (unsigned)((few < room ? few : room) + 7) / 8 * 8;
+      gemm_few_kernel<FA, FB, REC, OUT><<<blocks, kFThreads, 0, st>>>(a);
+      return hipGetLastError();
+    }
+  }
   const int64_t tiles =
       GRP == kGrpRows ? (g.R / kBM + g.experts) * a.tiles_n : (int64_t)a.tiles_m * a.tiles_n * g.experts;
   const int64_t cus = cu_count(stream_device(st));

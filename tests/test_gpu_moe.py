@@ -317,6 +317,49 @@ def test_gemm_rows_of_whole_step_groups(tokens, topk, experts, n, k, mx):
             _check_product(c[lo:hi], _values(a[lo:hi], fm.E5M2, s_a[lo:hi], mx), _values(b[e], fm.E4M3, s_b[e], mx, not mx))
 
 
+@pytest.mark.parametrize("tokens,topk,experts,n,k", [(4500, 2, 4, 2100, 400), (2600, 2, 3, 2180, 1024), (5000, 1, 2, 1700, 130 * 16)])
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("fa,fb,out", [(fm.E4M3, fm.E4M3, B), (fm.E5M2, fm.E4M3, F)])
+def test_gemm_rows_of_many_tiles(tokens, topk, experts, n, k, mx, fa, fb, out):
+    """More than 256 rows per expert and more tiles than run at once: the large
+    tiles, in which segments end halfway."""
+    need_gpu()
+    p = moe.sort(_routing(tokens, topk, experts, 53)[0], experts)
+    off = host(p.offsets)
+    per = 32 if mx else 128
+    kb, nb = -(-k // per), n if mx else -(-n // 128)
+    a, b = _codes((p.rows, k), fa, 1), _codes((experts, n, k), fb, 2)
+    s_a, s_b = _scales((p.rows, kb), mx, 3), _scales((experts, nb, kb), mx, 4)
+    recipe = fm.GEMM_MX_1x32 if mx else fm.GEMM_BLOCK_1x128_128x128
+    base = torch.full((p.rows + 128, n), 7.0, dtype=out, device="cuda")
+    c = moe.gemm(a, fa, s_a, b, fb, s_b, recipe, p.offsets, c=base[:p.rows])
+    for e in range(experts):
+        lo, hi = off[e], off[e + 1]
+        if k % 512:
+            want = fm.gemm(a[lo:hi], fa, s_a[lo:hi].contiguous(), b[e], fb, s_b[e].clone(), recipe, k, out)
+            assert torch.equal(c[lo:hi], want), f"expert {e}"
+    _check_product(c[lo:hi], _values(a[lo:hi], fa, s_a[lo:hi], mx), _values(b[-1], fb, s_b[-1], mx, not mx))
+    assert (base[off[-1]:] == 7).all()
+
+
+def test_many_tiles_offsets_outside_the_buffers_are_clamped():
+    """Whatever an offsets array holds, for a product in the large tiles."""
+    need_gpu()
+    rows, n, k, experts = 4096, 2200, 128, 4
+    a, b = _codes((rows, k), fm.E4M3, 1), _codes((experts, n, k), fm.E4M3, 2)
+    s_a, s_b = _scales((rows, 1), False, 3), _scales((experts, 18, 1), False, 4)
+    base = torch.full((rows + 512, n), 7.0, device="cuda")
+    off = torch.tensor([-5, 1601, 1 << 30, 130, 2000000000], dtype=torch.int32, device="cuda")
+    moe.gemm(a, fm.E4M3, s_a, b, fm.E4M3, s_b, fm.GEMM_BLOCK_1x128_128x128, off, c=base[:rows])
+    assert (base[rows:] == 7).all()
+    want = [fm.gemm(a, fm.E4M3, s_a, b[e], fm.E4M3, s_b[e].clone(), fm.GEMM_BLOCK_1x128_128x128, k, F) for e in (0, 1, 3)]
+    assert torch.equal(base[:128], want[0][:128])
+    some = base[:rows] == want[0]
+    for w in want[1:]:
+        some |= base[:rows] == w
+    assert some.all()
+
+
 def test_gemm_of_nothing_is_zero():
     """K = 0 writes zeros to the segments' rows; no rows, nothing."""
     need_gpu()
