@@ -156,17 +156,26 @@ __device__ __forceinline__ int lds_u8(uint32_t addr) {
 // (dword) = buffer[voff + soff].  Inline asm so that the compiler's wait-count
 // pass does not treat it as an LDS store aliasing every later LDS read (which
 // would drain vmcnt before each fragment read); completion is tracked with
-// wait_vmcnt.  The s_nop covers the M0-write -> LDS-DMA wait state.
+// wait_vmcnt.  The s_nop covers the M0-write -> LDS-DMA wait state (WAIT = 0).
+// Inline asm is opaque to the compiler's own hazard handling: where it spills
+// scalars into vector lanes, an operand may have come from a v_readlane right
+// before, which a vector memory instruction may read 5 wait states later at the
+// earliest.  The grouped products spill some: their loads wait that long
+// (kDmaSafe), but for the rows form's operand tiles, whose resources and
+// offsets stay in scalars (waiting there cost 1%).
+constexpr int kDmaSafe = 4;
+template <int WAIT = 0>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+  asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
-               : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_addr)
+               : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_addr), "n"(WAIT)
                : "memory");
 }
+template <int WAIT = 0>
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_addr, uint32_t voff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+  asm volatile("s_nop %3\n\tbuffer_load_dword %0, %1, 0 offen lds"
                :
-               : "v"(voff), "s"(rsrc), "{m0}"(lds_addr)
+               : "v"(voff), "s"(rsrc), "{m0}"(lds_addr), "n"(WAIT)
                : "memory");
 }
 
@@ -192,7 +201,7 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (
 // about 8 us, which shorter K loops feel more: 16384 rows over 8 experts,
 // 14336 x 4096 each, 1x128 x 128x128: 890 us, 2.16 PFLOP/s of the rows that
 // hold slots (68 row tiles in 15 rounds; one 16384-row product, 64 row tiles in
-// 14 rounds: 797 us); its weight gradient 1155 us, 1.66 PFLOP/s (28 tiles of 8
+// 14 rounds: 797 us); its weight gradient 1130 us, 1.70 PFLOP/s (28 tiles of 8
 // to 45 steps per workgroup; one product with K = 16384: 1006 us).  With few
 // rows per expert it streams the weights, in 128 x 128 tiles (gemm_few_kernel).
 constexpr int kGrpNone = 0, kGrpRows = 1, kGrpContract = 2;
@@ -303,9 +312,23 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
   int total = p.tiles_m * p.tiles_n;
   if constexpr (GRP == kGrpRows) total = __builtin_amdgcn_readfirstlane(seg_tile[p.experts]);
   if constexpr (GRP == kGrpContract) total *= p.experts;
-#pragma unroll 1
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    __syncthreads();  // every wave is done with the previous tile's LDS
+  // The contraction form runs its tiles in one chain (kChain): the last step's
+  // load phase sends for the next tile's first step, and the two groups stay a
+  // phase apart, so that a tile boundary is the epilogue alone.  Two sets of
+  // variables, then: what the loads on their way go by (ra .. nblk_ld; aim()
+  // sets them to a tile) and what the products and the epilogue do.  Its K
+  // loops are short: 16384 rows over 64 experts, 4096 x 2048 each, 514 -> 441 us
+  // (MX 498 -> 441); 4000 over 128, 2048 x 2048, 380 -> 340; 16384 over 8, 14336
+  // x 4096, 1157 -> 1130.  In the rows form, which has no scalars left for the
+  // second set, every step paid for it: 16384 rows over 8 experts, 14336 x 4096,
+  // 890 -> 928 us; over 64, 4096 x 2048, MX, 227 -> 226.
+  constexpr bool kChain = GRP == kGrpContract;
+  constexpr int kWait = GRP != kGrpNone ? kDmaSafe : 0, kWaitTile = kChain ? kDmaSafe : 0;
+  __amdgpu_buffer_rsrc_t ra = make_rsrc(nullptr, 0), rb = ra, rsa = ra, rsb = ra;
+  int ex_ld = 0, m0_ld = 0, n0_ld = 0, end_ld = 0, K_ld = 0, KT_ld = 0, rot_ld = 0, mis_ld = 0, nblk_ld = 0;
+  int nkb_b = p.nkb;  // grouped: scale entries between two rows of B
+  if constexpr (GRP == kGrpRows) nkb_b = p.nkb_b;
+  auto aim = [&](int tile) __attribute__((always_inline)) {
     // ---- tile assignment: XCD-contiguous ranges of the tile index (tiles t and
     // t + gridDim.x stay on one XCD when gridDim.x % 8 == 0), grouped 8 tile-rows deep
     int pid = tile;
@@ -349,37 +372,33 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     const int m_end = GRP == kGrpRows ? s1 : p.M;  // the tile's rows end here
     const int K = GRP == kGrpContract ? s1 - s0 : p.K;
     const int rows_a = min(kBM, m_end - m0), rows_b = min(kBN, p.N - n0);
-    const int KT = (K + kBK - 1) / kBK;
-    // kGrpRows: the step of K that loop step kt works on (see GroupArgs::turn)
-    int rot = 0;
-    if constexpr (GRP == kGrpRows) rot = p.turn ? (pn >> 1) * kSG % KT : 0;
-    auto step_of = [&](int kt) __attribute__((always_inline)) -> int {
-      if constexpr (GRP != kGrpRows) return kt;
-      const int k = kt + rot;
-      return k >= KT ? k - KT : k;
-    };
+    ex_ld = ex;
+    m0_ld = m0;
+    n0_ld = n0;
+    end_ld = m_end;
+    K_ld = K;
+    KT_ld = (K + kBK - 1) / kBK;
+    // kGrpRows: where the K loop starts (see GroupArgs::turn)
+    if constexpr (GRP == kGrpRows) rot_ld = p.turn ? (pn >> 1) * kSG % KT_ld : 0;
     // grouped: bytes before the operands' K windows, the expert's B and its
-    // scales; scale entries between two rows of A and of B.  The ranges end
-    // with the last row's window, so that no read leaves the operands however
-    // far apart their rows lie.
+    // scales.  The ranges end with the last row's window, so that no read leaves
+    // the operands however far apart their rows lie.
     const int k_at = GRP == kGrpContract ? s0 : 0;
     const uint8_t* b_ex = p.b;
     int64_t sb_ex = 0;
-    int nkb_b = p.nkb;
     if constexpr (GRP == kGrpRows) {
       b_ex += ex * p.stride_b;
       sb_ex = ex * p.stride_sb;
-      nkb_b = p.nkb_b;
     }
     const int nblk = GRP == kGrpContract ? K / (S::kMx ? 32 : 128) : p.nkb;  // scale blocks along K
+    nblk_ld = nblk;
     auto span = [&](int rows, int64_t ld, int64_t n) __attribute__((always_inline)) -> int64_t {
       return GRP == kGrpNone ? rows * ld : (rows - 1) * ld + n;
     };
 
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (int64_t)m0 * p.lda + k_at, (uint32_t)span(rows_a, p.lda, K));
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(b_ex + (int64_t)n0 * p.ldb + k_at, (uint32_t)span(rows_b, p.ldb, K));
+    ra = make_rsrc(p.a + (int64_t)m0 * p.lda + k_at, (uint32_t)span(rows_a, p.lda, K));
+    rb = make_rsrc(b_ex + (int64_t)n0 * p.ldb + k_at, (uint32_t)span(rows_b, p.ldb, K));
     // scale rows of this tile (range-checked: rows past the matrix read as zero)
-    __amdgpu_buffer_rsrc_t rsa = make_rsrc(nullptr, 0), rsb = make_rsrc(nullptr, 0);
     if constexpr (S::kRowA)
       rsa = make_rsrc(static_cast<const uint32_t*>(p.sa) + (int64_t)m0 * p.nkb + k_at / 128,
                       (uint32_t)(span(rows_a, p.nkb, nblk) * 4));
@@ -395,14 +414,41 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     if constexpr (S::kTileB)
       rsb = make_rsrc(static_cast<const uint32_t*>(p.sb) + sb_ex + (int64_t)(n0 / 128) * nkb_b,
                       (uint32_t)(span((rows_b + 127) / 128, nkb_b, nblk) * 4));
-    // (an expert's E8M0 bytes may start inside a dword: sb_mis bytes in)
-    int sb_mis = 0;
+    // (an expert's E8M0 bytes may start inside a dword: mis_ld bytes in)
     if constexpr (S::kMx) {
       const int64_t at = sb_ex + (int64_t)n0 * nkb_b + k_at / 32;
-      if constexpr (GRP == kGrpRows) sb_mis = (int)(at & 3);
-      rsb = make_rsrc(static_cast<const uint8_t*>(p.sb) + at - sb_mis,
-                      (uint32_t)((sb_mis + span(rows_b, nkb_b, nblk) + 3) & ~3));
+      if constexpr (GRP == kGrpRows) mis_ld = (int)(at & 3);
+      rsb = make_rsrc(static_cast<const uint8_t*>(p.sb) + at - mis_ld,
+                      (uint32_t)((mis_ld + span(rows_b, nkb_b, nblk) + 3) & ~3));
     }
+  };
+  // the step of K that loop step kt of the tile being loaded works on
+  auto step_ld = [&](int kt) __attribute__((always_inline)) -> int {
+    if constexpr (GRP != kGrpRows) return kt;
+    const int k = kt + rot_ld;
+    return k >= KT_ld ? k - KT_ld : k;
+  };
+  bool on_way = false;         // the tile's first step was sent for by the tile before
+  int par = 0, par_ld = 0;     // stage of a tile's step kt: (kt + par) & 1
+  int sgp = 0, sgp_ld = 0;     // buffer of its scale group g: (g + sgp) & 1
+
+#pragma unroll 1
+  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    if (!on_way) {
+      __syncthreads();  // every wave is done with the previous tile's LDS
+      aim(tile);
+      par_ld = sgp_ld = 0;
+    }
+    const int ex = ex_ld, m0 = m0_ld, n0 = n0_ld, m_end = end_ld, KT = KT_ld, rot = rot_ld, sb_mis = mis_ld, nblk = nblk_ld;
+    if constexpr (kChain) {
+      par = par_ld;
+      sgp = sgp_ld;
+    }
+    auto step_of = [&](int kt) __attribute__((always_inline)) -> int {
+      if constexpr (GRP != kGrpRows) return kt;
+      const int k = kt + rot;
+      return k >= KT ? k - KT : k;
+    };
 
     // One 1 KB tile segment (8 rows): segments 0..31 are A rows 8s.., 32..63
     // B rows 8(s-32)...  Lane l fetches chunk (l % 8) ^ swizzle of row 8s + l / 8: for an A row
@@ -429,7 +475,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     // addresses and keep them in private memory)
     auto dma_tile = [&](int seg, int kt, bool is_a, __amdgpu_buffer_rsrc_t rs, int stride, auto Tail, int i)
         __attribute__((always_inline)) {
-      const int k0 = step_of(kt) * kBK;
+      const int k0 = step_ld(kt) * kBK;
       // the segment's offset: from the registers set above, or the lane's
       // base plus the wave-uniform row offset 8 s ld (formed on the scalar
       // unit; ld passes through an empty asm so that it is formed at each
@@ -444,11 +490,11 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
         vo = (is_a ? base_a : ((seg & 2) ? base_b1 : base_b0)) + (uint32_t)(8 * (seg & 31)) * ld;
       }
       if constexpr (decltype(Tail)::value) {
-        if (k0 + chunk(is_a, seg) >= K) vo = kOOB;
+        if (k0 + chunk(is_a, seg) >= K_ld) vo = kOOB;
       }
-      uint32_t lb = __builtin_amdgcn_readfirstlane(lds_base + (kt & 1) * kTileBytes);
+      uint32_t lb = __builtin_amdgcn_readfirstlane(lds_base + ((kt + par_ld) & 1) * kTileBytes);
       asm volatile("" : "+s"(lb));
-      dma16(rs, lb + seg * 1024, vo, (uint32_t)k0);
+      dma16<kWaitTile>(rs, lb + seg * 1024, vo, (uint32_t)k0);
     };
     // Scales of the kSG steps from kt on (kt a multiple of kSG) into group
     // buffer (kt / kSG) & 1.  A side, each group its own 128 rows: waves
@@ -458,27 +504,27 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     // after them), or lanes 0 and 1 of wave 0 the two tiles' words.  Lanes
     // with nothing to bring read past the range (zeros) into slack space.
     auto dma_scl = [&](int kt, bool a_side, __amdgpu_buffer_rsrc_t rs) __attribute__((always_inline)) {
-      uint32_t sb = __builtin_amdgcn_readfirstlane(scl_base + ((kt / kSG) & 1) * kSclBytes);
+      uint32_t sb = __builtin_amdgcn_readfirstlane(scl_base + ((kt / kSG + sgp_ld) & 1) * kSclBytes);
       asm volatile("" : "+s"(sb));
-      const int nkb = a_side ? p.nkb : nkb_b, mis = a_side ? 0 : sb_mis;
-      const int ks = step_of(kt);
+      const int nkb = a_side ? p.nkb : nkb_b, mis = a_side ? 0 : mis_ld;
+      const int ks = step_ld(kt);
       auto first = [&](int row) -> uint32_t {  // aligned start of a row's group window
         return S::kMx ? ((((uint32_t)(mis + row * nkb)) & ~3u) + 4u * ks) : (uint32_t)((row * nkb + ks) * 4);
       };
       if (a_side) {
         if constexpr (S::kTileA) {
-          if (q == 0) dma16(rs, sb + kSclALo + 1024 * grp, lane == 0 ? (uint32_t)((grp * p.nkb + ks) * 4) : kOOB, 0);
+          if (q == 0) dma16<kWait>(rs, sb + kSclALo + 1024 * grp, lane == 0 ? (uint32_t)((grp * p.nkb + ks) * 4) : kOOB, 0);
         } else {
-          if (q < 2) dma16(rs, sb + kSclALo + 16 * (128 * grp + 64 * q), first(128 * grp + 64 * q + lane), 0);
+          if (q < 2) dma16<kWait>(rs, sb + kSclALo + 16 * (128 * grp + 64 * q), first(128 * grp + 64 * q + lane), 0);
           if constexpr (S::kMx)
-            if (q >= 2) dma4(rs, sb + kSclAHi + 4 * (128 * grp + 64 * (q - 2)), first(128 * grp + 64 * (q - 2) + lane) + 16u);
+            if (q >= 2) dma4<kWait>(rs, sb + kSclAHi + 4 * (128 * grp + 64 * (q - 2)), first(128 * grp + 64 * (q - 2) + lane) + 16u);
         }
       } else {
         if constexpr (S::kTileB) {
-          if (q == 0) dma16(rs, sb + kSclBLo, lane < 2 ? (uint32_t)((lane * nkb_b + ks) * 4) : kOOB, 0);
+          if (q == 0) dma16<kWait>(rs, sb + kSclBLo, lane < 2 ? (uint32_t)((lane * nkb_b + ks) * 4) : kOOB, 0);
         } else {
-          dma16(rs, sb + kSclBLo + 16 * 64 * q, first(64 * q + lane), 0);
-          if constexpr (S::kMx) dma4(rs, sb + kSclBHi + 4 * 64 * q, first(64 * q + lane) + 16u);
+          dma16<kWait>(rs, sb + kSclBLo + 16 * 64 * q, first(64 * q + lane), 0);
+          if constexpr (S::kMx) dma4<kWait>(rs, sb + kSclBHi + 4 * 64 * q, first(64 * q + lane) + 16u);
         }
       }
     };
@@ -500,7 +546,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
       }
     };
     auto issue = [&](int kt) __attribute__((always_inline)) {
-      if (step_of(kt) * kBK + kBK <= K) issue_set(kt, std::false_type{});
+      if (step_ld(kt) * kBK + kBK <= K_ld) issue_set(kt, std::false_type{});
       else issue_set(kt, std::true_type{});
     };
 
@@ -591,21 +637,21 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     // ---- load phase of step kt: B fragments and B-side scales into
     // registers, then the first A sub-tile of the group's own half
     auto load_phase = [&](int kt) __attribute__((always_inline)) {
-      const uint32_t stage = lds_base + (uint32_t)((kt & 1) * kTileBytes);
+      const uint32_t stage = lds_base + (uint32_t)(((kt + par) & 1) * kTileBytes);
       sa_lo = fa_lo + stage;
       sa_hi = fa_hi + stage;
       sb_lo = fb_lo + stage;
       sb_hi = fb_hi + stage;
       if constexpr (S::kRowA)
-        ssa = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclALo + 16 * arow + 4 * (kt % kSG));
+        ssa = scl_base + (uint32_t)(((kt / kSG + sgp) & 1) * kSclBytes + kSclALo + 16 * arow + 4 * (kt % kSG));
       asm volatile("" : "+v"(sa_lo), "+v"(sa_hi), "+v"(sb_lo), "+v"(sb_hi));
       if constexpr (S::kRowA) asm volatile("" : "+v"(ssa));
 #pragma unroll
       for (int j = 0; j < kNT; ++j) fb[j] = frag(sb_lo + (uint32_t)(4 * j * kBK), sb_hi + (uint32_t)(4 * j * kBK));
-      const uint8_t* sc = &sscl[(kt / kSG) & 1][0];
+      const uint8_t* sc = &sscl[(kt / kSG + sgp) & 1][0];
       const int ks = 4 * (kt % kSG);  // the step's word in a row's 16 bytes
       if constexpr (S::kRowB) {
-        uint32_t ssb = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclBLo + 16 * (wn * kWN + lg * kCPL) + ks);
+        uint32_t ssb = scl_base + (uint32_t)(((kt / kSG + sgp) & 1) * kSclBytes + kSclBLo + 16 * (wn * kWN + lg * kCPL) + ks);
         asm volatile("" : "+v"(ssb));
 #pragma unroll
         for (int j = 0; j < kNT; ++j)
@@ -624,8 +670,8 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
         if (kt % kSG < kSG - 1) {
           // b <= 14: every lane's byte is among its rows' 16 staged bytes,
           // at a constant distance from its first row's
-          uint32_t xa = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclALo + 16 * arow + b);
-          uint32_t xb = scl_base + (uint32_t)(((kt / kSG) & 1) * kSclBytes + kSclBLo + 16 * brow0 + bb);
+          uint32_t xa = scl_base + (uint32_t)(((kt / kSG + sgp) & 1) * kSclBytes + kSclALo + 16 * arow + b);
+          uint32_t xb = scl_base + (uint32_t)(((kt / kSG + sgp) & 1) * kSclBytes + kSclBLo + 16 * brow0 + bb);
           asm volatile("" : "+v"(xa), "+v"(xb));
 #pragma unroll
           for (int i = 0; i < kMT; ++i) sax[i] = lds_u8(xa + (uint32_t)(16 * 16 * i));
@@ -711,8 +757,10 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     };
 
     // ---- prologue: steps 0 and 1 whole, each wave its own DMA set of each
-    if (0 < KT) issue(0);
-    if (1 < KT) issue(1);
+    if (!on_way) {
+      if (0 < KT) issue(0);
+      if (1 < KT) issue(1);
+    }
     // channel scaling: the lane's row and column scales, fetched now so that
     // a short K loop does not end waiting on them
     const int cbase = n0 + wn * kWN + lg * kCPL;  // first of the lane's CPL output columns
@@ -728,8 +776,10 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
         csa[i] = (KT > 0 && row < m_end) ? sap[row] : 0.0f;
       }
     }
-    wait_vmcnt<0>();
-    __syncthreads();
+    if (!on_way) {
+      wait_vmcnt<0>();
+      __syncthreads();
+    }
 
     // Every wave runs L(k); barrier; C(k); barrier for k = 0 .. KT-1; group 1
     // passes one barrier first and group 0 one last, so group 0's L(k) and
@@ -742,11 +792,31 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     // group's A half for its own L(k+1).  Scales go out with the first step
     // of each group of kSG into the group buffer last used kSG to 2 kSG - 1
     // steps before, whose last reads are long done.
-    if (grp == 1) __syncthreads();
+    //
+    // In a chain the next tile's steps count on: its step 0 goes out in this
+    // one's last load phase into the stage and, with its scales, the group
+    // buffer whose turn it is, and group 0's epilogue shares a phase with group
+    // 1's last products and its own next load phase.  A tile without steps is
+    // neither sent for nor sends for the next.
+    if (!on_way && grp == 1) __syncthreads();
+    bool chained = false;
 #pragma unroll 1
     for (int k = 0; k < KT; ++k) {
       promote_tail();
-      if (k >= 1 && k + 1 < KT) issue(k + 1);
+      if constexpr (kChain) {
+        int next = k + 1;
+        bool go = (k >= 1 || on_way) && next < KT;
+        if (next == KT && tile + (int)gridDim.x < total) {
+          aim(tile + (int)gridDim.x);
+          par_ld = (par + KT) & 1;
+          sgp_ld = (sgp + (KT + kSG - 1) / kSG) & 1;
+          next = 0;
+          go = chained = KT_ld > 0;
+        }
+        if (go) issue(next);
+      } else {
+        if (k >= 1 && k + 1 < KT) issue(k + 1);
+      }
       load_phase(k);
       wait_lgkm0();
       __syncthreads();
@@ -815,7 +885,8 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
         }
       }
     }
-    if (grp == 0) __syncthreads();
+    if (!chained && grp == 0) __syncthreads();
+    on_way = chained;
   }  // tile loop
 }
 
@@ -944,15 +1015,15 @@ __global__ __launch_bounds__(kFThreads, 2) void gemm_few_kernel(GroupArgs p) {
       if constexpr (kMx) {
         const uint32_t wa = (uint32_t)(row * p.nkb & ~3) + 4u * ks, wb = (uint32_t)((sb_mis + row * p.nkb_b) & ~3) + 4u * ks;
         if (q < 2) {
-          dma16(rsa, sb + 16 * 64 * q, wa, 0);
-          dma16(rsb, sb + kFSclB + 16 * 64 * q, row < rows_b ? wb : kOOB, 0);
+          dma16<kDmaSafe>(rsa, sb + 16 * 64 * q, wa, 0);
+          dma16<kDmaSafe>(rsb, sb + kFSclB + 16 * 64 * q, row < rows_b ? wb : kOOB, 0);
         } else {
-          dma4(rsa, sb + kFSclHi + 4 * 64 * (q - 2), wa + 16u);
-          dma4(rsb, sb + kFSclB + kFSclHi + 4 * 64 * (q - 2), row < rows_b ? wb + 16u : kOOB);
+          dma4<kDmaSafe>(rsa, sb + kFSclHi + 4 * 64 * (q - 2), wa + 16u);
+          dma4<kDmaSafe>(rsb, sb + kFSclB + kFSclHi + 4 * 64 * (q - 2), row < rows_b ? wb + 16u : kOOB);
         }
       } else {
-        if (q < 2) dma16(rsa, sb + 16 * 64 * q, (uint32_t)((row * p.nkb + ks) * 4), 0);
-        else if (q == 2) dma16(rsb, sb + kFSclB, lane == 0 ? (uint32_t)(ks * 4) : kOOB, 0);
+        if (q < 2) dma16<kDmaSafe>(rsa, sb + 16 * 64 * q, (uint32_t)((row * p.nkb + ks) * 4), 0);
+        else if (q == 2) dma16<kDmaSafe>(rsb, sb + kFSclB, lane == 0 ? (uint32_t)(ks * 4) : kOOB, 0);
       }
     };
 

@@ -425,6 +425,32 @@ def test_gemm_contract(tokens, topk, experts, m, n, kind, mx, fa, fb, out):
             _check_product(c[e], _values(a[:, lo:hi], fa, s_a[:, sl], mx), _values(b[:, lo:hi], fb, s_b[:, sl], mx))
 
 
+@pytest.mark.parametrize("lens", [(1, 0, 9, 2, 0, 0, 5, 1, 1, 4, 0, 8), (1,), (0, 0, 0, 3, 0), (4, 5, 1)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_gemm_contract_of_many_tiles(lens, mx):
+    """Two tiles and more per workgroup, with contractions of every length after
+    each other: none, one step, odd and even numbers, whole groups of four."""
+    need_gpu()
+    m, n, experts = 700, 520, 70
+    seg = [lens[e % len(lens)] * 128 for e in range(experts)]
+    off = np.concatenate([[0], np.cumsum(seg)])
+    rows, per = int(off[-1]), 32 if mx else 128
+    a, b = _codes((m, rows), fm.E5M2, 1), _codes((n, rows), fm.E4M3, 2)
+    s_a, s_b = _scales((m, rows // per), mx, 3), _scales((n, rows // per), mx, 4)
+    recipe = fm.GEMM_MX_1x32 if mx else fm.GEMM_BLOCK_1x128_1x128
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    c = moe.gemm_wgrad(a, fm.E5M2, s_a, b, fm.E4M3, s_b, recipe, offsets, F)
+    for e in range(experts):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            assert not c[e].any()
+            continue
+        sl = slice(lo // per, hi // per)
+        want = fm.gemm(a[:, lo:hi].contiguous(), fm.E5M2, s_a[:, sl].contiguous(), b[:, lo:hi].contiguous(), fm.E4M3,
+                       s_b[:, sl].contiguous(), recipe, hi - lo, F)
+        assert torch.equal(c[e], want), f"expert {e}"
+
+
 def test_offsets_outside_the_buffers_are_clamped():
     """Whatever an offsets array holds, only the buffers' own rows are touched."""
     need_gpu()
