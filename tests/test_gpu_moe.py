@@ -451,6 +451,34 @@ def test_gemm_contract_of_many_tiles(lens, mx):
         assert torch.equal(c[e], want), f"expert {e}"
 
 
+@pytest.mark.parametrize("tokens", [300, 300000])
+def test_products_of_the_most_experts(tokens):
+    """1024 experts, a few slots each and a few hundred: both tile sizes and the
+    contraction, on sampled experts."""
+    need_gpu()
+    experts, n, k = 1024, 130, 16
+    p = moe.sort(_routing(tokens, 1, experts, 91)[0], experts)
+    off = host(p.offsets)
+    a, b = _codes((p.rows, k), fm.E4M3, 1), _codes((experts, n, k), fm.E4M3, 2)
+    s_a, s_b = _scales((p.rows, 1), False, 3), _scales((experts, 2, 1), False, 4)
+    c = moe.gemm(a, fm.E4M3, s_a, b, fm.E4M3, s_b, fm.GEMM_BLOCK_1x128_128x128, p.offsets, F)
+    at, bt = _codes((40, p.rows), fm.E4M3, 5), _codes((24, p.rows), fm.E4M3, 6)
+    s_at, s_bt = _scales((40, p.rows // 128), False, 7), _scales((24, p.rows // 128), False, 8)
+    g = moe.gemm_wgrad(at, fm.E4M3, s_at, bt, fm.E4M3, s_bt, fm.GEMM_BLOCK_1x128_1x128, p.offsets, F)
+    for e in (0, 1, 62, 63, 64, 65, 511, 512, 1000, 1022, 1023):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            assert not g[e].any()
+            continue
+        want = fm.gemm(a[lo:hi], fm.E4M3, s_a[lo:hi].contiguous(), b[e], fm.E4M3, s_b[e].clone(),
+                       fm.GEMM_BLOCK_1x128_128x128, k, F)
+        assert torch.equal(c[lo:hi], want), f"expert {e}"
+        sl = slice(lo // 128, hi // 128)
+        want = fm.gemm(at[:, lo:hi].contiguous(), fm.E4M3, s_at[:, sl].contiguous(), bt[:, lo:hi].contiguous(), fm.E4M3,
+                       s_bt[:, sl].contiguous(), fm.GEMM_BLOCK_1x128_1x128, hi - lo, F)
+        assert torch.equal(g[e], want), f"expert {e}"
+
+
 def test_offsets_outside_the_buffers_are_clamped():
     """Whatever an offsets array holds, only the buffers' own rows are touched."""
     need_gpu()
