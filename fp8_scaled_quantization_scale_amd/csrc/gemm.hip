@@ -901,7 +901,8 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
 // step or writes its tile, the other multiplies.  One barrier per step: it
 // publishes the step that landed and frees the other stage, whose next step
 // goes out before the products.  Fragments, swizzles, scale windows and the
-// order of every sum are those of the kernel above.
+// order of every sum are those of the kernel above, but that the column tiles
+// whose K loops start elsewhere (GroupArgs::turn) are half as wide.
 //
 // Bound by the weights' stream: 128 rows to 4 of 64 experts, 4096 x 2048 each,
 // 136 us, 3.9 TB/s of the 537 MB that its codes hold; 391 rows to 4 of 6, 128 x

@@ -391,10 +391,11 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
  *       stride_b, [N x K] with ldb; its scales s_b + e * stride_sb entries,
  *       rows (of 128x128 tiles: tile rows) ld_sb entries apart; c [rows x N].
  *       recipe GEMM_BLOCK_1x128_128x128 or GEMM_MX_1x32.  M is not used.  Where
- *       K is a multiple of 512 the order of a sum depends on its column (equal
- *       calls give equal bits; fp8_gemm_scaled's may differ in the last).  Rows
- *       without a slot are computed like the others; those behind the last
- *       segment are left as they were.
+ *       K is a multiple of 512 the order of a sum depends on its column and on
+ *       the sizes rows, N and experts (equal calls give equal bits;
+ *       fp8_gemm_scaled's may differ in the last).  Rows without a slot are
+ *       computed like the others; those behind the last segment are left as
+ *       they were.
  *   GROUP_CONTRACT (wgrad): for every expert, C_e = dequant(A[:, segment e]) .
  *       dequant(B[:, segment e])^T, zeros for an empty segment.
  *       a [M x rows], b [N x rows] (the COL outputs of fp8_moe_quantize), s_a
