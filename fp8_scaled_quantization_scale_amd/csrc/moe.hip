@@ -225,6 +225,7 @@ struct RowArgs {
   const void* expert_rows;
   void* out;
   float* dweights;
+  int64_t first;  // piece (combine's gradient: token) that the launch starts at
 };
 
 // Zeros in the rows of the sorted buffer that hold no slot, expert x's.
@@ -243,7 +244,7 @@ template <typename T, bool NT>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a, int64_t token_blocks) {
   if ((int64_t)blockIdx.x >= token_blocks) return zero_pads<T>(a, (int)(blockIdx.x - token_blocks));
   const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t unit = a.first + (int64_t)blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = unit / a.pieces;
   if (t >= a.tokens) return;
   const int64_t c0 = (unit - t * a.pieces) * kPieceCols + lane * 8;
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowArgs a, int64_
 template <typename T, bool NT>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t unit = a.first + (int64_t)blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = unit / a.pieces;
   if (t >= a.tokens) return;
   const int64_t c0 = (unit - t * a.pieces) * kPieceCols + lane * 8;
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowArgs a
   constexpr int kAtOnce = 8;
   __shared__ float red[kRowWaves][kAtOnce];
   const int tid = threadIdx.x % NT;
-  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / NT) + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  const int64_t t = a.first + (int64_t)blockIdx.x * (kRowThreads / NT) + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
   if (t >= a.tokens) return;  // (whole waves; a workgroup of one token has it)
   const T* dy = static_cast<const T*>(a.token_rows) + t * a.ld_token;
   for (int j0 = 0; j0 < a.topk; j0 += kAtOnce) {
@@ -415,7 +416,23 @@ RowArgs args_of(const MoeRowsParams& p) {
                  (int)p.topk,    (int)p.experts, (int)((p.cols + kPieceCols - 1) / kPieceCols),
                  p.offsets,      p.counts,     p.slot_row,
                  p.weights,      p.token_rows, p.expert_rows,
-                 p.out,          p.dweights};
+                 p.out,          p.dweights,   0};
+}
+
+// A launch has its work-items counted modulo 2^32: `groups` workgroups of
+// kRowThreads go out as launches of at most this many, each with the first of
+// its pieces (or tokens), `per` to a workgroup.  launch(args, groups, whether
+// it is the first launch).
+constexpr int64_t kMostGroups = (1LL << 31) / kRowThreads;
+template <typename Launch>
+hipError_t in_parts(RowArgs a, int64_t groups, int per, Launch&& launch) {
+  for (int64_t g = 0; g < groups; g += kMostGroups) {
+    a.first = g * per;
+    launch(a, groups - g < kMostGroups ? groups - g : kMostGroups, g == 0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // whether `rows` rows of output are written past the caches
@@ -468,44 +485,47 @@ hipError_t launch_moe_sort(const MoeSortParams& p, hipStream_t st) {
 }
 
 hipError_t launch_moe_dispatch(const MoeRowsParams& p, hipStream_t st) {
-  const RowArgs a = args_of(p);
-  const int64_t blocks = (p.tokens * a.pieces + kRowWaves - 1) / kRowWaves;
-  const unsigned grid = (unsigned)(blocks + p.experts);
+  const RowArgs all = args_of(p);
   const bool past = past_caches(p.tokens * p.topk, p);
-  if (p.dtype == kInBf16)
-    past ? dispatch_kernel<uint16_t, true><<<grid, kRowThreads, 0, st>>>(a, blocks)
-         : dispatch_kernel<uint16_t, false><<<grid, kRowThreads, 0, st>>>(a, blocks);
-  else
-    past ? dispatch_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a, blocks)
-         : dispatch_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a, blocks);
-  return hipGetLastError();
+  return in_parts(all, (p.tokens * all.pieces + kRowWaves - 1) / kRowWaves, kRowWaves,
+                  [&](const RowArgs& a, int64_t blocks, bool pads) {
+    const unsigned grid = (unsigned)(blocks + (pads ? p.experts : 0));
+    if (p.dtype == kInBf16)
+      past ? dispatch_kernel<uint16_t, true><<<grid, kRowThreads, 0, st>>>(a, blocks)
+           : dispatch_kernel<uint16_t, false><<<grid, kRowThreads, 0, st>>>(a, blocks);
+    else
+      past ? dispatch_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a, blocks)
+           : dispatch_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a, blocks);
+  });
 }
 
 hipError_t launch_moe_combine(const MoeRowsParams& p, hipStream_t st) {
-  const RowArgs a = args_of(p);
-  const unsigned grid = (unsigned)((p.tokens * a.pieces + kRowWaves - 1) / kRowWaves);
+  const RowArgs all = args_of(p);
   const bool past = past_caches(p.tokens, p);
-  if (p.dtype == kInBf16)
-    past ? combine_kernel<uint16_t, true><<<grid, kRowThreads, 0, st>>>(a)
-         : combine_kernel<uint16_t, false><<<grid, kRowThreads, 0, st>>>(a);
-  else
-    past ? combine_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a)
-         : combine_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a);
-  return hipGetLastError();
+  return in_parts(all, (p.tokens * all.pieces + kRowWaves - 1) / kRowWaves, kRowWaves,
+                  [&](const RowArgs& a, int64_t blocks, bool) {
+    const unsigned grid = (unsigned)blocks;
+    if (p.dtype == kInBf16)
+      past ? combine_kernel<uint16_t, true><<<grid, kRowThreads, 0, st>>>(a)
+           : combine_kernel<uint16_t, false><<<grid, kRowThreads, 0, st>>>(a);
+    else
+      past ? combine_kernel<float, true><<<grid, kRowThreads, 0, st>>>(a)
+           : combine_kernel<float, false><<<grid, kRowThreads, 0, st>>>(a);
+  });
 }
 
 hipError_t launch_moe_combine_backward(const MoeRowsParams& p, hipStream_t st) {
-  const RowArgs a = args_of(p);
   const bool wave = p.cols <= kWaveCols;
-  const int64_t blocks = wave ? (p.tokens + kRowWaves - 1) / kRowWaves : p.tokens;
-  const unsigned grid = (unsigned)(blocks + (p.out ? p.experts : 0));
-  if (p.dtype == kInBf16)
-    wave ? combine_backward_kernel<uint16_t, 64><<<grid, kRowThreads, 0, st>>>(a, blocks)
-         : combine_backward_kernel<uint16_t, kRowThreads><<<grid, kRowThreads, 0, st>>>(a, blocks);
-  else
-    wave ? combine_backward_kernel<float, 64><<<grid, kRowThreads, 0, st>>>(a, blocks)
-         : combine_backward_kernel<float, kRowThreads><<<grid, kRowThreads, 0, st>>>(a, blocks);
-  return hipGetLastError();
+  const int per = wave ? kRowWaves : 1;
+  return in_parts(args_of(p), (p.tokens + per - 1) / per, per, [&](const RowArgs& a, int64_t blocks, bool pads) {
+    const unsigned grid = (unsigned)(blocks + (pads && p.out ? p.experts : 0));
+    if (p.dtype == kInBf16)
+      wave ? combine_backward_kernel<uint16_t, 64><<<grid, kRowThreads, 0, st>>>(a, blocks)
+           : combine_backward_kernel<uint16_t, kRowThreads><<<grid, kRowThreads, 0, st>>>(a, blocks);
+    else
+      wave ? combine_backward_kernel<float, 64><<<grid, kRowThreads, 0, st>>>(a, blocks)
+           : combine_backward_kernel<float, kRowThreads><<<grid, kRowThreads, 0, st>>>(a, blocks);
+  });
 }
 
 }  // namespace fp8mi

@@ -343,7 +343,9 @@ int fp8_moe_sort(const void* expert, int idx_dtype, int64_t tokens, int64_t topk
 
 /* fp8_moe_dispatch -- y[slot_row[t][j]] = weights[t][j] * x[t] (weights NULL:
  * 1), zeros in a segment's rows without a slot.  x [tokens x cols] and y
- * [rows x cols] BF16 or FP32; weights float [tokens x topk]. */
+ * [rows x cols] BF16 or FP32; weights float [tokens x topk].  cols <= 2^28 and
+ * tokens * ceil(cols / 1024) <= 2^31, else FP8MI_ERR_UNSUPPORTED (of
+ * fp8_moe_combine too). */
 int fp8_moe_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, int64_t ld_x, int64_t topk,
                      const float* weights, const int32_t* slot_row, const int32_t* offsets, const int32_t* counts,
                      int64_t experts, void* y, int64_t rows, int64_t ld_y, void* stream);
