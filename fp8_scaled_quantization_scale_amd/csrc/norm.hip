@@ -399,13 +399,18 @@ __global__ __launch_bounds__(64) void norm_columns_kernel(NormArgs a) {
 // dw and db from the workgroups' sums: a workgroup takes 32 of the 2 cols
 // columns, four to a thread, and each of its 128 thread groups every 128th
 // partial, so that even a short norm's sums are read by many compute units.
+// A launch has its work-items counted modulo 2^32, and a column takes 64 of
+// them: from 2^26 columns on there are several launches, each with its first
+// group.
 constexpr int kReduceCols = 32, kReduceGroups = 128;
+constexpr int64_t kReduceMost = (1LL << 31) / 1024;  // workgroups of a launch
 template <typename W>
-__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* partial, int parts, int cols, W* dw, W* db) {
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* partial, int parts, int cols, W* dw, W* db,
+                                                           int64_t first) {
   __shared__ float sums[kReduceGroups][kReduceCols + 4];
   const int64_t width = 2 * (int64_t)cols;
   const int at = (threadIdx.x & 7) * 4, group = threadIdx.x >> 3;
-  const int64_t i = (int64_t)blockIdx.x * kReduceCols + at;
+  const int64_t i = (first + blockIdx.x) * kReduceCols + at;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (i + 4 <= width) {
     for (int p = group; p < parts; p += kReduceGroups) {
@@ -430,7 +435,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* partial,
   __syncthreads();
   sums[g][c] = q;
   __syncthreads();
-  const int64_t j = (int64_t)blockIdx.x * kReduceCols + c;
+  const int64_t j = (first + blockIdx.x) * kReduceCols + c;
   if (g != 0 || j >= width) return;
   q = 0.0f;
 #pragma unroll
@@ -484,9 +489,15 @@ hipError_t forward_any(const NormParams& p, hipStream_t st) {
 template <typename W>
 hipError_t reduce(const NormParams& p, int parts, hipStream_t st) {
   if (!p.dweight && !p.dbias) return hipGetLastError();
-  norm_reduce_kernel<W><<<(unsigned)((2 * p.cols + kReduceCols - 1) / kReduceCols), 1024, 0, st>>>(
-      p.workspace, parts, (int)p.cols, static_cast<W*>(p.dweight), static_cast<W*>(p.dbias));
-  return hipGetLastError();
+  const int64_t groups = (2 * p.cols + kReduceCols - 1) / kReduceCols;
+  for (int64_t g = 0; g < groups; g += kReduceMost) {
+    const int64_t n = groups - g < kReduceMost ? groups - g : kReduceMost;
+    norm_reduce_kernel<W><<<(unsigned)n, 1024, 0, st>>>(p.workspace, parts, (int)p.cols, static_cast<W*>(p.dweight),
+                                                        static_cast<W*>(p.dbias), g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T, typename W, int NT, int C, int AHEAD>
