@@ -16,6 +16,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (BLOCK_1x128, COL, GEMM_MX_1x32, GROUP_CONTRACT, GROUP_ROWS, IDX_I32, IDX_I64, IN_BF16, IN_FP32,
@@ -193,12 +194,16 @@ class _CombineFn(torch.autograd.Function):
 
 
 def _wants_grad(*tensors) -> bool:
+    for t in tensors:  # (a dual tensor need not require grad: its tangent would be lost without a word)
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise Fp8Error("dispatch and combine have no forward-mode derivative")
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def dispatch(x: torch.Tensor, plan: Plan, weights: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The sorted rows [plan.rows x cols] of x [tokens x cols], each times its
-    slot's weight.  Differentiable in x and weights (on the current stream)."""
+    slot's weight.  Differentiable in x and weights, once and in reverse mode (on
+    the current stream)."""
     if _wants_grad(x, weights):
         _need(stream is None, "with gradients, a call runs on the current stream")
         return _DispatchFn.apply(x, weights, plan)
@@ -208,7 +213,7 @@ def dispatch(x: torch.Tensor, plan: Plan, weights: torch.Tensor | None = None, s
 def combine(ys: torch.Tensor, plan: Plan, weights: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Each token's sum [tokens x cols] of its slots' rows of ys [plan.rows x
     cols] times their weights (float [tokens x topk]; None: 1).  Differentiable
-    in ys and weights (on the current stream)."""
+    in ys and weights, once and in reverse mode (on the current stream)."""
     if _wants_grad(ys, weights):
         _need(stream is None, "with gradients, a call runs on the current stream")
         return _CombineFn.apply(ys, weights, plan)
