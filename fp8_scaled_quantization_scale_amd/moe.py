@@ -235,7 +235,7 @@ def quantize(x: torch.Tensor, plan: Plan, recipe: int, fmt: int, orient: int = R
         raise Fp8Error("experts take the recipes BLOCK_1x128, MX_1x32 and MX_1x32_OCP: other scales would span experts")
     rows, cols, dev = plan.rows, x.shape[1], x.device
     out = Quantized(fmt=fmt, recipe=recipe, nonfinite=nonfinite)
-    ld_r, ld_c = _pad16(cols), _pad16(rows)
+    ld_r, ld_c = _pad16(cols), rows  # (rows: a multiple of 128, or none, which a product takes as its contraction)
     with _scope(dev, stream):
         if orient & ROW:
             out.q_row = torch.empty(rows, ld_r, dtype=torch.uint8, device=dev)
