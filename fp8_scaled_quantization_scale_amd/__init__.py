@@ -313,6 +313,11 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t with row-major strides (of an empty tensor contiguous() leaves any)."""
+    return t.contiguous() if t.numel() else t.clone(memory_format=torch.contiguous_format)
+
+
 def _is_matrix(t, dtypes) -> bool:
     return (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
             and t.dtype in dtypes)

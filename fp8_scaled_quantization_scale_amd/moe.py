@@ -20,7 +20,7 @@ from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (BLOCK_1x128, COL, GEMM_MX_1x32, GROUP_CONTRACT, GROUP_ROWS, IDX_I32, IDX_I64, IN_BF16, IN_FP32,
-               MAX_EXPERTS, MX_1x32, MX_1x32_OCP, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _at, _ceil, _check, _here, _is_matrix,
+               MAX_EXPERTS, MX_1x32, MX_1x32_OCP, OUT_BF16, OUT_FP32, ROW, Fp8Error, Quantized, _at, _ceil, _check, _dense, _here, _is_matrix,
                _is_vector, _ld, _matrix, _need, _one_device, _pad16, _scope, _vector, load, scale_grid_shape)
 from . import quantize as _quantize_matrix
 
@@ -155,7 +155,7 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor | None, plan: Plan, weig
 
 
 def _row_major(t: torch.Tensor) -> torch.Tensor:
-    return t if t.stride(1) == 1 and _ld(t) >= t.shape[1] else t.contiguous()
+    return t if t.stride(1) == 1 and _ld(t) >= t.shape[1] else _dense(t)
 
 
 class _DispatchFn(torch.autograd.Function):
@@ -377,7 +377,7 @@ class _GroupedLinearFn(torch.autograd.Function):
         qxt, sxt, qwt, swt = ctx.saved_tensors
         p, mplan, (e, n, k), (need_dx, need_dw) = ctx.p, ctx.mplan, ctx.shape, ctx.need
         (_, fx), (_, fw), (rg, fg) = p.quant["x"], p.quant["w"], p.quant["g"]
-        dy = dy.contiguous()
+        dy = _dense(dy)
         if dy.dtype not in _DTYPES:
             dy = dy.float()
         qg = quantize(dy, mplan, rg, fg, (ROW if need_dx else 0) | (COL if need_dw else 0), gather=False)
@@ -438,5 +438,5 @@ class GroupedLinear(torch.nn.Module):
         grad = torch.is_grad_enabled()
         if grad and self.weight.requires_grad and plan.rows > _MOST_LD:
             raise Fp8Error(f"the weight's gradient takes at most {_MOST_LD} sorted rows; the plan has {plan.rows}")
-        return _GroupedLinearFn.apply(x.contiguous(), self.weight.contiguous(), plan, p, gather,
+        return _GroupedLinearFn.apply(_dense(x), self.weight.contiguous(), plan, p, gather,
                                       grad and x.requires_grad, grad and self.weight.requires_grad)

@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (IN_BF16, IN_FP32, Fp8Error, _at, _check, _here, _is_matrix, _is_vector, _ld, _matrix, _one_device,
+from . import (IN_BF16, IN_FP32, Fp8Error, _at, _check, _dense, _here, _is_matrix, _is_vector, _ld, _matrix, _one_device,
                _scope, _vector, load)
 
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
@@ -103,7 +103,7 @@ class _LayerNormFn(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         if dy.dtype != x.dtype or dy.stride(-1) != 1 or (dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]):
-            dy = dy.to(x.dtype).contiguous()
+            dy = _dense(dy.to(x.dtype))
         params = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         dx, dw, db = layer_norm_backward(dy, x, weight, mean, rstd, params)
         return (dx if ctx.needs_input_grad[0] else None, dw if ctx.needs_input_grad[1] else None,
@@ -131,5 +131,5 @@ class LayerNorm(torch.nn.Module):
             raise Fp8Error("inputs and weights are BF16 or FP32")
         x2d = x.reshape(-1, self.features)
         if x2d.stride(1) != 1 or _ld(x2d) < self.features:
-            x2d = x2d.contiguous()
+            x2d = _dense(x2d)
         return _LayerNormFn.apply(x2d, self.weight, self.bias, self.eps).reshape(x.shape)
