@@ -237,6 +237,36 @@ struct GroupArgs : GArgs {
   int turn;
 };
 
+// The segments' bounds into LDS (at [experts + 1]).  Whatever the array holds,
+// they lie in [0, R] on multiples of 128, and one that would begin before an
+// earlier ends begins there: no row is in two, and tiles number through.
+template <int THREADS>
+__device__ __forceinline__ void read_segments(const GroupArgs& p, int* at) {
+  for (int e = threadIdx.x; e <= p.experts; e += THREADS) at[e] = min(max(p.offsets[e], 0), p.R) & ~127;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    bool falls = false;
+    for (int e = lane; e < p.experts; e += 64) falls = falls || at[e + 1] < at[e];
+    if (__any(falls)) {
+      int top = 0;
+      for (int e0 = 0; e0 <= p.experts; e0 += 64) {
+        const int e = e0 + lane;
+        int v = e <= p.experts ? at[e] : 0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {  // running maximum over the wave
+          const int o = __shfl_up(v, off, 64);
+          if (lane >= off) v = max(v, o);
+        }
+        v = max(v, top);
+        if (e <= p.experts) at[e] = v;
+        top = __shfl(v, 63, 64);
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // What each recipe stages per K step.
 template <int REC>
 struct Scl {
@@ -285,17 +315,13 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
   // (8 KB for the most experts, beside 148 KB of stages and scales)
   __shared__ int seg_at[GRP == kGrpNone ? 1 : kMaxExperts + 1];
   __shared__ int seg_tile[GRP == kGrpRows ? kMaxExperts + 1 : 1];
-  if constexpr (GRP != kGrpNone) {
-    // whatever the array holds, every segment lies in [0, R) on multiples of 128
-    for (int e = tid; e <= p.experts; e += 512) seg_at[e] = min(max(p.offsets[e], 0), p.R) & ~127;
-    __syncthreads();
-  }
+  if constexpr (GRP != kGrpNone) read_segments<512>(p, seg_at);
   if constexpr (GRP == kGrpRows) {
     if (wave == 0) {
       int before = 0;
       for (int e0 = 0; e0 < p.experts; e0 += 64) {
         const int e = e0 + lane;
-        int n = e < p.experts ? (max(seg_at[e + 1] - seg_at[e], 0) + kBM - 1) / kBM * p.tiles_n : 0;
+        int n = e < p.experts ? (seg_at[e + 1] - seg_at[e] + kBM - 1) / kBM * p.tiles_n : 0;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {  // inclusive scan over the wave
           const int o = __shfl_up(n, off, 64);
@@ -359,7 +385,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
     }
     if constexpr (GRP != kGrpNone) {
       s0 = __builtin_amdgcn_readfirstlane(seg_at[ex]);
-      s1 = max(__builtin_amdgcn_readfirstlane(seg_at[ex + 1]), s0);
+      s1 = __builtin_amdgcn_readfirstlane(seg_at[ex + 1]);
     }
     if constexpr (GRP == kGrpRows) tiles_m = (s1 - s0 + kBM - 1) / kBM;
     constexpr int GROUP_M = 8;
@@ -932,28 +958,10 @@ __global__ __launch_bounds__(kFThreads, 2) void gemm_few_kernel(GroupArgs p) {
   const uint32_t fb_lo = (uint32_t)(kFM * kBK + brow0 * kBK + ((lg ^ swb) << 4));
   const uint32_t fb_hi = (uint32_t)(kFM * kBK + brow0 * kBK + (((4 + lg) ^ swb) << 4));
 
-  for (int e = tid; e <= p.experts; e += kFThreads) seg_at[e] = min(max(p.offsets[e], 0), p.R) & ~127;
-  __syncthreads();
-  // a segment that would begin before an earlier one ends begins there: row
-  // tiles are numbered through, whatever the array holds
-  if (q == 0) {
-    int top = 0;
-    for (int e0 = 0; e0 <= p.experts; e0 += 64) {
-      const int e = e0 + lane;
-      int v = e <= p.experts ? seg_at[e] : 0;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(v, off, 64);
-        if (lane >= off) v = max(v, o);
-      }
-      v = max(v, top);
-      if (e <= p.experts) seg_at[e] = v;
-      top = __shfl(v, 63, 64);
-    }
-  }
-  __syncthreads();
+  read_segments<kFThreads>(p, seg_at);
   const int tiles_n = (p.N + kFN - 1) / kFN;
-  const int total = __builtin_amdgcn_readfirstlane(seg_at[p.experts]) / kFM * tiles_n;
+  const int base = __builtin_amdgcn_readfirstlane(seg_at[0]);  // rows before the first segment have no tile
+  const int total = (__builtin_amdgcn_readfirstlane(seg_at[p.experts]) - base) / kFM * tiles_n;
   const int KT = (p.K + kBK - 1) / kBK;
 
 #pragma unroll 1
@@ -964,10 +972,10 @@ __global__ __launch_bounds__(kFThreads, 2) void gemm_few_kernel(GroupArgs p) {
     int ex = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 64) {
       const int e = e0 + lane;
-      ex += __popcll(__ballot(e < p.experts && seg_at[min(e, p.experts - 1) + 1] / kFM * tiles_n <= pid));
+      ex += __popcll(__ballot(e < p.experts && (seg_at[min(e, p.experts - 1) + 1] - base) / kFM * tiles_n <= pid));
     }
     const int s0 = __builtin_amdgcn_readfirstlane(seg_at[ex]), s1 = __builtin_amdgcn_readfirstlane(seg_at[ex + 1]);
-    const int local = max(pid - s0 / kFM * tiles_n, 0), blocks = max((s1 - s0) / kFM, 1);
+    const int local = pid - (s0 - base) / kFM * tiles_n, blocks = (s1 - s0) / kFM;
     const int pm = local % blocks, pn = local / blocks;  // an expert's row tiles share B in turn
     const int m0 = s0 + pm * kFM, n0 = pn * kFN;
     const int rows_b = min(kFN, p.N - n0);

@@ -406,7 +406,7 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
  *       stride_sb are not used.
  * offsets: int32 [experts + 1] as fp8_moe_sort gives it (read on the device;
  * values outside [0, rows] are clamped to it, others rounded down to multiples
- * of 128).  rows % 128 == 0, K % 16 == 0, stride_b % 16 == 0; other
+ * of 128, and one below an earlier one is raised to it).  rows % 128 == 0, K % 16 == 0, stride_b % 16 == 0; other
  * requirements, errors, tolerance and non-finite inputs as for
  * fp8_gemm_scaled.  GROUP_CONTRACT needs rows <= 4194304. */
 int fp8_gemm_grouped(const uint8_t* a, int fmt_a, const void* s_a, int64_t lda,
