@@ -160,9 +160,12 @@ __device__ __forceinline__ int lds_u8(uint32_t addr) {
 // Inline asm is opaque to the compiler's own hazard handling: where it spills
 // scalars into vector lanes, an operand may have come from a v_readlane right
 // before, which a vector memory instruction may read 5 wait states later at the
-// earliest.  The grouped products spill some: their loads wait that long
-// (kDmaSafe), but for the rows form's operand tiles, whose resources and
-// offsets stay in scalars (waiting there cost 1%).
+// earliest.  The grouped products' loads wait that long by themselves
+// (kDmaSafe); a contraction form whose loads did not left rows zero.  It costs
+// the rows form 1 to 2% (16384 rows over 8 experts, 14336 x 4096 each: 869 ->
+// 878 us, MX 854 -> 872).  The plain products do without: in their machine code
+// no spill stands so near a load, which tests/test_lds_load_waits.py reads in
+// every build.
 constexpr int kDmaSafe = 4;
 template <int WAIT = 0>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
@@ -349,7 +352,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
   // second set, every step paid for it: 16384 rows over 8 experts, 14336 x 4096,
   // 890 -> 928 us; over 64, 4096 x 2048, MX, 227 -> 226.
   constexpr bool kChain = GRP == kGrpContract;
-  constexpr int kWait = GRP != kGrpNone ? kDmaSafe : 0, kWaitTile = kChain ? kDmaSafe : 0;
+  constexpr int kWait = GRP != kGrpNone ? kDmaSafe : 0;
   __amdgpu_buffer_rsrc_t ra = make_rsrc(nullptr, 0), rb = ra, rsa = ra, rsb = ra;
   int ex_ld = 0, m0_ld = 0, n0_ld = 0, end_ld = 0, K_ld = 0, KT_ld = 0, rot_ld = 0, mis_ld = 0, nblk_ld = 0;
   int nkb_b = p.nkb;  // grouped: scale entries between two rows of B
@@ -520,7 +523,7 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
       }
       uint32_t lb = __builtin_amdgcn_readfirstlane(lds_base + ((kt + par_ld) & 1) * kTileBytes);
       asm volatile("" : "+s"(lb));
-      dma16<kWaitTile>(rs, lb + seg * 1024, vo, (uint32_t)k0);
+      dma16<kWait>(rs, lb + seg * 1024, vo, (uint32_t)k0);
     };
     // Scales of the kSG steps from kt on (kt a multiple of kSG) into group
     // buffer (kt / kSG) & 1.  A side, each group its own 128 rows: waves
@@ -1009,14 +1012,14 @@ __global__ __launch_bounds__(kFThreads, 2) void gemm_few_kernel(GroupArgs p) {
         const int seg = 4 * q + i, ca = 16 * ((lane & 7) ^ (lane >> 3));
         uint32_t vo = (uint32_t)((8 * seg + (lane >> 3)) * (int)p.lda + ca);
         if (k0 + ca >= p.K) vo = kOOB;
-        dma16(ra, lb + seg * 1024, vo, (uint32_t)k0);
+        dma16<kDmaSafe>(ra, lb + seg * 1024, vo, (uint32_t)k0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int seg = 4 * q + i, cb = 16 * ((lane & 7) ^ (((lane >> 3) & 3) | ((seg & 2) << 1)));
         uint32_t vo = (uint32_t)((8 * seg + (lane >> 3)) * (int)p.ldb + cb);
         if (k0 + cb >= p.K) vo = kOOB;
-        dma16(rb, lb + kFM * kBK + seg * 1024, vo, (uint32_t)k0);
+        dma16<kDmaSafe>(rb, lb + kFM * kBK + seg * 1024, vo, (uint32_t)k0);
       }
       if (kt % kSG) return;
       const uint32_t sb = scl_base + (uint32_t)(((kt / kSG) & 1) * kFScl);
