@@ -281,13 +281,15 @@ _NOTHING = _Nothing()
 
 def _scope(device: torch.device, stream):
     """Where a call allocates and launches: on `stream` (a torch stream or a
-    raw handle), else on the current stream of the tensors' device.  What is
+    raw handle, of the tensors' device), else on the current stream of the tensors' device.  What is
     allocated inside belongs to that stream, so a workspace that is freed when
     the call returns is not handed to another stream's work before its own."""
     if stream is None:
         return _NOTHING if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise Fp8Error(f"the stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
 
 
