@@ -220,6 +220,9 @@ int fp8_gemm_grouped(const uint8_t* a, int fmt_a, const void* s_a, int64_t lda, 
   // the persistent grid numbers all experts' 256 x 256 tiles with 32-bit ints
   const int64_t tm = contract ? (m + 255) / 256 * experts : m / 256 + experts, tn = (N + 255) / 256;
   if (tm > 0x7FFFFFFFLL / tn) return FP8MI_ERR_UNSUPPORTED;
+  // no element of C in two experts' products: one after the other, or row by row in turn
+  if (contract && experts > 1 && stride_c < (m - 1) * ldc + N && (stride_c < N || (experts - 1) * stride_c + N > ldc))
+    return FP8MI_ERR_SHAPE;
   fp8mi::GroupedGemmParams p{contract, a, fmt_a, s_a, lda, b, fmt_b, s_b, ldb, stride_b, ld_sb, stride_sb, recipe,
                              offsets, experts, rows, contract ? M : 0, N, contract ? 0 : K, c, c_dtype, ldc, stride_c};
   return fp8mi::hip_status(fp8mi::launch_gemm_grouped(p, (hipStream_t)stream));

@@ -320,7 +320,8 @@ def gemm_wgrad(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, 
     """c[e] = dequant(a[:, segment e]) . dequant(b[:, segment e])^T for every
     expert: a [M x rows], b [N x rows] the transposed codes of the sorted rows
     (quantize's COL outputs), s_a and s_b their grids [M x rows/128] and [N x
-    rows/128] (GEMM_MX_1x32: rows/32 bytes); c [experts x M x N]."""
+    rows/128] (GEMM_MX_1x32: rows/32 bytes); c [experts x M x N] with unit last
+    stride, the experts one after the other or their rows in turn."""
     for name, t in (("a", a), ("b", b)):
         if not _is_matrix(t, _CODES):
             _matrix(name, t, _CODES)
@@ -337,8 +338,6 @@ def gemm_wgrad(a: torch.Tensor, fmt_a: int, s_a: torch.Tensor, b: torch.Tensor, 
     with _scope(a.device, stream):
         c = _out_of(c, (experts, m, n), out_dtype, a.device)
         ldc = c.stride(1) if m > 1 else max(c.stride(1), n)
-        if experts > 1 and m * n > 0 and c.stride(0) < (m - 1) * ldc + n:
-            raise Fp8Error("c's experts must not overlap")
         st = load().fp8_gemm_grouped(a.data_ptr(), fmt_a, s_a.data_ptr(), _ld(a), b.data_ptr(), fmt_b, s_b.data_ptr(),
                                      _ld(b), 0, 0, 0, recipe, GROUP_CONTRACT, offsets.data_ptr(), experts, rows, m, n,
                                      0, c.data_ptr(), _OUT_DTYPES[c.dtype], ldc, c.stride(0), _here(a.device))

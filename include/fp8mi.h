@@ -401,7 +401,9 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
  *   GROUP_CONTRACT (wgrad): for every expert, C_e = dequant(A[:, segment e]) .
  *       dequant(B[:, segment e])^T, zeros for an empty segment.
  *       a [M x rows], b [N x rows] (the COL outputs of fp8_moe_quantize), s_a
- *       and s_b their dense grids; C_e = c + e * stride_c, [M x N] with ldc.
+ *       and s_b their dense grids; C_e = c + e * stride_c, [M x N] with ldc,
+ *       the C_e one after the other (stride_c >= (M - 1) ldc + N) or their rows
+ *       in turn (stride_c >= N, ldc >= (experts - 1) stride_c + N).
  *       recipe GEMM_BLOCK_1x128_1x128 or GEMM_MX_1x32.  K, stride_b, ld_sb and
  *       stride_sb are not used.
  * offsets: int32 [experts + 1] as fp8_moe_sort gives it (read on the device;
