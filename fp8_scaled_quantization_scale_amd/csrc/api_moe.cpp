@@ -12,10 +12,10 @@
 namespace {
 
 using fp8mi::aligned_to;
+using fp8mi::check_matrix;
+using fp8mi::in_dtype_ok;
+using fp8mi::in_size;
 using fp8mi::span_ok;
-
-bool dtype_ok(int d) { return d == FP8MI_IN_BF16 || d == FP8MI_IN_FP32; }
-int64_t size_of(int dtype) { return dtype == FP8MI_IN_BF16 ? 2 : 4; }
 
 // tokens, choices and experts that every entry point takes
 int check_routing(int64_t tokens, int64_t topk, int64_t experts) {
@@ -28,12 +28,6 @@ int check_routing(int64_t tokens, int64_t topk, int64_t experts) {
 int check_rows(int64_t rows) {
   if (rows < 0 || rows % FP8MI_EXPERT_ALIGN) return FP8MI_ERR_SHAPE;
   return rows > 0x7FFFFF00LL ? FP8MI_ERR_UNSUPPORTED : FP8MI_OK;
-}
-
-int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t esize) {
-  if (!p) return FP8MI_ERR_NULL;
-  if (ld < cols || !span_ok(rows, ld, esize)) return FP8MI_ERR_SHAPE;
-  return aligned_to(p, esize) ? FP8MI_OK : FP8MI_ERR_ALIGN;
 }
 
 }  // namespace
@@ -80,7 +74,7 @@ int fp8_moe_sort(const void* expert, int idx_dtype, int64_t tokens, int64_t topk
 int fp8_moe_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, int64_t ld_x, int64_t topk,
                      const float* weights, const int32_t* slot_row, const int32_t* offsets, const int32_t* counts,
                      int64_t experts, void* y, int64_t rows, int64_t ld_y, void* stream) {
-  if (!dtype_ok(dtype)) return FP8MI_ERR_ENUM;
+  if (!in_dtype_ok(dtype)) return FP8MI_ERR_ENUM;
   int st = check_routing(tokens, topk, experts);
   if (st != FP8MI_OK) return st;
   if ((st = check_rows(rows)) != FP8MI_OK) return st;
@@ -88,11 +82,11 @@ int fp8_moe_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, int
   if (tokens == 0 || cols == 0 || rows == 0) return FP8MI_OK;
   if (cols > (1LL << 28) || tokens * ((cols + 1023) / 1024) > (1LL << 31)) return FP8MI_ERR_UNSUPPORTED;
   if (!slot_row || !offsets || !counts) return FP8MI_ERR_NULL;
-  if ((st = check_matrix(x, tokens, cols, ld_x, size_of(dtype))) != FP8MI_OK) return st;
-  if ((st = check_matrix(y, rows, cols, ld_y, size_of(dtype))) != FP8MI_OK) return st;
+  if ((st = check_matrix(x, tokens, cols, ld_x, in_size(dtype))) != FP8MI_OK) return st;
+  if ((st = check_matrix(y, rows, cols, ld_y, in_size(dtype))) != FP8MI_OK) return st;
   if (!aligned_to(weights, 4) || !aligned_to(slot_row, 4) || !aligned_to(offsets, 4) || !aligned_to(counts, 4))
     return FP8MI_ERR_ALIGN;
-  fp8mi::MoeRowsParams p{dtype, tokens, topk, experts, cols, rows, offsets, counts, nullptr, slot_row, weights,
+  fp8mi::MoeRowsParams p{dtype, tokens, topk, experts, cols, rows, offsets, counts, slot_row, weights,
                          x, ld_x, nullptr, 0, y, ld_y, nullptr};
   return fp8mi::hip_status(fp8mi::launch_moe_dispatch(p, (hipStream_t)stream));
 }
@@ -101,7 +95,7 @@ int fp8_moe_quantize(const void* x, int x_dtype, int64_t x_rows, int64_t cols, i
                      int64_t topk, const float* weights, const int32_t* offsets, int64_t experts, int64_t rows,
                      int recipe, int fmt, int orient, int margin, uint8_t* q_row, int64_t ld_q_row, void* s_row,
                      uint8_t* q_col, int64_t ld_q_col, void* s_col, int32_t* nonfinite, void* stream) {
-  if (!dtype_ok(x_dtype)) return FP8MI_ERR_ENUM;
+  if (!in_dtype_ok(x_dtype)) return FP8MI_ERR_ENUM;
   if (recipe < FP8MI_TENSOR_CURRENT || recipe > FP8MI_MX_1x32_OCP) return FP8MI_ERR_ENUM;
   if (fmt != FP8MI_E4M3 && fmt != FP8MI_E5M2) return FP8MI_ERR_ENUM;
   if (orient != FP8MI_ROW && orient != FP8MI_COL && orient != FP8MI_ROW_AND_COL) return FP8MI_ERR_ENUM;
@@ -117,7 +111,7 @@ int fp8_moe_quantize(const void* x, int x_dtype, int64_t x_rows, int64_t cols, i
   const bool row = orient & FP8MI_ROW, col = orient & FP8MI_COL;
   if (!offsets || (x_rows > 0 && !x)) return FP8MI_ERR_NULL;
   if ((row && (!q_row || !s_row)) || (col && (!q_col || !s_col))) return FP8MI_ERR_NULL;
-  const int64_t es = size_of(x_dtype);
+  const int64_t es = in_size(x_dtype);
   if (ld_x < cols || (row && ld_q_row < cols) || (col && ld_q_col < rows)) return FP8MI_ERR_SHAPE;
   if (!span_ok(x_rows, ld_x, es) || (row && !span_ok(rows, ld_q_row, 1)) || (col && !span_ok(cols, ld_q_col, 1)))
     return FP8MI_ERR_SHAPE;
@@ -134,7 +128,7 @@ int fp8_moe_quantize(const void* x, int x_dtype, int64_t x_rows, int64_t cols, i
 
 int fp8_moe_combine(const void* ys, int dtype, int64_t rows, int64_t cols, int64_t ld_ys, const int32_t* slot_row,
                     int64_t tokens, int64_t topk, const float* weights, void* y, int64_t ld_y, void* stream) {
-  if (!dtype_ok(dtype)) return FP8MI_ERR_ENUM;
+  if (!in_dtype_ok(dtype)) return FP8MI_ERR_ENUM;
   int st = check_routing(tokens, topk, 1);
   if (st != FP8MI_OK) return st;
   if ((st = check_rows(rows)) != FP8MI_OK) return st;
@@ -142,10 +136,10 @@ int fp8_moe_combine(const void* ys, int dtype, int64_t rows, int64_t cols, int64
   if (tokens == 0 || cols == 0) return FP8MI_OK;
   if (cols > (1LL << 28) || tokens * ((cols + 1023) / 1024) > (1LL << 31)) return FP8MI_ERR_UNSUPPORTED;
   if (!slot_row) return FP8MI_ERR_NULL;
-  if (rows > 0 && (st = check_matrix(ys, rows, cols, ld_ys, size_of(dtype))) != FP8MI_OK) return st;
-  if ((st = check_matrix(y, tokens, cols, ld_y, size_of(dtype))) != FP8MI_OK) return st;
+  if (rows > 0 && (st = check_matrix(ys, rows, cols, ld_ys, in_size(dtype))) != FP8MI_OK) return st;
+  if ((st = check_matrix(y, tokens, cols, ld_y, in_size(dtype))) != FP8MI_OK) return st;
   if (!aligned_to(weights, 4) || !aligned_to(slot_row, 4)) return FP8MI_ERR_ALIGN;
-  fp8mi::MoeRowsParams p{dtype, tokens, topk, 0, cols, rows, nullptr, nullptr, nullptr, slot_row, weights,
+  fp8mi::MoeRowsParams p{dtype, tokens, topk, 0, cols, rows, nullptr, nullptr, slot_row, weights,
                          nullptr, 0, ys, ld_ys, y, ld_y, nullptr};
   return fp8mi::hip_status(fp8mi::launch_moe_combine(p, (hipStream_t)stream));
 }
@@ -154,7 +148,7 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
                              int64_t ld_ys, const int32_t* slot_row, const int32_t* offsets, const int32_t* counts,
                              int64_t experts, int64_t topk, const float* weights, void* dys, int64_t rows,
                              int64_t ld_dys, float* dweights, void* stream) {
-  if (!dtype_ok(dtype)) return FP8MI_ERR_ENUM;
+  if (!in_dtype_ok(dtype)) return FP8MI_ERR_ENUM;
   int st = check_routing(tokens, topk, experts);
   if (st != FP8MI_OK) return st;
   if ((st = check_rows(rows)) != FP8MI_OK) return st;
@@ -162,7 +156,7 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
   if (tokens == 0 || (!dys && !dweights)) return FP8MI_OK;
   if (cols > (1LL << 28)) return FP8MI_ERR_UNSUPPORTED;
   if (!slot_row || (dys && (!offsets || !counts))) return FP8MI_ERR_NULL;
-  const int64_t es = size_of(dtype);
+  const int64_t es = in_size(dtype);
   if (cols > 0) {
     if ((st = check_matrix(dy, tokens, cols, ld_dy, es)) != FP8MI_OK) return st;
     if (rows > 0 && dweights && (st = check_matrix(ys, rows, cols, ld_ys, es)) != FP8MI_OK) return st;
@@ -171,7 +165,7 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
   if (!aligned_to(weights, 4) || !aligned_to(slot_row, 4) || !aligned_to(offsets, 4) || !aligned_to(counts, 4) ||
       !aligned_to(dweights, 4))
     return FP8MI_ERR_ALIGN;
-  fp8mi::MoeRowsParams p{dtype, tokens, topk, experts, cols, rows, offsets, counts, nullptr, slot_row, weights,
+  fp8mi::MoeRowsParams p{dtype, tokens, topk, experts, cols, rows, offsets, counts, slot_row, weights,
                          dy, ld_dy, ys, ld_ys, dys, ld_dys, dweights};
   return fp8mi::hip_status(fp8mi::launch_moe_combine_backward(p, (hipStream_t)stream));
 }

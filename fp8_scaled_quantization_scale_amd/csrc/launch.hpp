@@ -128,7 +128,7 @@ struct MoeSortParams {
 struct MoeRowsParams {
   int dtype;
   int64_t tokens, topk, experts, cols, rows;
-  const int32_t *offsets, *counts, *row_slot, *slot_row;
+  const int32_t *offsets, *counts, *slot_row;
   const float* weights;
   const void* token_rows;  // x / dy
   int64_t ld_token;
@@ -151,7 +151,6 @@ struct NormParams {
   void* out;  // y / dx
   void *dweight, *dbias;
   float* workspace;
-  int64_t workspace_floats;
 };
 
 // FP8MI_OK, or FP8MI_ERR_HIP with the error's text kept for fp8_status_string
