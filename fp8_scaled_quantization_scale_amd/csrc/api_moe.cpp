@@ -116,7 +116,7 @@ int fp8_moe_quantize(const void* x, int x_dtype, int64_t x_rows, int64_t cols, i
   if (!span_ok(x_rows, ld_x, es) || (row && !span_ok(rows, ld_q_row, 1)) || (col && !span_ok(cols, ld_q_col, 1)))
     return FP8MI_ERR_SHAPE;
   if (x_rows > 0x7FFFFFFFLL || (cols + 127) / 128 > 0x7FFFFFFFLL / (rows / 128)) return FP8MI_ERR_UNSUPPORTED;
-  if (!aligned_to(x, 16) || (ld_x * es) % 16 || (row && (!aligned_to(q_row, 16) || ld_q_row % 16)) ||
+  if (!aligned_to(x, 16) || ld_x % (16 / es) || (row && (!aligned_to(q_row, 16) || ld_q_row % 16)) ||
       (col && (!aligned_to(q_col, 16) || ld_q_col % 16)) || !aligned_to(offsets, 4) || !aligned_to(row_slot, 4) ||
       !aligned_to(weights, 4))
     return FP8MI_ERR_ALIGN;
