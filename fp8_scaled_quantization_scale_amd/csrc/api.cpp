@@ -60,9 +60,13 @@ int check_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64
   if (!aligned16(x) || (ld_x * esize) % 16) return FP8MI_ERR_ALIGN;
   if (row && (!aligned16(q_row) || ld_q_row % 16)) return FP8MI_ERR_ALIGN;
   if (col && (!aligned16(q_col) || ld_q_col % 16)) return FP8MI_ERR_ALIGN;
-  // channel scaling launches one workgroup per tile on a 1-D grid
-  if (recipe == FP8MI_CHANNEL && ((rows + 127) / 128) * ((cols + 127) / 128) > 0x7FFFFFFF)
-    return FP8MI_ERR_UNSUPPORTED;
+  // channel scaling launches a workgroup of 256 per tile, and 16 work-items per
+  // row (column) that has several; a launch counts them modulo 2^32
+  if (recipe == FP8MI_CHANNEL) {
+    const int64_t tx = (cols + 127) / 128, ty = (rows + 127) / 128;
+    if (tx * ty > 0xFFFFFF || (row && tx > 1 && rows > 0xFFFFFF0) || (col && ty > 1 && cols > 0xFFFFFF0))
+      return FP8MI_ERR_UNSUPPORTED;
+  }
   return FP8MI_OK;
 }
 

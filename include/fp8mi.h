@@ -169,9 +169,11 @@ extern "C" {
  * Alignment: x, q_row, q_col 16-byte aligned; ld_x * sizeof(elem),
  * ld_q_row and ld_q_col multiples of 16 bytes.  Sizes: rows * ld_x *
  * sizeof(elem), rows * ld_q_row and cols * ld_q_col must fit in int64 (else
- * FP8MI_ERR_SHAPE); CHANNEL needs ceil(rows/128) * ceil(cols/128) < 2^31
- * (else FP8MI_ERR_UNSUPPORTED); the other recipes take any size.  rows == 0 or cols == 0 is
- * allowed (CURRENT then writes amax = 0, scale = scale_inv = 1).
+ * FP8MI_ERR_SHAPE); CHANNEL needs ceil(rows/128) * ceil(cols/128) < 2^24, of
+ * over 128 columns at most 2^28 - 16 rows for ROW and of over 128 rows at most
+ * 2^28 - 16 columns for COL (else FP8MI_ERR_UNSUPPORTED); the other recipes
+ * take any size.  rows == 0 or cols == 0 is allowed (CURRENT then writes
+ * amax = 0, scale = scale_inv = 1).
  * Returns FP8MI_OK or an FP8MI_ERR_* code; nothing is launched on error. */
 int fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
                  int recipe, int fmt, int orient, int margin,
