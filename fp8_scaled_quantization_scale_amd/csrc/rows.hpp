@@ -15,9 +15,15 @@ typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // NT: written past the caches, for output that nothing reads before it would
-// have left them anyway
-template <bool NT, typename V>
-__device__ __forceinline__ void put(V v, V* p) {
+// have left them anyway.  (Not a template over the vector's type: deduction
+// drops the typedefs' alignment, and the stores would claim 16 bytes.)
+template <bool NT>
+__device__ __forceinline__ void put(u32x4a2 v, u32x4a2* p) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+template <bool NT>
+__device__ __forceinline__ void put(f32x4a4 v, f32x4a4* p) {
   if constexpr (NT) __builtin_nontemporal_store(v, p);
   else *p = v;
 }
