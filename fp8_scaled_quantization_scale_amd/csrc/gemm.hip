@@ -202,9 +202,9 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (
 //
 // Bound as the kernel itself is, by the matrix cores and the tile boundary of
 // about 8 us, which shorter K loops feel more: 16384 rows over 8 experts,
-// 14336 x 4096 each, 1x128 x 128x128: 890 us, 2.16 PFLOP/s of the rows that
+// 14336 x 4096 each, 1x128 x 128x128: 893 us, 2.15 PFLOP/s of the rows that
 // hold slots (68 row tiles in 15 rounds; one 16384-row product, 64 row tiles in
-// 14 rounds: 797 us); its weight gradient 1116 us, 1.72 PFLOP/s (28 tiles of 8
+// 14 rounds: 797 us); its weight gradient 1132 us, 1.70 PFLOP/s (28 tiles of 8
 // to 45 steps per workgroup; one product with K = 16384: 1006 us).  With few
 // rows per expert it streams the weights, in 128 x 128 tiles (gemm_few_kernel).
 constexpr int kGrpNone = 0, kGrpRows = 1, kGrpContract = 2;
@@ -344,13 +344,14 @@ __global__ __launch_bounds__(512, 1) void gemm_kernel(std::conditional_t<GRP == 
   // The contraction form runs its tiles in one chain (kChain): the last step's
   // load phase sends for the next tile's first step, and the two groups stay a
   // phase apart, so that a tile boundary is the epilogue alone.  Two sets of
-  // variables, then: what the loads on their way go by (ra .. nblk_ld; aim()
-  // sets them to a tile) and what the products and the epilogue do.  Its K
-  // loops are short: 16384 rows over 64 experts, 4096 x 2048 each, 514 -> 441 us
-  // (MX 498 -> 441); 4000 over 128, 2048 x 2048, 380 -> 340; 16384 over 8, 14336
-  // x 4096, 1152 -> 1116.  In the rows form, which has no scalars left for the
-  // second set, every step paid for it: 16384 rows over 8 experts, 14336 x 4096,
-  // 890 -> 928 us; over 64, 4096 x 2048, MX, 227 -> 226.
+  // integers, then: what the loads on their way go by (ex_ld .. nblk_ld; aim()
+  // sets these and the resources to a tile) and what the products and the
+  // epilogue do.  Its K loops are short: 16384 rows over 64 experts, 4096 x 2048
+  // each, 514 -> 441 us (MX 498 -> 441); 4000 over 128, 2048 x 2048, 380 -> 340;
+  // 16384 over 8, 14336 x 4096, 1152 -> 1116.  In the rows form, with aim() in
+  // the K loop, the spilled scalars go from 17 to 39 (MX: 24 to 47) and every
+  // step pays: 16384 rows over 8 experts, 14336 x 4096, 890 -> 928 us; over 64,
+  // 4096 x 2048, MX, 227 -> 226.
   constexpr bool kChain = GRP == kGrpContract;
   constexpr int kWait = GRP != kGrpNone ? kDmaSafe : 0;
   __amdgpu_buffer_rsrc_t ra = make_rsrc(nullptr, 0), rb = ra, rsa = ra, rsb = ra;

@@ -1,6 +1,7 @@
 // moe.hip -- tokens sorted by expert and back, for gfx950: the sort, the plain
 // dispatch, the weighted combine and its gradient.  (The dispatch into FP8
-// codes is the tile kernel of quantize.hip reading through the sort's row map.)
+// codes reads through the sort's row map in quantize.hip: moe_tile_kernel for
+// BF16 rows of whole tiles, the MOE form of quant_tile_kernel for the others.)
 //
 // Slot s = t topk + j is token t's j-th choice.  The sorted buffer holds one
 // segment per expert, each starting on a multiple of 128 rows, so that a

@@ -12,10 +12,14 @@
 // 8 elements each), so the two passes of the variance cost no second read;
 // statistics and sums are FP32.  Workgroups are persistent: the weight (and
 // the backward pass's column sums) stay in registers from row to row, and the
-// next row's words are on their way while one row is reduced.
+// next row's words are on their way while one row is reduced (backward: two
+// rows' of 1025 to 8192 columns, one's up to 1024, none's over 8192).
 //
-// Measured (MI355X): forward 8192 x 16384 BF16 97 us (5.6 TB/s of what it must
-// move), backward 16384 x 8192 157 us (5.1 TB/s), 8192 x 4096 42 us (4.8 TB/s).
+// Measured (MI355X): forward 8192 x 16384 BF16 96 us with x partly in the
+// caches, 111 without (4.8 TB/s); backward 16384 x 8192 157 us (5.1 TB/s), 8192
+// x 4096 45 us (4.5 TB/s).  Over 16384 columns the rows are read again from the
+// caches: 4096 x 32768 BF16 forward 171 us (3.1 TB/s), backward 386 (2.1; its
+// column sums read x and dy once more), 1024 x 65536 81 (3.3) and 243 (1.7).
 //
 // The weight's gradient needs a sum over all rows: every workgroup leaves the
 // sums of its own rows in a workspace, and a second launch adds these in a
@@ -523,8 +527,9 @@ hipError_t backward_any(const NormParams& p, hipStream_t st) {
   // Threads and chunks per row: few enough threads that a row's sum ends in
   // few waves, few enough chunks that sums, weight and the rows ahead stay in
   // registers.  Two rows ahead beat one where they fit (8192 x 4096 BF16: 42 us
-  // against 47); a 16384-column row leaves no room for any (8192 rows BF16: 161
-  // us; with one ahead 275 us of spills; 512 threads of 4 chunks 162 us).
+  // against 47); a 16384-column row leaves no room for any (8192 rows BF16: 165
+  // us, with 2 registers spilled, 6 beside FP32 weights; one row ahead 275 us of
+  // spills; 512 threads of 4 chunks 162 us).
   if (p.cols <= 512) return backward<T, W, 64, 1, 1>(p, st);
   if (p.cols <= 1024) return backward<T, W, 64, 2, 1>(p, st);
   if (p.cols <= 2048) return backward<T, W, 256, 1, 2>(p, st);
