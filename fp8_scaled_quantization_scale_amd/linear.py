@@ -45,7 +45,7 @@ import torch
 
 from . import (BLOCK_1x128, BLOCK_128x128, CHANNEL, COL, E4M3, E5M2, GEMM_BLOCK_1x128_1x128,
                GEMM_BLOCK_1x128_128x128, GEMM_CHANNEL, GEMM_MX_1x32, GEMM_TENSOR, MX_1x32, ROW,
-               TENSOR_CURRENT, TENSOR_DELAYED, DelayedState, Fp8Error, gemm, load, quantize)
+               TENSOR_CURRENT, TENSOR_DELAYED, DelayedState, Fp8Error, _dense, gemm, load, quantize)
 
 
 class Format(enum.Enum):
@@ -234,7 +234,7 @@ class _Fp8LinearFn(torch.autograd.Function):
         x_dt, w_dt = ctx.dtypes
         fx, fw = ctx.fmts
         need_dx, need_dw = ctx.need
-        dy = dy.contiguous()
+        dy = _dense(dy)
         if dy.dtype not in (torch.bfloat16, torch.float32):
             dy = dy.float()
         qg = _cast("g", dy, (ROW if need_dx else 0) | (COL if need_dw else 0), p, states, interval)
@@ -293,7 +293,7 @@ class Linear(torch.nn.Module):
             raise Fp8Error("inputs and weights are BF16 or FP32")
         load()
         lead = x.shape[:-1]
-        x2d = x.reshape(-1, self.in_features).contiguous()
+        x2d = _dense(x.reshape(-1, self.in_features))
         grad = torch.is_grad_enabled()
         need_dx, need_dw = grad and x.requires_grad, grad and self.weight.requires_grad
         if need_dw and x2d.shape[0] % 16:
