@@ -46,7 +46,9 @@ EXPORTS = ("fp8_quantize", "fp8_quantize_static_scratch", "fp8_amax_history_upda
            "fp8_bf16_gemm", "fp8_status_string", "fp8_version",
            "fp8_layer_norm_forward", "fp8_layer_norm_workspace", "fp8_layer_norm_backward",
            "fp8_moe_rows", "fp8_moe_sort_workspace", "fp8_moe_sort", "fp8_moe_dispatch", "fp8_moe_quantize",
-           "fp8_moe_combine", "fp8_moe_combine_backward", "fp8_gemm_grouped")
+           "fp8_moe_combine", "fp8_moe_combine_backward", "fp8_gemm_grouped",
+           "fp8_rms_norm_forward", "fp8_rms_norm_quantize", "fp8_rms_norm_workspace", "fp8_rms_norm_backward",
+           "fp8_moe_route_workspace", "fp8_moe_route", "fp8_moe_balance", "fp8_moe_route_backward")
 
 
 class Fp8Error(RuntimeError):
@@ -103,6 +105,23 @@ def load(path: str = LIB_PATH):
     lib.fp8_gemm_grouped.restype = i32
     lib.fp8_gemm_grouped.argtypes = [vp, i32, vp, i64, vp, i32, vp, i64, i64, i64, i64, i32, i32, vp, i64, i64, i64,
                                      i64, i64, vp, i32, i64, i64, vp]
+    lib.fp8_rms_norm_forward.restype = i32
+    lib.fp8_rms_norm_forward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, i64, vp, vp]
+    lib.fp8_rms_norm_quantize.restype = i32
+    lib.fp8_rms_norm_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, i32, i32, i32, i32,
+                                          vp, i64, vp, vp, i64, vp, vp, vp]
+    lib.fp8_rms_norm_workspace.restype = i64
+    lib.fp8_rms_norm_workspace.argtypes = [i64, i64]
+    lib.fp8_rms_norm_backward.restype = i32
+    lib.fp8_rms_norm_backward.argtypes = [vp, i64, vp, i32, i64, i64, i64, vp, i32, vp, vp, i64, vp, i64, vp, vp, i64, vp]
+    lib.fp8_moe_route_workspace.restype = i64
+    lib.fp8_moe_route_workspace.argtypes = [i64, i64]
+    lib.fp8_moe_route.restype = i32
+    lib.fp8_moe_route.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.fp8_moe_balance.restype = i32
+    lib.fp8_moe_balance.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, i64, vp, vp, vp, vp, i64, vp]
+    lib.fp8_moe_route_backward.restype = i32
+    lib.fp8_moe_route_backward.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, i32, vp, vp, vp, i64, vp]
     lib.fp8_status_string.restype = ctypes.c_char_p
     lib.fp8_status_string.argtypes = [i32]
     lib.fp8_version.restype = i32
@@ -254,6 +273,57 @@ def fp8_moe_combine_backward(dy, dtype, tokens, cols, ld_dy, ys, ld_ys, slot_row
     return load().fp8_moe_combine_backward(_p(dy), dtype, tokens, cols, ld_dy, _p(ys), ld_ys, _p(slot_row),
                                            _p(offsets), _p(counts), experts, topk, _p(weights), _p(dys), rows, ld_dys,
                                            _p(dweights), _stream(stream))
+
+
+def fp8_rms_norm_forward(x, x_dtype, rows, cols, ld_x, residual, ld_residual, weight, w_dtype, eps, total, ld_total, y,
+                         ld_y, rstd, stream=None) -> int:
+    return load().fp8_rms_norm_forward(_p(x), x_dtype, rows, cols, ld_x, _p(residual), ld_residual, _p(weight), w_dtype,
+                                       eps, _p(total), ld_total, _p(y), ld_y, _p(rstd), _stream(stream))
+
+
+def fp8_rms_norm_quantize(x, x_dtype, rows, cols, ld_x, residual, ld_residual, weight, w_dtype, eps, total, ld_total, rstd,
+                          recipe, fmt, orient, margin, q_row, ld_q_row, s_row, q_col, ld_q_col, s_col, nonfinite,
+                          stream=None) -> int:
+    return load().fp8_rms_norm_quantize(_p(x), x_dtype, rows, cols, ld_x, _p(residual), ld_residual, _p(weight), w_dtype,
+                                        eps, _p(total), ld_total, _p(rstd), recipe, fmt, orient, margin, _p(q_row),
+                                        ld_q_row, _p(s_row), _p(q_col), ld_q_col, _p(s_col), _p(nonfinite),
+                                        _stream(stream))
+
+
+def fp8_rms_norm_workspace(rows, cols) -> int:
+    return load().fp8_rms_norm_workspace(rows, cols)
+
+
+def fp8_rms_norm_backward(dy, ld_dy, total, x_dtype, rows, cols, ld_total, weight, w_dtype, rstd, dtotal, ld_dtotal, dx,
+                          ld_dx, dweight, workspace, workspace_bytes, stream=None) -> int:
+    return load().fp8_rms_norm_backward(_p(dy), ld_dy, _p(total), x_dtype, rows, cols, ld_total, _p(weight), w_dtype,
+                                        _p(rstd), _p(dtotal), ld_dtotal, _p(dx), ld_dx, _p(dweight), _p(workspace),
+                                        workspace_bytes, _stream(stream))
+
+
+def fp8_moe_route_workspace(tokens, experts) -> int:
+    return load().fp8_moe_route_workspace(tokens, experts)
+
+
+def fp8_moe_route(logits, dtype, tokens, experts, ld_logits, mask, topk, normalize, expert, weights, loss, counts, slope,
+                  workspace, workspace_bytes, stream=None) -> int:
+    return load().fp8_moe_route(_p(logits), dtype, tokens, experts, ld_logits, _p(mask), topk, normalize, _p(expert),
+                                _p(weights), _p(loss), _p(counts), _p(slope), _p(workspace), workspace_bytes,
+                                _stream(stream))
+
+
+def fp8_moe_balance(logits, dtype, tokens, experts, ld_logits, mask, expert, idx_dtype, topk, ld_expert, loss, counts,
+                    slope, workspace, workspace_bytes, stream=None) -> int:
+    return load().fp8_moe_balance(_p(logits), dtype, tokens, experts, ld_logits, _p(mask), _p(expert), idx_dtype, topk,
+                                  ld_expert, _p(loss), _p(counts), _p(slope), _p(workspace), workspace_bytes,
+                                  _stream(stream))
+
+
+def fp8_moe_route_backward(logits, dtype, tokens, experts, ld_logits, mask, expert, topk, dweights, normalize, slope, dloss,
+                           dlogits, ld_dlogits, stream=None) -> int:
+    return load().fp8_moe_route_backward(_p(logits), dtype, tokens, experts, ld_logits, _p(mask), _p(expert), topk,
+                                         _p(dweights), normalize, _p(slope), _p(dloss), _p(dlogits), ld_dlogits,
+                                         _stream(stream))
 
 
 def fp8_gemm_grouped(a, fmt_a, s_a, lda, b, fmt_b, s_b, ldb, stride_b, ld_sb, stride_sb, recipe, group, offsets,

@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8mi.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["gemm.hip", "quantize.hip", "norm.hip", "moe.hip", "history.hip", "api.cpp", "api_moe.cpp", "api_norm.cpp"]
+SOURCES = ["gemm.hip", "quantize.hip", "rms.hip", "norm.hip", "route.hip", "moe.hip", "history.hip", "api.cpp", "api_moe.cpp", "api_norm.cpp",
+           "api_rms.cpp", "api_route.cpp"]
 PROBE_LIB = os.path.join(HERE, "libfp8mi_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"

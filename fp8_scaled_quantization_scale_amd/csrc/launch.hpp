@@ -153,6 +153,56 @@ struct NormParams {
   float* workspace;
 };
 
+// RMS norm: forward (out: y), into codes (q's recipe and outputs), backward (x:
+// the rows the forward pass normed, residual: the gradient that reaches them by
+// itself, out: dx)
+struct RmsParams {
+  int x_dtype, w_dtype;
+  int64_t rows, cols;
+  const void* x;
+  int64_t ld_x;
+  const void* residual;
+  int64_t ld_residual;
+  const void* weight;
+  float eps;
+  void* total;
+  int64_t ld_total;
+  float* rstd;
+  void* out;
+  int64_t ld_out;
+  const void* dy;
+  int64_t ld_dy;
+  void* dweight;
+  float* workspace;
+  QuantParams q;
+};
+
+// the router: choices, counts and balance loss of logits (given: of choices
+// that the caller made, chosen), and the logits' gradient
+struct RouteParams {
+  const void* logits;
+  int dtype;
+  int64_t tokens, experts, ld;
+  const uint8_t* mask;
+  int64_t topk;
+  int normalize;
+  int32_t* expert;
+  float* weights;
+  bool given;
+  const void* chosen;
+  int idx_dtype;
+  int64_t ld_chosen;
+  float* loss;
+  int32_t* counts;
+  float* slope;
+  void* workspace;
+  // backward
+  const float* dweights;
+  const float* dloss;
+  void* dlogits;
+  int64_t ld_dlogits;
+};
+
 // FP8MI_OK, or FP8MI_ERR_HIP with the error's text kept for fp8_status_string
 int hip_status(hipError_t e);
 
@@ -176,5 +226,12 @@ hipError_t launch_moe_combine_backward(const MoeRowsParams& p, hipStream_t st);
 hipError_t launch_norm_forward(const NormParams& p, hipStream_t st);
 hipError_t launch_norm_backward(const NormParams& p, hipStream_t st);
 int64_t norm_partials(int64_t rows);
+hipError_t launch_rms_forward(const RmsParams& p, hipStream_t st);
+hipError_t launch_rms_quantize(const RmsParams& p, hipStream_t st);
+hipError_t launch_rms_backward(const RmsParams& p, hipStream_t st);
+int64_t rms_partials(int64_t rows);
+hipError_t launch_route(const RouteParams& p, hipStream_t st);
+hipError_t launch_route_backward(const RouteParams& p, hipStream_t st);
+int64_t route_blocks(int64_t tokens);
 
 }  // namespace fp8mi

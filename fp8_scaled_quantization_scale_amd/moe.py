@@ -1,9 +1,10 @@
-"""Experts over the libfp8mi C ABI: tokens sorted by expert and back, and the
-experts' scaled FP8 products on the sorted rows.
+"""Experts over the libfp8mi C ABI: the router, tokens sorted by expert and back,
+and the experts' scaled FP8 products on the sorted rows.
 
-    plan = moe.sort(expert, experts)              # expert: [tokens x topk] from the router
+    r = moe.route(logits, topk)                   # logits: [tokens x experts]; r.loss balances the experts
+    plan = moe.sort(r.expert, experts)
     h = up(x, plan, gather=True)                  # GroupedLinear: dispatch, cast and products
-    y = moe.combine(down(act(h), plan), plan, weights)
+    y = moe.combine(down(act(h), plan), plan, r.weights)
 
 The sorted buffers have ``plan.rows`` rows, the most that any routing needs;
 expert e's segment starts at ``plan.offsets[e]``, a multiple of 128, and ends
@@ -96,6 +97,173 @@ def _rows_matrix(name: str, t: torch.Tensor, rows: int) -> None:
         _matrix(name, t, tuple(_DTYPES))
     if t.shape[0] != rows:
         raise Fp8Error(f"{name} has {t.shape[0]} rows; needs {rows}")
+
+
+# ---------------------------------------------------------------------------
+# the router
+# ---------------------------------------------------------------------------
+
+class Routing(NamedTuple):
+    """What a router gives its experts."""
+    expert: torch.Tensor   # int32 [tokens x topk], -1 for no choice
+    weights: torch.Tensor  # float [tokens x topk], 0 for no choice
+    loss: torch.Tensor     # float scalar: experts * sum of f_e P_e, 1 where the load is even
+    counts: torch.Tensor   # int32 [experts] choices of each
+    slope: torch.Tensor    # float [experts]: the loss's derivative by each token's probability
+
+
+def _check_logits(logits, mask) -> None:
+    if not _is_matrix(logits, _DTYPES):
+        _matrix("logits", logits, tuple(_DTYPES))
+    if logits.shape[1] < 1:
+        raise Fp8Error("logits needs at least one expert")
+    if mask is not None:
+        if not _is_vector(mask, torch.bool, logits.shape[0]):
+            _vector("mask", mask, torch.bool, logits.shape[0])
+        if mask.numel() != logits.shape[0]:
+            raise Fp8Error(f"mask has {mask.numel()} elements; needs {logits.shape[0]}")
+        _one_device(logits, mask)
+
+
+def _sums(tokens: int, experts: int, dev):
+    """loss, counts, slope and the workspace of a forward pass."""
+    size = load().fp8_moe_route_workspace(tokens, experts)
+    if size < 0:
+        _check(size, "fp8_moe_route_workspace")
+    return (torch.empty((), dtype=torch.float32, device=dev), torch.empty(experts, dtype=torch.int32, device=dev),
+            torch.empty(experts, dtype=torch.float32, device=dev), torch.empty(size, dtype=torch.uint8, device=dev), size)
+
+
+def _route(logits, topk, normalize, mask, stream):
+    tokens, experts = logits.shape
+    dev = logits.device
+    with _scope(dev, stream):
+        loss, counts, slope, ws, size = _sums(tokens, experts, dev)
+        expert = torch.empty(tokens, max(topk, 0), dtype=torch.int32, device=dev)
+        weights = torch.empty(tokens, max(topk, 0), dtype=torch.float32, device=dev)
+        st = load().fp8_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, _ld(logits), _at(mask), topk,
+                                  normalize, expert.data_ptr(), weights.data_ptr(), loss.data_ptr(), counts.data_ptr(),
+                                  slope.data_ptr(), ws.data_ptr(), size, _here(dev))
+    _check(st, "fp8_moe_route")
+    return expert, weights, loss, counts, slope
+
+
+def _balance(logits, expert, mask, stream):
+    tokens, experts = logits.shape
+    dev = logits.device
+    with _scope(dev, stream):
+        loss, counts, slope, ws, size = _sums(tokens, experts, dev)
+        st = load().fp8_moe_balance(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, _ld(logits), _at(mask),
+                                    expert.data_ptr(), _IDX[expert.dtype], expert.shape[1], _ld(expert), loss.data_ptr(),
+                                    counts.data_ptr(), slope.data_ptr(), ws.data_ptr(), size, _here(dev))
+    _check(st, "fp8_moe_balance")
+    return loss, counts, slope
+
+
+def route_backward(logits: torch.Tensor, expert: torch.Tensor | None, dweights: torch.Tensor | None, slope: torch.Tensor,
+                   dloss: torch.Tensor | None, normalize: bool = True, mask: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The logits' gradient, of the weights' (dweights float [tokens x topk], with
+    the expert that route gave; None: without) and of the loss's (dloss, a float on
+    the device, with the slope of route or balance; None: without)."""
+    _check_logits(logits, mask)
+    tokens, experts = logits.shape
+    topk = 1
+    if dweights is not None:
+        if not (isinstance(expert, torch.Tensor) and expert.dim() == 2 and expert.shape[0] == tokens and expert.shape[1] >= 1):
+            raise Fp8Error(f"expert must be [{tokens} x topk]")
+        topk = expert.shape[1]
+        for name, t, dtype in (("expert", expert, torch.int32), ("dweights", dweights, torch.float32)):
+            if not _is_vector(t, dtype, tokens * topk):
+                _vector(name, t, dtype, tokens * topk)
+        if dweights.numel() != tokens * topk:
+            raise Fp8Error(f"dweights is {tuple(dweights.shape)}; needs {tokens} x {topk}")
+    else:
+        expert = None
+    if dloss is not None:
+        for name, t, n in (("dloss", dloss, 1), ("slope", slope, experts)):
+            if not _is_vector(t, torch.float32, n):
+                _vector(name, t, torch.float32, n)
+    else:
+        slope = None
+    _one_device(logits, expert, dweights, slope, dloss)
+    dev = logits.device
+    with _scope(dev, stream):
+        dlogits = torch.empty(tokens, experts, dtype=logits.dtype, device=dev)
+        st = load().fp8_moe_route_backward(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, _ld(logits), _at(mask),
+                                           _at(expert), topk, _at(dweights), normalize, _at(slope), _at(dloss),
+                                           dlogits.data_ptr(), experts, _here(dev))
+    _check(st, "fp8_moe_route_backward")
+    return dlogits
+
+
+class _RouteFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk, normalize, mask):
+        ctx.set_materialize_grads(False)
+        expert, weights, loss, counts, slope = _route(logits, topk, normalize, mask, None)
+        ctx.normalize = normalize
+        ctx.mark_non_differentiable(expert, counts, slope)
+        ctx.save_for_backward(logits, expert, slope, mask)
+        return expert, weights, loss, counts, slope
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, dweights, dloss, *__):
+        logits, expert, slope, mask = ctx.saved_tensors
+        if dweights is None and dloss is None:
+            return None, None, None, None
+        dweights = None if dweights is None else _dense(dweights)
+        return route_backward(logits, expert, dweights, slope, dloss, ctx.normalize, mask), None, None, None
+
+
+class _BalanceFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, expert, mask):
+        ctx.set_materialize_grads(False)
+        loss, counts, slope = _balance(logits, expert, mask, None)
+        ctx.mark_non_differentiable(counts, slope)
+        ctx.save_for_backward(logits, slope, mask)
+        return loss, counts, slope
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, *_):
+        logits, slope, mask = ctx.saved_tensors
+        return None if dloss is None else route_backward(logits, None, None, slope, dloss, mask=mask), None, None
+
+
+def route(logits: torch.Tensor, topk: int, normalize: bool = True, mask: torch.Tensor | None = None,
+          stream=None) -> Routing:
+    """Each token's ``topk`` experts of the largest logits [tokens x experts] (BF16
+    or FP32, the lowest expert first among equal ones), their weights (softmax over
+    all experts; normalize: divided by their sum), and the balance loss of the
+    choices.  mask (bool [tokens]) leaves tokens out, and so does a row of -inf;
+    a choice that would fall on -inf is none (-1).  weights and loss are
+    differentiable in the logits, once and in reverse mode (on the current stream)."""
+    _check_logits(logits, mask)
+    if not 1 <= topk <= logits.shape[1]:
+        raise Fp8Error(f"topk must be in [1, {logits.shape[1]}]")
+    if _wants_grad(logits):
+        _need(stream is None, "with gradients, a call runs on the current stream")
+        return Routing(*_RouteFn.apply(logits, topk, bool(normalize), mask))
+    return Routing(*_route(logits, topk, bool(normalize), mask, stream))
+
+
+def balance(logits: torch.Tensor, expert: torch.Tensor, mask: torch.Tensor | None = None, stream=None):
+    """(loss, counts, slope) of choices that another rule made: expert [tokens x
+    topk], int32 or int64; numbers outside the experts are not counted.  loss is
+    differentiable in the logits as route's is."""
+    _check_logits(logits, mask)
+    if not _is_matrix(expert, _IDX):
+        raise Fp8Error("expert must be a 2-D int32 or int64 device tensor with unit column stride")
+    if expert.shape[0] != logits.shape[0] or expert.shape[1] < 1:
+        raise Fp8Error(f"expert is {tuple(expert.shape)}; needs {logits.shape[0]} rows and at least one choice")
+    _one_device(logits, expert)
+    if _wants_grad(logits):
+        _need(stream is None, "with gradients, a call runs on the current stream")
+        return _BalanceFn.apply(logits, expert, mask)
+    return _balance(logits, expert, mask, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -196,7 +364,7 @@ class _CombineFn(torch.autograd.Function):
 def _wants_grad(*tensors) -> bool:
     for t in tensors:  # (a dual tensor need not require grad: its tangent would be lost without a word)
         if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
-            raise Fp8Error("dispatch and combine have no forward-mode derivative")
+            raise Fp8Error("dispatch, combine and the router have no forward-mode derivative")
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 

@@ -307,6 +307,54 @@ int fp8_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int x_
                             void* dx, int64_t ld_dx, void* dweight, void* dbias,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---- RMS norm ---------------------------------------------------------------
+ * Root-mean-square norm of the rows of x [rows x cols], after the addition of a
+ * residual of x's type, to x's type or straight to FP8 codes.  Conventions as
+ * for the layer norm: FP32 statistics and sums, each output rounded once, no
+ * output overlapping an input, cols >= 1 (at most 2^28). */
+
+/* fp8_rms_norm_forward --
+ *   t = x + residual, rounded to x's type (residual NULL: t = x),
+ *   rstd = 1 / sqrt(sum(t^2) / cols + eps), y = t * rstd * weight.
+ *   total : where t goes, the residual stream's new value and what the backward
+ *           pass takes; not used without a residual.
+ *   weight: [cols] of w_dtype, NULL for 1; rstd: float [rows]; eps >= 0.
+ *   The squares are summed in FP32: sum(t^2) has to stay below 2^128. */
+int fp8_rms_norm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                         const void* residual, int64_t ld_residual, const void* weight, int w_dtype, float eps,
+                         void* total, int64_t ld_total, void* y, int64_t ld_y, float* rstd, void* stream);
+
+/* fp8_rms_norm_quantize -- the FP8 codes and scales of y in place of y: as
+ * fp8_quantize of a [rows x cols] matrix that holds y in FP32 (y is not rounded
+ * to x's type first).  recipe: BLOCK_1x128, MX_1x32 or MX_1x32_OCP (others:
+ * FP8MI_ERR_UNSUPPORTED).  x, residual and total need the alignment of their
+ * element only; outputs, scale layouts, alignment and nonfinite as for
+ * fp8_quantize; total, rstd and the other arguments as for
+ * fp8_rms_norm_forward.  COL outputs take a second launch, which reads t
+ * again. */
+int fp8_rms_norm_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                          const void* residual, int64_t ld_residual, const void* weight, int w_dtype, float eps,
+                          void* total, int64_t ld_total, float* rstd, int recipe, int fmt, int orient, int margin,
+                          uint8_t* q_row, int64_t ld_q_row, void* s_row, uint8_t* q_col, int64_t ld_q_col, void* s_col,
+                          int32_t* nonfinite, void* stream);
+
+/* fp8_rms_norm_workspace -- bytes of device memory that the weight's gradient
+ * needs (each workgroup's column sums); negative: an error. */
+int64_t fp8_rms_norm_workspace(int64_t rows, int64_t cols);
+
+/* fp8_rms_norm_backward -- with n = t rstd, g = dy * weight:
+ *   dx = rstd * (g - n * sum(g n) / cols) + dtotal, the gradient of x and of the
+ *   residual alike; dweight = sum over rows of dy n.
+ *   total : the rows that were normed (x, without a residual); dtotal: the
+ *   gradient that reaches them by itself, NULL for none; dweight ([cols] of
+ *   w_dtype) may be NULL; with it, workspace holds fp8_rms_norm_workspace(rows,
+ *   cols) bytes, which calls that overlap in time may not share.  Sums are added
+ *   in a fixed order.  rows == 0 writes a zero dweight. */
+int fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* total, int x_dtype, int64_t rows, int64_t cols,
+                          int64_t ld_total, const void* weight, int w_dtype, const float* rstd, const void* dtotal,
+                          int64_t ld_dtotal, void* dx, int64_t ld_dx, void* dweight, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
 /* ---- experts ----------------------------------------------------------------
  * A router gives token t the experts expert[t][0 .. topk).  Slot s = t * topk +
  * j is one of these choices; a slot whose expert lies outside [0, experts) is
@@ -382,6 +430,54 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
                              const void* ys, int64_t ld_ys, const int32_t* slot_row, const int32_t* offsets,
                              const int32_t* counts, int64_t experts, int64_t topk, const float* weights,
                              void* dys, int64_t rows, int64_t ld_dys, float* dweights, void* stream);
+
+/* Bytes of device memory that fp8_moe_route and fp8_moe_balance need; negative:
+ * an error. */
+int64_t fp8_moe_route_workspace(int64_t tokens, int64_t experts);
+
+/* fp8_moe_route -- the router: from each token's logits to its experts, their
+ * weights and the balance loss.
+ *   logits  : [tokens x experts] BF16 or FP32; p = softmax over a token's.
+ *   mask    : bytes [tokens], 0 for a token that is left out (padding); NULL:
+ *             none.  A token whose logits are all -inf is left out too.
+ *   expert  : int32 [tokens x topk], the experts of the topk largest logits, the
+ *             lowest expert first among equal ones; -1 where a token is left out
+ *             or has no more logits above -inf.  topk <= experts.  (NaN counts
+ *             as the largest; its token's weights and the loss are NaN.)
+ *   weights : float [tokens x topk], p of the experts, or with normalize that
+ *             divided by its sum over the token's choices; 0 where expert is -1.
+ *   counts  : int32 [experts], choices of each expert.
+ *   loss    : float, experts * sum over e of f_e P_e with f_e = counts[e] / (n
+ *             topk) and P_e the mean of p over the n tokens that are not left
+ *             out (1 where both are even); 0 with n = 0.
+ *   slope   : float [experts], experts f_e / n: the derivative of loss by p[t][e],
+ *             the same for all tokens, which the backward pass takes.
+ *   workspace: fp8_moe_route_workspace bytes; calls that overlap in time may not
+ *             share it.  Sums are added in a fixed order. */
+int fp8_moe_route(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld_logits,
+                  const uint8_t* mask, int64_t topk, int normalize, int32_t* expert, float* weights, float* loss,
+                  int32_t* counts, float* slope, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* fp8_moe_balance -- counts, loss and slope of choices that the caller made:
+ * expert [tokens x topk] int32 or int64 (idx_dtype) with ld_expert; numbers
+ * outside [0, experts), and those of tokens that are left out, are not counted.
+ * The rest as for fp8_moe_route. */
+int fp8_moe_balance(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld_logits,
+                    const uint8_t* mask, const void* expert, int idx_dtype, int64_t topk, int64_t ld_expert,
+                    float* loss, int32_t* counts, float* slope, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* fp8_moe_route_backward -- the gradient of the logits:
+ *   dp[t][e] = dloss * slope[e] + (dweights[t][j] where expert[t][j] is e),
+ *   dlogits = p * (dp - sum over e of p dp);
+ *   with normalize, the weights' part is w_j (dweights_j - sum over i of w_i
+ *   dweights_i) at expert[t][j] instead.
+ *   expert, slope: as fp8_moe_route left them; dweights float [tokens x topk]
+ *   (NULL: none; expert and topk are not used then); dloss: a float on the
+ *   device (NULL: none).  dlogits as logits; zeros for a token left out. */
+int fp8_moe_route_backward(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld_logits,
+                           const uint8_t* mask, const int32_t* expert, int64_t topk, const float* dweights,
+                           int normalize, const float* slope, const float* dloss, void* dlogits, int64_t ld_dlogits,
+                           void* stream);
 
 /* which index of the products the experts share out (fp8_gemm_grouped) */
 #define FP8MI_GROUP_ROWS 0

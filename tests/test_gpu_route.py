@@ -1,0 +1,429 @@
+"""The experts' router (moe.route, moe.balance, moe.route_backward) against plain
+definitions in float64.
+
+Tolerances, derived before the first run, in steps of 2^-24 (half a step of
+binary32).  With x = l - max, e^x is off by at most 3 |x| + 4 steps of itself (x
+and x log2(e) are rounded, log2(e) is, and the exponential's own 2), a sum over the
+experts by 70 more (at most 64 in a lane, 4 across), so a probability or weight by
+K = 4 max|x| + 160, counting the quotient.  The loss adds up positive terms, at
+most tokens / 8192 one after the other in a register: K + 64 + tokens / 8192.  A
+gradient subtracts: p |slope dloss| + p sum p |slope dloss| + w |dw| + w sum w |dw|
+are its terms, each off by at most 3 K steps of itself."""
+import pytest
+import torch
+
+import fp8_scaled_quantization_scale_amd as fm
+from fp8_scaled_quantization_scale_amd import linear, moe, norm
+from gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+E32 = 2.0 ** -24
+TINY = 2.0 ** -120  # what a result below binary32's normal range may be off by
+U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+B, F = torch.bfloat16, torch.float32
+INF = float("inf")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _logits(tokens, experts, dt, seed=0, ld=None):
+    g = _gen(seed + 7 * tokens + experts)
+    x = 2.0 * torch.randn(tokens, ld or experts, generator=g, device="cuda") + torch.randn(1, ld or experts, generator=g, device="cuda")
+    return x.to(dt)[:, :experts]
+
+
+def _reference(logits, topk, normalize, mask, expert=None):
+    """expert, weights, loss, counts, slope, p in 64 bits; expert given: of those choices."""
+    l = logits.double()
+    t, e = l.shape
+    real = (l > -INF).any(1)
+    if mask is not None:
+        real &= mask
+    p = torch.softmax(torch.where(real[:, None], l, 0.0), 1) * real[:, None]
+    if expert is None:
+        top = torch.sort(l, dim=1, descending=True, stable=True)
+        expert = torch.where(real[:, None] & (top.values[:, :topk] > -INF), top.indices[:, :topk], -1)
+    expert = expert.long()
+    kept = (expert >= 0) & (expert < e) & real[:, None]
+    w = torch.where(kept, p.gather(1, expert.clamp(0, e - 1)), 0.0)
+    if normalize:
+        s = w.sum(1, keepdim=True)
+        w = torch.where(s > 0, w / s, 0.0)
+    counts = torch.bincount(expert[kept], minlength=e)
+    n = int(real.sum())
+    slope = counts.double() * e / (topk * n * n) if n else torch.zeros(e, dtype=torch.float64, device="cuda")
+    return expert, w, (slope * p.sum(0)).sum(), counts, slope, p
+
+
+def _steps(logits, real=None):
+    l = logits.double()
+    x = (l.amax(1, keepdim=True) - l)[l > -INF]
+    return (4 * min(float(x.max()) if x.numel() else 0.0, 150.0) + 160) * E32  # (beyond 150 all is below TINY)
+
+
+def _check(r, logits, topk, normalize, mask):
+    expert, w, loss, counts, slope, _ = _reference(logits, topk, normalize, mask)
+    assert torch.equal(r.expert.long(), expert), "expert"
+    k = _steps(logits)
+    assert ((r.weights.double() - w).abs() <= k * w + TINY).all(), "weights"
+    assert torch.equal(r.counts.long(), counts), "counts"
+    assert ((r.slope.double() - slope).abs() <= 4 * E32 * slope).all(), "slope"
+    assert abs(r.loss.double() - loss) <= (k + (64 + logits.shape[0] / 8192) * E32) * loss, "loss"
+    assert r.expert.dtype == r.counts.dtype == torch.int32 and r.weights.dtype == r.loss.dtype == r.slope.dtype == F
+
+
+# every number of experts a lane may hold and its borders, odd sizes and strides
+SHAPES = [(1, 1, 1, F), (1, 8, 2, F), (5, 16, 16, B), (7, 17, 3, F), (128, 8, 2, F), (100, 33, 8, B), (333, 64, 4, F), (64, 65, 6, B),
+          (50, 100, 16, F), (1000, 128, 8, B), (31, 129, 17, F), (2100, 256, 8, B), (17, 257, 20, F), (40, 512, 40, B), (9, 600, 64, F),
+          (33, 1024, 8, B), (3, 1000, 1000, F), (20000, 16, 2, F), (9000, 64, 8, B)]
+
+
+@pytest.mark.parametrize("tokens,experts,topk,dt", SHAPES, ids=[f"{t}x{e}top{k}" for t, e, k, _ in SHAPES])
+def test_forward(tokens, experts, topk, dt):
+    need_gpu()
+    mask = torch.rand(tokens, generator=_gen(1), device="cuda") < 0.8
+    for ld, m, normalize in ((experts, None, True), (experts + 3, mask, False), (experts + 8, mask, True)):
+        logits = _logits(tokens, experts, dt, 0, ld)
+        r = moe.route(logits, topk, normalize, m)
+        _check(r, logits, topk, normalize, m)
+        again = moe.route(logits, topk, normalize, m)
+        assert all(torch.equal(a, b) for a, b in zip(r, again))  # fixed order of addition
+        # the same choices given: the same sums, whatever their integers' width and stride
+        wide = torch.full((tokens, topk + 2), 5, dtype=torch.int64, device="cuda")
+        wide[:, :topk] = r.expert
+        for given in (r.expert, wide[:, :topk]):
+            loss, counts, slope = moe.balance(logits, given, m)
+            assert torch.equal(loss, r.loss) and torch.equal(counts, r.counts) and torch.equal(slope, r.slope)
+
+
+def test_ties_and_zeros():
+    """Equal logits go to the lowest expert, and -0 is 0."""
+    need_gpu()
+    for experts in (5, 16, 40, 64, 200, 256, 1024):
+        r = moe.route(torch.zeros(9, experts, device="cuda"), min(5, experts))
+        assert torch.equal(r.expert, torch.arange(min(5, experts), device="cuda", dtype=torch.int32).expand(9, -1))
+        assert abs(r.loss - 1.0) <= 230 * E32  # (even P: 1 whatever the counts)
+        l = torch.randint(0, 3, (50, experts), generator=_gen(experts), device="cuda").float() * torch.where(
+            torch.rand(50, experts, generator=_gen(2), device="cuda") < 0.5, -1.0, 1.0)
+        for dt in (F, B):
+            _check(moe.route(l.to(dt), min(8, experts)), l.to(dt), min(8, experts), True, None)
+
+
+@pytest.mark.parametrize("experts", [8, 64, 300])
+def test_closed_experts_and_tokens_left_out(experts):
+    """Logits of -inf are never chosen and have no weight; a token of nothing else
+    is left out, like a masked one whatever its logits hold; the type's lowest
+    value is a logit like others."""
+    need_gpu()
+    l = _logits(40, experts, F)
+    l[:, 3] = -INF
+    l[5] = -INF
+    l[6, 2:] = -INF
+    l[7] = torch.finfo(F).min
+    l[8, 1:] = torch.finfo(F).min
+    l[9, : experts - 1] = -INF
+    mask = torch.ones(40, dtype=torch.bool, device="cuda")
+    mask[10:13] = False
+    l[10], l[11], l[12, 0] = float("nan"), INF, INF
+    for normalize in (True, False):
+        clean = l.clone()
+        clean[10:13] = 0.0
+        r = moe.route(l, 4, normalize, mask)
+        _check(r, clean, 4, normalize, mask)
+        assert (r.expert[5] == -1).all() and (r.expert[10:13] == -1).all() and not r.weights[10:13].any() and not r.weights[5].any()
+        assert torch.equal(r.expert[6], torch.tensor([r.expert[6, 0], r.expert[6, 1], -1, -1], device="cuda", dtype=torch.int32))
+        closed = torch.arange(40, device="cuda")  # all rows but the two of lowest values, whose expert 3 is open
+        closed = closed[(closed != 7) & (closed != 8)]
+        assert not (r.expert[closed] == 3).any()
+        d = moe.route_backward(l, r.expert, torch.randn(40, 4, device="cuda"), r.slope, torch.ones((), device="cuda"), normalize, mask)
+        assert d.isfinite().all() and not d[5].any() and not d[10:13].any() and not d[closed, 3].any()
+    # nobody left
+    nobody = torch.zeros(40, dtype=torch.bool, device="cuda")
+    r = moe.route(l, 2, True, nobody)
+    assert (r.expert == -1).all() and not r.weights.any() and r.loss == 0 and not r.counts.any() and not r.slope.any()
+    d = moe.route_backward(l, r.expert, torch.ones(40, 2, device="cuda"), r.slope, torch.ones((), device="cuda"), True, nobody)
+    assert not d.any()
+
+
+@pytest.mark.parametrize("experts,topk", [(8, 2), (64, 8), (100, 20)])
+def test_nan_and_inf_logits(experts, topk):
+    """NaN and +inf spoil their own token's weights, and the loss; its choices stay
+    in range and differ, and other tokens keep theirs."""
+    need_gpu()
+    l = _logits(30, experts, F)
+    want = moe.route(l, topk)
+    bad = l.clone()
+    bad[4, 5], bad[9, 0], bad[9, 1], bad[13] = float("nan"), INF, INF, float("nan")
+    r = moe.route(bad, topk)
+    keep = torch.tensor([i for i in range(30) if i not in (4, 9, 13)], device="cuda")
+    assert torch.equal(r.expert[keep], want.expert[keep]) and torch.equal(r.weights[keep], want.weights[keep])
+    assert r.loss.isnan() and r.expert[4, 0] == 5 and r.expert[9, 0] == 0 and r.expert[9, 1] == 1
+    assert r.weights[4].isnan().all() and r.weights[13].isnan().all() and r.weights[9].isnan().any()
+    assert ((r.expert >= 0) & (r.expert < experts)).all()
+    assert all(len(set(row)) == topk for row in r.expert.tolist()) and int(r.counts.sum()) == 30 * topk
+    d = moe.route_backward(bad, r.expert, torch.ones(30, topk, device="cuda"), want.slope, torch.ones((), device="cuda"))
+    assert d[keep].isfinite().all() and d[4].isnan().all() and d[13].isnan().all()
+
+
+def test_no_tokens():
+    need_gpu()
+    l = torch.zeros(0, 8, device="cuda", requires_grad=True)
+    r = moe.route(l, 2)
+    assert r.expert.shape == r.weights.shape == (0, 2) and r.loss == 0 and not r.counts.any() and not r.slope.any()
+    (r.loss + r.weights.sum()).backward()
+    assert l.grad.shape == (0, 8)
+
+
+def test_given_choices_may_be_anything():
+    """Numbers outside the experts and repeated ones: the first are not counted,
+    the second each time."""
+    need_gpu()
+    l = _logits(300, 12, F)
+    given = torch.randint(-3, 15, (300, 5), generator=_gen(4), device="cuda")
+    given[0] = 7
+    given[1] = torch.tensor([1 << 40, -(1 << 40), (1 << 32) + 3, 12, -1], device="cuda")
+    loss, counts, slope = moe.balance(l, given)
+    _, _, want, c, s, _ = _reference(l, 5, False, None, given)
+    assert torch.equal(counts.long(), c) and abs(loss.double() - want) <= (_steps(l) + 64 * E32) * want
+    assert ((slope.double() - s).abs() <= 4 * E32 * s).all()
+
+
+def _grad_check(d, logits, expert, dweights, slope, dloss, normalize, mask):
+    """against the formula in 64 bits, by autograd"""
+    l = logits.double().requires_grad_()
+    real = (logits.float() > -INF).any(1)
+    if mask is not None:
+        real &= mask
+    p = torch.softmax(torch.where(real[:, None], l, 0.0), 1) * real[:, None]
+    out = (p * slope.double()).sum() * dloss.double() if dloss is not None else 0.0
+    size = noise = 0.0
+    if dloss is not None:
+        a = (slope.double() * dloss.double()).abs()
+        size = size + p * (a + (p * a).sum(1, keepdim=True))
+    if dweights is not None:
+        at = expert.long().clamp(min=0)
+        kept = expert >= 0
+        w = torch.where(kept, p.gather(1, at), 0.0)
+        dw = torch.where(kept, dweights.double(), 0.0)
+        if normalize:
+            s = w.sum(1, keepdim=True)
+            w = torch.where(s > 0, w / torch.where(s > 0, s, 1.0), 0.0)
+        out = out + (w * dw).sum()
+        along = (w * dw.abs()).sum(1, keepdim=True)
+        size = size + torch.zeros_like(p).scatter_add(1, at, torch.where(kept, w * (dw.abs() + along), 0.0)) + (0.0 if normalize else p * along)
+        # with normalize, the gradient of a logit that is not chosen is 0; autograd's is the
+        # difference of two sums of p w dw in 64 bits, off by fewer than 2^7 half steps of
+        # 2^-53 of it: 2^-46, which is 2^-22 of a binary32 step
+        noise = 2.0 ** -46 * p * along
+    ref, = torch.autograd.grad(out, l)
+    bad = (d.double() - ref).abs() > U[d.dtype] * ref.abs() + 3 * _steps(logits) * torch.as_tensor(size).detach() + noise + TINY
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} out of tolerance"
+
+
+@pytest.mark.parametrize("tokens,experts,topk,dt", SHAPES, ids=[f"{t}x{e}top{k}" for t, e, k, _ in SHAPES])
+def test_backward(tokens, experts, topk, dt):
+    need_gpu()
+    mask = torch.rand(tokens, generator=_gen(1), device="cuda") < 0.8
+    for ld, m, normalize in ((experts, None, True), (experts + 3, mask, False), (experts + 8, mask, True)):
+        logits = _logits(tokens, experts, dt, 1, ld)
+        r = moe.route(logits, topk, normalize, m)
+        dw = torch.randn(tokens, topk, generator=_gen(2), device="cuda")
+        dloss = torch.rand((), generator=_gen(3), device="cuda") * tokens
+        for dweights, dl in ((dw, dloss), (dw, None), (None, dloss)):
+            d = moe.route_backward(logits, r.expert, dweights, r.slope, dl, normalize, m)
+            assert d.dtype == dt and d.shape == logits.shape
+            _grad_check(d, logits, r.expert, dweights, r.slope, dl, normalize, m)
+        assert not moe.route_backward(logits, None, None, None, None, normalize, m).any()
+
+
+def test_autograd():
+    """Through the layer's own calls: weights and loss together and alone, leading
+    strides and BF16, and balance."""
+    need_gpu()
+    for dt in (F, B):
+        base = _logits(200, 64, dt, 5, 72).detach()
+        l = base.clone()[:, :64].requires_grad_()
+        r = moe.route(l, 4)
+        dw, dl = torch.randn(200, 4, device="cuda"), torch.rand((), device="cuda")
+        torch.autograd.backward([r.weights, r.loss], [dw, dl])
+        want = moe.route_backward(l.detach(), r.expert, dw, r.slope, dl)
+        assert torch.equal(l.grad, want) and not r.expert.requires_grad and not r.counts.requires_grad and not r.slope.requires_grad
+        l.grad = None
+        (0.01 * moe.route(l, 4).loss).backward()
+        assert torch.equal(l.grad, moe.route_backward(l.detach(), None, None, r.slope, torch.full((), 0.01, device="cuda")))
+        l.grad = None
+        loss, _, slope = moe.balance(l, r.expert)
+        loss.backward()
+        assert torch.equal(l.grad, moe.route_backward(l.detach(), None, None, slope, torch.ones((), device="cuda")))
+        l.grad = None
+        moe.route(l, 4).weights.t()[0].sum().backward()  # a gradient with strides of its own
+        one = torch.zeros(200, 4, device="cuda")
+        one[:, 0] = 1
+        assert torch.equal(l.grad, moe.route_backward(l.detach(), r.expert, one, None, None))
+
+
+def test_gradient_against_differences():
+    """In 64 bits, of the definition (the choices and counts held still)."""
+    need_gpu()
+    l = _logits(20, 12, F, 8)
+    for normalize in (True, False):
+        r = moe.route(l, 3, normalize)
+        dw = torch.randn(20, 3, generator=_gen(4), device="cuda")
+        grad = moe.route_backward(l, r.expert, dw, r.slope, torch.full((), 20.0, device="cuda"), normalize).double()
+
+        def loss(x):
+            p = torch.softmax(x, 1)
+            w = p.gather(1, r.expert.long())
+            w = w / w.sum(1, keepdim=True) if normalize else w
+            return (w * dw.double()).sum() + 20.0 * (p * r.slope.double()).sum()
+
+        d = torch.randn(20, 12, generator=_gen(6), device="cuda", dtype=torch.float64)
+        slope = (loss(l.double() + 1e-5 * d) - loss(l.double() - 1e-5 * d)) / 2e-5
+        assert abs(slope - (grad * d).sum()) <= 2e-5 * (grad * d).abs().sum() + 1e-8
+
+
+def test_neighbours_are_left_alone():
+    need_gpu()
+    tokens, experts, topk = 203, 40, 5
+    l = _logits(tokens, experts, B)
+    want = moe.route(l, topk)
+    i = lambda n: torch.full((n + 2,), 7, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = lambda n: torch.full((n + 2,), 7.0, device="cuda")  # noqa: E731
+    size = fm.fp8_moe_route_workspace(tokens, experts)
+    expert, weights, loss, counts, slope, ws = i(tokens * topk), f(tokens * topk), f(1), i(experts), f(experts), f(size // 4)
+    assert fm.fp8_moe_route(l, fm.IN_BF16, tokens, experts, experts, None, topk, 1, expert[1:], weights[1:], loss[1:], counts[1:],
+                            slope[1:], ws[1:], size) == fm.OK
+    for got, ref in ((expert, want.expert), (weights, want.weights), (loss, want.loss), (counts, want.counts), (slope, want.slope)):
+        assert torch.equal(got[1:-1], ref.reshape(-1)) and got[0] == 7 and got[-1] == 7
+    assert ws[0] == 7 and ws[-1] == 7
+    out = torch.full((tokens + 2, experts + 5), 7.0, dtype=B, device="cuda")
+    dw = torch.randn(tokens, topk, device="cuda")
+    assert fm.fp8_moe_route_backward(l, fm.IN_BF16, tokens, experts, experts, None, want.expert, topk, dw, 1, want.slope, want.loss,
+                                     out[1:], experts + 5) == fm.OK
+    assert torch.equal(out[1:-1, :experts], moe.route_backward(l, want.expert, dw, want.slope, want.loss))
+    assert (out[0] == 7).all() and (out[-1] == 7).all() and (out[:, experts:] == 7).all()
+
+
+def test_expert_block_eager_and_captured():
+    """A block of norm, router, sort, experts and combine with its backward pass,
+    eager and in a graph replayed with other inputs between eager work."""
+    need_gpu()
+    tokens, width, experts, topk = 256, 256, 8, 2
+    rec = linear.Float8BlockScaling()
+    rms = norm.RMSNorm(width, device="cuda")
+    router = torch.nn.Linear(width, experts, bias=False, device="cuda", dtype=B)
+    up = moe.GroupedLinear(experts, width, 512, rec, device="cuda")
+    down = moe.GroupedLinear(experts, 512, width, rec, device="cuda")
+    params = [rms.weight, router.weight, up.weight, down.weight]
+    mask = torch.ones(tokens, dtype=torch.bool, device="cuda")
+
+    def step(x, res, dy, mask):
+        x, res = x.detach().requires_grad_(), res.detach().requires_grad_()
+        n, total = rms(x, res)
+        r = moe.route(router(n).float(), topk, True, mask)
+        p = moe.sort(r.expert, experts)
+        y = total + moe.combine(down(torch.nn.functional.silu(up(n, p, gather=True)), p), p, r.weights)
+        grads = torch.autograd.grad([y, r.loss], [x, res, *params], [dy, torch.full_like(r.loss, 0.5)])
+        return tuple(t.detach() for t in (y, *r[:4], *grads))  # (no graph outlives its step)
+
+    def inputs(seed):
+        g = _gen(seed)
+        x, res, dy = (torch.randn(tokens, width, generator=g, device="cuda").to(B) for _ in range(3))
+        return x, res, dy, torch.rand(tokens, generator=g, device="cuda") < 0.9
+
+    static = [t.clone() for t in inputs(1)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(*static)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*static)
+    for seed in (2, 3, 4, 1):
+        fresh = inputs(seed)
+        want = step(*fresh)
+        torch.cuda.synchronize()
+        for a, b in zip(static, fresh):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(t.isfinite().all() for t in want if t.is_floating_point())
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), seed
+        # padding takes no part: its rows pass through, and its gradient is the residual's
+        off = ~fresh[3]
+        assert (want[1][off] == -1).all() and torch.equal(want[0][off], (fresh[0] + fresh[1])[off])
+        assert int(want[4].sum()) == topk * int(fresh[3].sum())
+
+
+def test_side_stream():
+    need_gpu()
+    l = _logits(500, 64, F)
+    want = moe.route(l, 4)
+    d = moe.route_backward(l, want.expert, want.weights, want.slope, want.loss)
+    torch.cuda.synchronize()
+    for raw in (False, True):
+        s = torch.cuda.Stream()
+        arg = s.cuda_stream if raw else s
+        r = moe.route(l, 4, stream=arg)
+        b = moe.balance(l, r.expert, stream=arg)
+        got = moe.route_backward(l, r.expert, r.weights, r.slope, r.loss, stream=arg)
+        s.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(r, want)) and torch.equal(got, d) and torch.equal(b[0], want.loss)
+
+
+def test_offsets_past_32_bits():
+    """Logits of more than 4 GiB: the last tokens, and the sums over all."""
+    need_gpu()
+    tokens, experts, topk = 2200000, 512, 2
+    g = _gen(1)
+    l = torch.randn(tokens, experts, generator=g, device="cuda")
+    l[:, 0] += 3.0
+    r = moe.route(l, topk)
+    few = moe.route(l[-50:].clone(), topk)
+    assert torch.equal(r.expert[-50:], few.expert) and torch.equal(r.weights[-50:], few.weights)
+    assert torch.equal(r.counts.long(), torch.bincount(r.expert.reshape(-1).long(), minlength=experts))
+    total = torch.zeros(experts, dtype=torch.float64, device="cuda")
+    for i in range(0, tokens, 200000):
+        total += torch.softmax(l[i:i + 200000].double(), 1).sum(0)
+    ref = (r.slope.double() * total).sum()
+    assert abs(r.loss.double() - ref) <= (4 * 16 + 160 + 64 + tokens / 8192) * E32 * ref
+    dw = torch.ones(tokens, topk, device="cuda")
+    dw[:, 1] = -1
+    d = moe.route_backward(l, r.expert, dw, r.slope, r.loss)
+    # (the slope is all tokens', the rest a token's own)
+    assert torch.equal(d[-50:], moe.route_backward(l[-50:].clone(), few.expert, dw[-50:].clone(), r.slope, r.loss))
+
+
+def test_refusals():
+    need_gpu()
+    l = _logits(20, 8, F)
+    r = moe.route(l, 2)
+    i64 = r.expert.long()
+    dw, one = torch.ones(20, 2, device="cuda"), torch.ones((), device="cuda")
+    mask = torch.ones(20, dtype=torch.bool, device="cuda")
+    back = moe.route_backward
+    for bad in (lambda: moe.route(l.half(), 2), lambda: moe.route(l[0], 2), lambda: moe.route(l.t(), 2), lambda: moe.route(l, 0),
+                lambda: moe.route(l, 9), lambda: moe.route(l[:, :0], 1), lambda: moe.route(l[:1].expand(20, 8), 2),
+                lambda: moe.route(torch.zeros(2, 1025, device="cuda"), 2), lambda: moe.route(l, 2, True, mask[:19]),
+                lambda: moe.route(l, 2, True, mask.int()), lambda: moe.route(l, 2, True, mask.cpu()),
+                lambda: moe.route(l, 2, True, torch.ones(21, dtype=torch.bool, device="cuda")),
+                lambda: moe.route(l.clone().requires_grad_(), 2, stream=torch.cuda.Stream()),
+                lambda: moe.balance(l, i64[:19]), lambda: moe.balance(l, i64.float()), lambda: moe.balance(l, i64[:, :0]),
+                lambda: moe.balance(l, i64.cpu()), lambda: moe.balance(l, i64[:1].expand(20, 2)),
+                lambda: back(l, i64, dw, r.slope, one), lambda: back(l, r.expert, dw[:19], r.slope, one),
+                lambda: back(l, r.expert[:19], dw, r.slope, one), lambda: back(l, None, dw, r.slope, one),
+                lambda: back(l, r.expert, dw.double(), r.slope, one), lambda: back(l, r.expert, dw, r.slope[:7], one),
+                lambda: back(l, r.expert, dw, None, one), lambda: back(l, r.expert, dw, r.slope, one.double())):
+        with pytest.raises(fm.Fp8Error):
+            bad()
+    # the gradient's own gradient is not there
+    x = l.clone().requires_grad_()
+    g, = torch.autograd.grad(moe.route(x, 2).loss, x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
