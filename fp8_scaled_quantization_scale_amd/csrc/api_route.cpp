@@ -25,8 +25,9 @@ int check_routing(int dtype, int64_t tokens, int64_t experts, int64_t topk) {
 
 int check_sums(int64_t tokens, int64_t experts, const float* loss, const int32_t* counts, const float* slope,
                const void* workspace, int64_t workspace_bytes) {
-  if (!loss || !counts || !slope || !workspace) return FP8MI_ERR_NULL;
-  if (workspace_bytes < fp8_moe_route_workspace(tokens, experts)) return FP8MI_ERR_SHAPE;
+  const int64_t need = fp8_moe_route_workspace(tokens, experts);
+  if (!loss || !counts || !slope || (need > 0 && !workspace)) return FP8MI_ERR_NULL;
+  if (workspace_bytes < need) return FP8MI_ERR_SHAPE;
   return aligned_to(loss, 4) && aligned_to(counts, 4) && aligned_to(slope, 4) && aligned_to(workspace, 4)
              ? FP8MI_OK
              : FP8MI_ERR_ALIGN;
@@ -39,7 +40,7 @@ extern "C" {
 int64_t fp8_moe_route_workspace(int64_t tokens, int64_t experts) {
   const int st = check_routing(FP8MI_IN_FP32, tokens, experts, 1);
   if (st != FP8MI_OK) return st;
-  return fp8mi::route_blocks(tokens) * (2 * experts + 1) * (int64_t)sizeof(float);
+  return fp8mi::route_workspace(tokens, experts);
 }
 
 int fp8_moe_route(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t ld_logits,

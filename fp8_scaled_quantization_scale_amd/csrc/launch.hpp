@@ -232,6 +232,7 @@ hipError_t launch_rms_backward(const RmsParams& p, hipStream_t st);
 int64_t rms_partials(int64_t rows);
 hipError_t launch_route(const RouteParams& p, hipStream_t st);
 hipError_t launch_route_backward(const RouteParams& p, hipStream_t st);
-int64_t route_blocks(int64_t tokens);
+int64_t route_blocks(int64_t tokens, int64_t experts);
+int64_t route_workspace(int64_t tokens, int64_t experts);
 
 }  // namespace fp8mi

@@ -8,14 +8,22 @@
 //   dp = dloss slope + (the weights' part), dl = p (dp - <p, dp>).
 //
 // 16 lanes own a token, V neighbouring experts each, so that a maximum or a sum
-// over the experts is one of V registers and four DPP rotations, and equal
-// logits are in the order of the lanes.  Logits are compared as integers that
-// order like them (NaN on top, -0 with 0); an expert of logit -inf, and one that
-// is taken, has the integer 0 and is not chosen.  Sums over the tokens are
-// taken in registers, then over the workgroup and, by a second launch in a fixed
-// order, over all workgroups; only integers are counted with atomics.
-#include <atomic>
-
+// over the experts is one of V registers and four DPP rotations; the next
+// token's logits are on their way while one is worked on.
+//
+// The choice.  Logits are compared as integers that order like them, with the
+// expert's number in the low bits so that no two are equal (of equal logits the
+// lowest expert is the largest).  The next choice is then the largest integer
+// below the last one: the largest difference to it modulo 2^32, one subtraction
+// and half a three-way maximum per expert, and nothing is marked as taken.  FP32
+// logits lose as many low bits as an expert's number has: where two of a token's
+// topk + 1 largest are equal without them, and where a NaN, an infinity or the
+// lowest values are among the chosen, the wave chooses once more by whole
+// integers (choose_exact), as it does for more than 16 choices.
+//
+// Sums over the tokens are taken in registers, then over the workgroup and, by a
+// second launch in a fixed order, over all workgroups; only integers are counted
+// with atomics.
 #include "launch.hpp"
 #include "rows.hpp"
 #include "tile.hpp"
@@ -24,9 +32,18 @@ namespace fp8mi {
 
 namespace {
 
-constexpr int kRouteThreads = 256, kRouteGroups = kRouteThreads / 16;
-constexpr int kRouteMaxBlocks = 512;
-constexpr int kRouteTokens = 4;  // tokens per group of lanes before there are more workgroups
+constexpr int kRouteMaxBlocks = 256;
+constexpr int kRouteOneBlock = 4;  // tokens per group of lanes up to which there is one workgroup, and one launch
+
+// threads of the forward pass: as many as the registers of V experts allow
+constexpr int route_threads(int v) { return v <= 16 ? 1024 : (v <= 32 ? 512 : 256); }
+// experts per lane: the power of two that 16 lanes hold them with
+constexpr int per_lane(int64_t experts) {
+  int v = 1;
+  while (16 * v < experts) v *= 2;
+  return v;
+}
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
 struct RouteArgs {
   const void* logits;
@@ -41,167 +58,265 @@ struct RouteArgs {
   float* loss;
   int32_t* counts;
   float* slope;
-  float* psum;    // [blocks][experts]
-  int32_t* hist;  // [blocks][experts + 1], the last one tokens
+  // the workgroups' sums
+  float* psum;        // [blocks][experts]
+  int32_t* hist;      // [blocks][experts]
+  int32_t* held;      // [blocks] tokens
+  float* part;        // [32] of the loss
+  uint32_t* ticket;
   const float* dweights;
   const float* dloss;
   void* dlogits;
   int64_t ld_dlogits;
 };
 
+__device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
+__device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
 __device__ __forceinline__ float row16_sum(float v) {
-  auto add = [](float x, uint32_t o) __attribute__((always_inline)) { return x + __builtin_bit_cast(float, o); };
-  v = add(v, dpp<0x128>(__builtin_bit_cast(uint32_t, v)));
-  v = add(v, dpp<0x124>(__builtin_bit_cast(uint32_t, v)));
-  v = add(v, dpp<0x122>(__builtin_bit_cast(uint32_t, v)));
-  return add(v, dpp<0x121>(__builtin_bit_cast(uint32_t, v)));
+  v += as_float(dpp<0x128>(as_bits(v)));
+  v += as_float(dpp<0x124>(as_bits(v)));
+  v += as_float(dpp<0x122>(as_bits(v)));
+  return v + as_float(dpp<0x121>(as_bits(v)));
+}
+__device__ __forceinline__ float row16_fmax(float v) {
+  v = fmaxf(v, as_float(dpp<0x128>(as_bits(v))));
+  v = fmaxf(v, as_float(dpp<0x124>(as_bits(v))));
+  v = fmaxf(v, as_float(dpp<0x122>(as_bits(v))));
+  return fmaxf(v, as_float(dpp<0x121>(as_bits(v))));
 }
 
-// an integer that orders like the logit; 0: not to be chosen
+constexpr float kNegInf = -__builtin_inff();
+
+// an integer that orders like the logit, NaN on top; 0: not to be chosen (-inf)
 __device__ __forceinline__ uint32_t key_of(float v) {
   v += 0.0f;  // -0 is 0
   if (v != v) return 0xFFFFFFFFu;
-  const uint32_t b = __builtin_bit_cast(uint32_t, v);
-  const uint32_t k = (int32_t)b < 0 ? ~b : b | 0x80000000u;
-  return k == 0x007FFFFFu ? 0u : k;  // -inf
-}
-__device__ __forceinline__ float logit_of(uint32_t k) {
-  if (k == 0) return -__builtin_inff();
-  return __builtin_bit_cast(float, (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);  // (NaN stays NaN)
+  const uint32_t b = as_bits(v);
+  return __builtin_elementwise_sub_sat(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 0x007FFFFFu);
 }
 
-// V logits of a token from expert `at` on, as integers (0 past the end)
+// e^(v - most)
+__device__ __forceinline__ float weight_of(float v, float most) {
+  return __builtin_amdgcn_exp2f((v - most) * 1.44269504088896340736f);
+}
+
+// V logits as they lie in memory, of which n are there
 template <typename T, int V>
-__device__ __forceinline__ void load_logits(float (&v)[V], const T* p, int at, int experts) {
-  if constexpr (V >= 8) {
+struct Logits {
+  static constexpr int kChunks = V >= 8 ? V / 8 : 1;
+  typedef T vec __attribute__((ext_vector_type(V >= 8 ? 2 : (V < 2 ? 2 : V)), aligned(sizeof(T))));
+  Chunk<T> c[V >= 8 ? kChunks : 1];
+  T e[V >= 8 ? 1 : V];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (V >= 8) {
 #pragma unroll
-    for (int c = 0; c < V / 8; ++c) {
-      Chunk<T> k;
-      float w[8];
-      const int n = experts - at - 8 * c;
-      k.load(p + at + 8 * c, n);
-      k.get(w);
+      for (int k = 0; k < kChunks; ++k) c[k].load(p + 8 * k, n - 8 * k);
+    } else if constexpr (V == 1) {
+      if (n > 0) e[0] = p[0];
+    } else {
+      if (n >= V) {
+        const vec v = *reinterpret_cast<const vec*>(p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * c + e] = e < n ? w[e] : -__builtin_inff();
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (at + e < experts) {
-        if constexpr (sizeof(T) == 2) v[e] = bf_lo(p[at + e]);
-        else v[e] = p[at + e];
+        for (int i = 0; i < V; ++i) e[i] = v[i];
       } else {
-        v[e] = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < n) e[i] = p[i];
       }
     }
   }
+  // -inf past the end
+  __device__ __forceinline__ void get(float (&v)[V], int n) const {
+    if constexpr (V >= 8) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        float w[8];
+        c[k].get(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * k + i] = 8 * k + i < n ? w[i] : kNegInf;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (sizeof(T) == 2) v[i] = i < n ? bf_lo(e[i]) : kNegInf;
+        else v[i] = i < n ? e[i] : kNegInf;
+      }
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float logit_at(const T* row, int e) {
+  if constexpr (sizeof(T) == 2) return bf_lo(row[e]);
+  else return row[e];
 }
 
-// e^(v - most) of the experts, 0 for -inf (whose token has another)
-__device__ __forceinline__ float weight_of(float v, float most) { return __expf(v - most); }
+// A token's largest logit, to all its lanes (-inf where it has none; NaN is none
+// of the others).
+template <int V>
+__device__ __forceinline__ float most_of(const float (&v)[V]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+  m = row16_fmax(m);
+  if (__any(m == kNegInf)) {  // nothing but -inf, or NaN beside it
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s = v[i] != v[i] ? v[i] : s;
+    s = row16_sum(s);
+    if (m == kNegInf && s != s) m = s;
+  }
+  return m;
+}
+
+// The `last` (at most 16) next choices of a token, one for each lane to keep; -1
+// for none.  key: 0 where taken or not to be chosen.
+template <int V>
+__device__ __forceinline__ int choose_exact(uint32_t (&key)[V], int last) {
+  const int li = threadIdx.x & 15, at = li * V;
+  int mine = -1;
+  for (int j = 0; j < last; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = umax32(best, key[i]);
+    best = row16_max(best);
+    int e = 0x4000;  // the lowest expert that has it
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) e = key[i] == best ? i : e;
+    e = 0x7FFF - (int)row16_max((uint32_t)(0x7FFF - at - e));
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = e - at == i ? 0 : key[i];
+    if (li == j) mine = best ? e : -1;
+  }
+  return mine;
+}
+
+// counts, slope and one token's loss of an expert with c choices and sum p
+__device__ __forceinline__ float settle(const RouteArgs& a, int e, int c, double p, int held) {
+  const double n = held;
+  const float slope = held ? (float)c * (float)((double)a.experts / (n * n * (double)a.topk)) : 0.0f;
+  a.counts[e] = c;
+  a.slope[e] = slope;
+  return (float)((double)slope * p);
+}
 
 template <typename T, int V, bool CHOSEN>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
-  __shared__ int cnt[kMaxExperts + 1];
-  __shared__ float sums[4][16 * V];
+__global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
+  constexpr int NT = route_threads(V), kGroups = NT / 16, kWaves = NT / 64;
+  constexpr int kBits = log2_of(16 * V);  // of an expert's number
+  __shared__ int cnt[16 * V + 1];
+  __shared__ float sums[kWaves][16 * V];
   const int tid = threadIdx.x, li = tid & 15, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e <= a.experts; e += kRouteThreads) cnt[e] = 0;
+  for (int e = tid; e <= 16 * V; e += NT) cnt[e] = 0;
   __syncthreads();
-  const int at = li * V;
-  float ps[V];  // sums of p
+  const int at = li * V, n = a.experts - at;  // this lane's experts, of which n are there
+  float ps[V];                                // sums of p
 #pragma unroll
   for (int i = 0; i < V; ++i) ps[i] = 0.0f;
   int held = 0;  // tokens counted
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t step = (int64_t)a.blocks * kGroups;
+  const int64_t t_first = (int64_t)blockIdx.x * kGroups + (tid >> 4);
+  const bool few = a.topk <= 16;
 
+  Logits<T, V> next;
+  bool next_real = t_first < a.tokens && (!a.mask || a.mask[t_first]);
+  if (next_real) next.load(logits + t_first * a.ld + at, n);
   // (whole waves go round together: the lanes of a group are never apart)
-  for (int64_t t0 = (int64_t)blockIdx.x * kRouteGroups; t0 < a.tokens; t0 += (int64_t)a.blocks * kRouteGroups) {
-    const int64_t t = t0 + (tid >> 4);
-    const bool there = t < a.tokens;
-    const bool real = there && (!a.mask || a.mask[t]);
+  for (int64_t t = t_first; __any(t < a.tokens); t += step) {
+    const bool there = t < a.tokens, real = next_real;
     float v[V];
-    uint32_t key[V], top = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = -__builtin_inff();
-    if (real) load_logits<T, V>(v, static_cast<const T*>(a.logits) + t * a.ld, at, a.experts);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      key[i] = key_of(v[i]);
-      top = umax32(top, key[i]);
-    }
-    top = row16_max(top);
-    const float most = logit_of(top);
-    float s = 0.0f;
+    next.get(v, real ? n : 0);
+    const int64_t tn = t + step;
+    next_real = tn < a.tokens && (!a.mask || a.mask[tn]);
+    if (next_real) next.load(logits + tn * a.ld + at, n);
+
+    const float most = most_of<V>(v);
+    const bool live = most != kNegInf;
+    float e[V], s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[i] = top == 0 ? 0.0f : weight_of(v[i], most);
-      s += v[i];
+      e[i] = weight_of(v[i], live ? most : 0.0f);
+      s += e[i];
     }
     s = row16_sum(s);
-    const float inv = top == 0 ? 0.0f : 1.0f / s;
+    const float inv = live ? 1.0f / s : 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) ps[i] += v[i] * inv;
-    if (top != 0 && li == 0) ++held;
+    for (int i = 0; i < V; ++i) ps[i] += e[i] * inv;
+    if (live && li == 0) ++held;
 
     if constexpr (CHOSEN) {
-      if (real && top != 0)
+      if (live)
         for (int j = li; j < a.topk; j += 16) {
-          int64_t e;
-          if (a.wide) e = static_cast<const int64_t*>(a.chosen)[t * a.ld_chosen + j];
-          else e = static_cast<const int32_t*>(a.chosen)[t * a.ld_chosen + j];
-          if (e >= 0 && e < a.experts) atomicAdd(&cnt[e], 1);
+          int64_t x;
+          if (a.wide) x = static_cast<const int64_t*>(a.chosen)[t * a.ld_chosen + j];
+          else x = static_cast<const int32_t*>(a.chosen)[t * a.ld_chosen + j];
+          if (x >= 0 && x < a.experts) atomicAdd(&cnt[x], 1);
         }
     } else {
-      float total = 0.0f;  // of the chosen ones' e^
-      for (int base = 0; base < a.topk; base += 16) {
-        // the choices base .. base + 15: one for each lane to keep
-        int mine = -1;
-        float mine_w = 0.0f;
-        const int last = min(a.topk - base, 16);
-        for (int j = 0; j < last; ++j) {
-          uint32_t m = 0;
+      int mine = -1;  // this lane's choice of the first 16
+      bool again = !few;
+      if (few) {
+        uint32_t pk[V], best = 0, other = 0;
 #pragma unroll
-          for (int i = 0; i < V; ++i) m = umax32(m, key[i]);
-          const uint32_t best = row16_max(m);
-          // the lowest lane that has it, and in it the lowest expert
-          const uint64_t has = __ballot(m == best && best != 0);
-          const uint32_t group = (uint32_t)(has >> (lane & 48)) & 0xFFFFu;
-          const int win = __ffs((int)group) - 1;
-          int e = -1;
-          float w = 0.0f;
-          if (li == win) {
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-              if (key[i] == best) {
-                e = at + i;
-                w = v[i];
-              }
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-              if (at + i == e) key[i] = 0;
-            atomicAdd(&cnt[e], 1);
-          }
-          const int from = win < 0 ? lane : (lane & 48) | win;
-          e = __shfl(e, from, 64);
-          w = __shfl(w, from, 64);
-          if (win < 0) e = -1;
-          if (li == j) {
-            mine = e;
-            mine_w = e < 0 ? 0.0f : w;
-          }
+        for (int i = 0; i < V; ++i) {
+          const uint32_t b = as_bits(v[i] + 0.0f);
+          const uint32_t k = __builtin_elementwise_sub_sat(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 0x007FFFFFu);
+          pk[i] = ((k & ~((1u << kBits) - 1)) | (uint32_t)(16 * V - 1 - at)) ^ (uint32_t)i;  // (the expert's number from the top)
+          best = umax32(best, pk[i]);
         }
-        if (there && li < last) a.expert[t * a.topk + base + li] = mine;
-        total += row16_sum(mine_w);
-        if (!a.normalize || a.topk <= 16) {
-          if (there && li < last)
-            a.weights[t * a.topk + base + li] = mine < 0 ? 0.0f : (a.normalize ? mine_w / total : mine_w * inv);
-        } else if (there && li < last) {
-          a.weights[t * a.topk + base + li] = mine_w;
+        best = row16_max(best);
+        bool odd = s != s;
+        for (int j = 0; j < a.topk; ++j) {
+          if (li == j) mine = 16 * V - 1 - (int)(best & ((1u << kBits) - 1));
+          odd = odd || best >> kBits == 0;
+          if (sizeof(T) == 2 && j + 1 == a.topk) break;  // (BF16: what was cut off is zero)
+          other = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) other = umax32(other, pk[i] - best);
+          other = row16_max(other) + best;
+          if (sizeof(T) == 4) odd = odd || (other ^ best) >> kBits == 0;
+          best = other;
+        }
+        again = __any(odd && live);
+      }
+      const int64_t slot = t * a.topk;
+      if (again) {
+        uint32_t key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
+        if (few) {
+          mine = choose_exact<V>(key, a.topk);
+        } else {
+          for (int base = 0; base < a.topk; base += 16) {
+            mine = choose_exact<V>(key, min(a.topk - base, 16));
+            if (there && base + li < a.topk) a.expert[slot + base + li] = mine;
+          }
         }
       }
-      if (a.normalize && a.topk > 16 && there) {
+      // weights: few choices are one to a lane, others were just written by it
+      float total = 0.0f;
+      for (int j = li; j < a.topk; j += 16) {
+        if (!there) break;
+        const int x = few ? (live ? mine : -1) : a.expert[slot + j];
+        float w = 0.0f;
+        if (x >= 0) {
+          atomicAdd(&cnt[x], 1);
+          w = weight_of(logit_at(logits + t * a.ld, x), most);
+          total += w;
+        }
+        if (few) a.expert[slot + j] = x;
+        a.weights[slot + j] = few && a.normalize ? w : w * inv;
+        mine = x;
+      }
+      if (a.normalize) {
+        total = row16_sum(total);
+        const float by = 1.0f / total;
         for (int j = li; j < a.topk; j += 16) {
-          float* w = a.weights + t * a.topk + j;  // (this lane's own)
-          *w = total == 0.0f ? 0.0f : *w / total;
+          if (!there) break;
+          const int x = few ? mine : a.expert[slot + j];
+          a.weights[slot + j] = x < 0 ? 0.0f : weight_of(logit_at(logits + t * a.ld, x), most) * by;
         }
       }
     }
@@ -212,67 +327,88 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   for (int i = 0; i < V; ++i) {
     ps[i] += __shfl_xor(ps[i], 16, 64);
     ps[i] += __shfl_xor(ps[i], 32, 64);
+    if (lane < 16) sums[wave][at + i] = ps[i];
   }
-  if (lane < 16) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) sums[wave][at + i] = ps[i];
-  }
-  if (li == 0 && held) atomicAdd(&cnt[a.experts], held);
+  if (li == 0 && held) atomicAdd(&cnt[16 * V], held);
   __syncthreads();
-  for (int e = tid; e < a.experts; e += kRouteThreads)
-    a.psum[(int64_t)blockIdx.x * a.experts + e] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
-  for (int e = tid; e <= a.experts; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * (a.experts + 1) + e] = cnt[e];
+  auto sum_of = [&](int e) {
+    float p = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) p += sums[w][e];
+    return p;
+  };
+  if (a.blocks == 1) {  // all there is
+    __shared__ float parts[kWaves];
+    float loss = 0.0f;
+    for (int e = tid; e < a.experts; e += NT) loss += settle(a, e, cnt[e], sum_of(e), cnt[16 * V]);
+    loss = wave_sum(loss);
+    if (lane == 0) parts[wave] = loss;
+    __syncthreads();
+    if (tid == 0) {
+      loss = 0.0f;
+      for (int w = 0; w < kWaves; ++w) loss += parts[w];
+      *a.loss = loss;
+    }
+    return;
+  }
+  for (int e = tid; e < a.experts; e += NT) {
+    a.psum[(int64_t)blockIdx.x * a.experts + e] = sum_of(e);
+    a.hist[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
+  }
+  if (tid == 0) {
+    a.held[blockIdx.x] = cnt[16 * V];
+    if (blockIdx.x == 0) *a.ticket = 0;
+  }
 }
 
-// Counts, slope and loss from the workgroups' sums, by one workgroup: as many
-// threads per expert as there are.
-constexpr int kSumThreads = 1024;
+// Counts, slope and loss from the workgroups' sums: a workgroup takes 32 experts,
+// each of its 32 thread groups every 32nd sum; the last one to end adds up the
+// parts of the loss, in order.
+constexpr int kSumThreads = 1024, kSumExperts = 32;
 __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
-  __shared__ int n_tokens;
-  __shared__ int c_part[kSumThreads];
-  __shared__ double p_part[kSumThreads];
-  const int tid = threadIdx.x;
-  const int wide = a.experts > 1 ? 1 << (32 - __clz(a.experts - 1)) : 1;  // experts, up to a power of two
-  const int groups = kSumThreads / wide, e = tid & (wide - 1);
-  int c = 0, n = 0;
+  __shared__ int c_part[kSumThreads / kSumExperts][kSumExperts + 1];
+  __shared__ double p_part[kSumThreads / kSumExperts][kSumExperts + 1];
+  __shared__ int tokens[kSumThreads / 64];
+  const int tid = threadIdx.x, x = tid & (kSumExperts - 1), g = tid / kSumExperts;
+  const int e = (int)blockIdx.x * kSumExperts + x;
+  int c = 0, n = tid < a.blocks ? a.held[tid] : 0;
   double p = 0.0;
   if (e < a.experts)
-    for (int b = tid / wide; b < a.blocks; b += groups) {
-      c += a.hist[(int64_t)b * (a.experts + 1) + e];
+    for (int b = g; b < a.blocks; b += kSumThreads / kSumExperts) {
+      c += a.hist[(int64_t)b * a.experts + e];
       p += a.psum[(int64_t)b * a.experts + e];
     }
-  if (tid < 64) {
-    for (int b = tid; b < a.blocks; b += 64) n += a.hist[(int64_t)b * (a.experts + 1) + a.experts];
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, 64);
-    if (tid == 0) n_tokens = n;
-  }
-  c_part[tid] = c;
-  p_part[tid] = p;
+  for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, 64);
+  if ((tid & 63) == 0) tokens[tid >> 6] = n;
+  c_part[g][x] = c;
+  p_part[g][x] = p;
   __syncthreads();
-  double loss = 0.0;
-  if (tid < a.experts) {
-    for (int g = 1; g < groups; ++g) {
-      c += c_part[g * wide + tid];
-      p += p_part[g * wide + tid];
+  if (tid >= 64) return;
+  float loss = 0.0f;
+  if (tid < kSumExperts && e < a.experts) {
+    n = 0;
+    for (int w = 0; w < kSumThreads / 64; ++w) n += tokens[w];
+    for (int k = 1; k < kSumThreads / kSumExperts; ++k) {
+      c += c_part[k][x];
+      p += p_part[k][x];
     }
-    const double t = n_tokens;
-    const float slope = n_tokens ? (float)c * (float)((double)a.experts / (t * t * (double)a.topk)) : 0.0f;
-    a.counts[tid] = c;
-    a.slope[tid] = slope;
-    loss = (double)slope * p;
+    loss = settle(a, e, c, p, n);
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) loss += __shfl_xor(loss, off, 64);
-  __syncthreads();
-  if ((tid & 63) == 0) p_part[tid >> 6] = loss;
-  __syncthreads();
-  if (tid == 0) {
-    double l = 0.0;
-    for (int w = 0; w < kSumThreads / 64; ++w) l += p_part[w];
-    *a.loss = (float)l;
+  loss = wave_sum(loss);
+  if (tid != 0) return;
+  if (gridDim.x > 1) {
+    a.part[blockIdx.x] = loss;
+    __threadfence();
+    if (atomicAdd(a.ticket, 1u) != gridDim.x - 1) return;
+    __threadfence();
+    loss = 0.0f;
+    for (unsigned b = 0; b < gridDim.x; ++b) loss += __hip_atomic_load(a.part + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  *a.loss = loss;
 }
+
+constexpr int kRouteThreads = 256, kRouteGroups = kRouteThreads / 16;  // of the backward pass
 
 template <typename T, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
@@ -291,25 +427,22 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
     const bool there = t < a.tokens;
     const bool real = there && (!a.mask || a.mask[t]);
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    Logits<T, V> raw;
+    if (real) raw.load(row + at, a.experts - at);
     float v[V];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = -__builtin_inff();
-    if (real) load_logits<T, V>(v, row, at, a.experts);
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = umax32(top, key_of(v[i]));
-    top = row16_max(top);
-    const float most = logit_of(top);
+    raw.get(v, real ? a.experts - at : 0);
+    const float most = most_of<V>(v);
+    const bool live = most != kNegInf;
     float s = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[i] = top == 0 ? 0.0f : weight_of(v[i], most);
+      v[i] = weight_of(v[i], live ? most : 0.0f);
       s += v[i];
       dot += v[i] * slope[i];
     }
     s = row16_sum(s);
     dot = row16_sum(dot);
-    const float inv = top == 0 ? 0.0f : 1.0f / s;
+    const float inv = live ? 1.0f / s : 0.0f;
     dot *= inv;
 
     // the weights' part: an addition to the chosen experts' elements each, and
@@ -322,17 +455,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
       for (int j = li; j < a.topk; j += 16) {
         const int e = real ? a.expert[t * a.topk + j] : -1;
         if (e >= 0 && e < a.experts) {
-          float l;
-          if constexpr (sizeof(T) == 2) l = bf_lo(row[e]);
-          else l = row[e];
-          const float w = weight_of(l, most);
+          const float w = weight_of(logit_at(row, e), most);
           total += w;
           along += w * a.dweights[t * a.topk + j];
         }
       }
       total = row16_sum(total);
       along = row16_sum(along);
-      const float unit = top == 0 || (a.normalize && total == 0.0f) ? 0.0f : (a.normalize ? 1.0f / total : inv);
+      const float unit = !live || (a.normalize && total == 0.0f) ? 0.0f : (a.normalize ? 1.0f / total : inv);
       along *= unit;
       if (!a.normalize) dot += along;
       for (int base = 0; base < a.topk; base += 16) {
@@ -341,10 +471,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         if (real && base + li < a.topk) {
           e = a.expert[t * a.topk + base + li];
           if (e >= 0 && e < a.experts) {
-            float l;
-            if constexpr (sizeof(T) == 2) l = bf_lo(row[e]);
-            else l = row[e];
-            add = weight_of(l, most) * unit * (a.dweights[t * a.topk + base + li] - (a.normalize ? along : 0.0f));
+            add = weight_of(logit_at(row, e), most) * unit * (a.dweights[t * a.topk + base + li] - (a.normalize ? along : 0.0f));
           }
         }
         const int last = min(a.topk - base, 16);
@@ -360,7 +487,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
     if (there) {
       T* out = static_cast<T*>(a.dlogits) + t * a.ld_dlogits;
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = top == 0 ? 0.0f : d[i] + v[i] * inv * (slope[i] - dot);
+      for (int i = 0; i < V; ++i) d[i] = live ? d[i] + v[i] * inv * (slope[i] - dot) : 0.0f;
       if constexpr (V >= 8) {
 #pragma unroll
         for (int c = 0; c < V / 8; ++c) {
@@ -400,9 +527,14 @@ RouteArgs args_of(const RouteParams& p) {
   a.loss = p.loss;
   a.counts = p.counts;
   a.slope = p.slope;
-  a.blocks = (int)route_blocks(p.tokens);
+  a.blocks = (int)route_blocks(p.tokens, p.experts);
   a.psum = static_cast<float*>(p.workspace);
-  a.hist = reinterpret_cast<int32_t*>(a.psum + a.blocks * p.experts);
+  if (a.blocks > 1) {
+    a.hist = reinterpret_cast<int32_t*>(a.psum + a.blocks * p.experts);
+    a.held = a.hist + a.blocks * p.experts;
+    a.part = reinterpret_cast<float*>(a.held + a.blocks);
+    a.ticket = reinterpret_cast<uint32_t*>(a.part + kMaxExperts / kSumExperts);
+  }
   a.dweights = p.dweights;
   a.dloss = p.dloss;
   a.dlogits = p.dlogits;
@@ -412,11 +544,11 @@ RouteArgs args_of(const RouteParams& p) {
 
 template <typename T, int V>
 hipError_t route(const RouteArgs& a, bool given, hipStream_t st) {
-  if (given) route_kernel<T, V, true><<<(unsigned)a.blocks, kRouteThreads, 0, st>>>(a);
-  else route_kernel<T, V, false><<<(unsigned)a.blocks, kRouteThreads, 0, st>>>(a);
+  if (given) route_kernel<T, V, true><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
+  else route_kernel<T, V, false><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  route_sum_kernel<<<1, kSumThreads, 0, st>>>(a);
+  if (e != hipSuccess || a.blocks == 1) return e;
+  route_sum_kernel<<<(unsigned)((a.experts + kSumExperts - 1) / kSumExperts), kSumThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -427,28 +559,37 @@ hipError_t route_back(const RouteArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// experts per lane: as few powers of two as hold them
 template <typename T, bool BACK>
 hipError_t route_any(const RouteArgs& a, bool given, hipStream_t st) {
   auto go = [&](auto v) {
     if constexpr (BACK) return route_back<T, decltype(v)::value>(a, st);
     else return route<T, decltype(v)::value>(a, given, st);
   };
-  if (a.experts <= 16) return go(std::integral_constant<int, 1>{});
-  if (a.experts <= 32) return go(std::integral_constant<int, 2>{});
-  if (a.experts <= 64) return go(std::integral_constant<int, 4>{});
-  if (a.experts <= 128) return go(std::integral_constant<int, 8>{});
-  if (a.experts <= 256) return go(std::integral_constant<int, 16>{});
-  if (a.experts <= 512) return go(std::integral_constant<int, 32>{});
+  switch (per_lane(a.experts)) {
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 4: return go(std::integral_constant<int, 4>{});
+    case 8: return go(std::integral_constant<int, 8>{});
+    case 16: return go(std::integral_constant<int, 16>{});
+    case 32: return go(std::integral_constant<int, 32>{});
+  }
   return go(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
 
-// workgroups of the forward pass, each of which leaves its sums
-int64_t route_blocks(int64_t tokens) {
-  const int64_t n = (tokens + kRouteGroups * kRouteTokens - 1) / (kRouteGroups * kRouteTokens);
-  return n < 1 ? 1 : (n < kRouteMaxBlocks ? n : kRouteMaxBlocks);
+// workgroups of the forward pass
+int64_t route_blocks(int64_t tokens, int64_t experts) {
+  const int64_t groups = route_threads(per_lane(experts)) / 16;
+  if (tokens <= kRouteOneBlock * groups) return 1;
+  const int64_t n = (tokens + groups - 1) / groups;
+  return n < kRouteMaxBlocks ? n : kRouteMaxBlocks;
+}
+
+// bytes that they leave for the second launch (none where there is one)
+int64_t route_workspace(int64_t tokens, int64_t experts) {
+  const int64_t blocks = route_blocks(tokens, experts);
+  return blocks > 1 ? (blocks * (2 * experts + 1) + kMaxExperts / kSumExperts + 1) * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_route(const RouteParams& p, hipStream_t st) {

@@ -131,7 +131,8 @@ def _sums(tokens: int, experts: int, dev):
     if size < 0:
         _check(size, "fp8_moe_route_workspace")
     return (torch.empty((), dtype=torch.float32, device=dev), torch.empty(experts, dtype=torch.int32, device=dev),
-            torch.empty(experts, dtype=torch.float32, device=dev), torch.empty(size, dtype=torch.uint8, device=dev), size)
+            torch.empty(experts, dtype=torch.float32, device=dev),
+            torch.empty(size, dtype=torch.uint8, device=dev) if size else None, size)
 
 
 def _route(logits, topk, normalize, mask, stream):
@@ -143,7 +144,7 @@ def _route(logits, topk, normalize, mask, stream):
         weights = torch.empty(tokens, max(topk, 0), dtype=torch.float32, device=dev)
         st = load().fp8_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, _ld(logits), _at(mask), topk,
                                   normalize, expert.data_ptr(), weights.data_ptr(), loss.data_ptr(), counts.data_ptr(),
-                                  slope.data_ptr(), ws.data_ptr(), size, _here(dev))
+                                  slope.data_ptr(), _at(ws), size, _here(dev))
     _check(st, "fp8_moe_route")
     return expert, weights, loss, counts, slope
 
@@ -155,7 +156,7 @@ def _balance(logits, expert, mask, stream):
         loss, counts, slope, ws, size = _sums(tokens, experts, dev)
         st = load().fp8_moe_balance(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, _ld(logits), _at(mask),
                                     expert.data_ptr(), _IDX[expert.dtype], expert.shape[1], _ld(expert), loss.data_ptr(),
-                                    counts.data_ptr(), slope.data_ptr(), ws.data_ptr(), size, _here(dev))
+                                    counts.data_ptr(), slope.data_ptr(), _at(ws), size, _here(dev))
     _check(st, "fp8_moe_balance")
     return loss, counts, slope
 

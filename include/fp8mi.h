@@ -431,8 +431,8 @@ int fp8_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t 
                              const int32_t* counts, int64_t experts, int64_t topk, const float* weights,
                              void* dys, int64_t rows, int64_t ld_dys, float* dweights, void* stream);
 
-/* Bytes of device memory that fp8_moe_route and fp8_moe_balance need; negative:
- * an error. */
+/* Bytes of device memory that fp8_moe_route and fp8_moe_balance need (0 for few
+ * tokens); negative: an error. */
 int64_t fp8_moe_route_workspace(int64_t tokens, int64_t experts);
 
 /* fp8_moe_route -- the router: from each token's logits to its experts, their

@@ -43,7 +43,7 @@ STUB(launch_route, RouteParams, g_route)
 STUB(launch_route_backward, RouteParams, g_route)
 // the most that these say
 int64_t rms_partials(int64_t) { return 512; }
-int64_t route_blocks(int64_t) { return 1024; }
+int64_t route_workspace(int64_t, int64_t experts) { return 4 * (256 * (2 * experts + 1) + 33); }
 int hip_status(hipError_t e) { return e == hipSuccess ? FP8MI_OK : FP8MI_ERR_HIP; }
 }  // namespace fp8mi
 

@@ -78,7 +78,8 @@ def _check(r, logits, topk, normalize, mask):
 # every number of experts a lane may hold and its borders, odd sizes and strides
 SHAPES = [(1, 1, 1, F), (1, 8, 2, F), (5, 16, 16, B), (7, 17, 3, F), (128, 8, 2, F), (100, 33, 8, B), (333, 64, 4, F), (64, 65, 6, B),
           (50, 100, 16, F), (1000, 128, 8, B), (31, 129, 17, F), (2100, 256, 8, B), (17, 257, 20, F), (40, 512, 40, B), (9, 600, 64, F),
-          (33, 1024, 8, B), (3, 1000, 1000, F), (20000, 16, 2, F), (9000, 64, 8, B)]
+          (33, 1024, 8, B), (3, 1000, 1000, F), (20000, 16, 2, F), (9000, 64, 8, B), (256, 64, 4, F), (257, 64, 4, F), (128, 300, 8, F), (129, 300, 8, F),
+          (64, 700, 4, B), (65, 700, 4, B)]
 
 
 @pytest.mark.parametrize("tokens,experts,topk,dt", SHAPES, ids=[f"{t}x{e}top{k}" for t, e, k, _ in SHAPES])
@@ -287,7 +288,7 @@ def test_gradient_against_differences():
 
 def test_neighbours_are_left_alone():
     need_gpu()
-    tokens, experts, topk = 203, 40, 5
+    tokens, experts, topk = 403, 40, 5
     l = _logits(tokens, experts, B)
     want = moe.route(l, topk)
     i = lambda n: torch.full((n + 2,), 7, dtype=torch.int32, device="cuda")  # noqa: E731
@@ -427,3 +428,21 @@ def test_refusals():
     g, = torch.autograd.grad(moe.route(x, 2).loss, x, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+@pytest.mark.parametrize("experts,topk", [(64, 8), (256, 8), (1000, 16)])
+def test_logits_that_agree_in_their_first_bits(experts, topk):
+    """FP32 logits a few steps of the type apart, of either sign, and the lowest
+    values: the choice and its order go by all bits."""
+    need_gpu()
+    g = _gen(experts)
+    for base in (1.0, -1.0, 1e-38, -3e38, 0.0):
+        b = torch.full((70, experts), base, device="cuda").view(torch.int32)
+        l = (b + torch.randint(0, 6, (70, experts), generator=g, device="cuda", dtype=torch.int32)).view(torch.float32)
+        l[::7] = 2.0 * torch.randn(10, experts, generator=g, device="cuda")  # other tokens of the same waves
+        l[3, 5:] = -INF
+        l[10] = torch.finfo(F).min
+        l[11, 2:] = torch.finfo(F).min
+        _check(moe.route(l, topk), l, topk, True, None)
+        half = l.bfloat16()
+        _check(moe.route(half, topk), half, topk, True, None)

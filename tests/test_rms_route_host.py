@@ -76,13 +76,13 @@ def test_sizes():
     assert fm.fp8_rms_norm_workspace(8, 64) >= 64 * 4 and fm.fp8_rms_norm_workspace(0, 64) > 0
     assert fm.fp8_rms_norm_workspace(-1, 64) == fm.fp8_rms_norm_workspace(8, 0) == fm.ERR_SHAPE
     assert fm.fp8_rms_norm_workspace(8, (1 << 28) + 1) == fm.ERR_UNSUPPORTED
-    assert fm.fp8_moe_route_workspace(0, 8) > 0 and fm.fp8_moe_route_workspace(1 << 20, 1024) > 0
+    assert fm.fp8_moe_route_workspace(0, 8) == 0 and fm.fp8_moe_route_workspace(1000, 8) > 0 and fm.fp8_moe_route_workspace(1 << 20, 1024) > 0
     assert fm.fp8_moe_route_workspace(-1, 8) == fm.fp8_moe_route_workspace(8, 0) == fm.ERR_SHAPE
     assert fm.fp8_moe_route_workspace(1, 1025) == fm.fp8_moe_route_workspace((1 << 30) + 1, 8) == fm.ERR_UNSUPPORTED
 
 
 def _route(**kw):
-    a = dict(logits=P, dtype=fm.IN_FP32, tokens=100, experts=8, ld_logits=8, mask=P, topk=2, normalize=1, expert=P, weights=P, loss=P,
+    a = dict(logits=P, dtype=fm.IN_FP32, tokens=1000, experts=8, ld_logits=8, mask=P, topk=2, normalize=1, expert=P, weights=P, loss=P,
              counts=P, slope=P, workspace=P, workspace_bytes=1 << 20, stream=0)
     a.update(kw)
     return fm.fp8_moe_route(**a)
@@ -106,7 +106,7 @@ def test_route(kw, code):
 @pytest.mark.parametrize("kw,code", ROUTE + [(dict(idx_dtype=2), fm.ERR_ENUM), (dict(ld_expert=1), fm.ERR_SHAPE),
                                              (dict(expert=P + 4, idx_dtype=fm.IDX_I64), fm.ERR_ALIGN)])
 def test_balance(kw, code):
-    a = dict(logits=P, dtype=fm.IN_FP32, tokens=100, experts=8, ld_logits=8, mask=P, expert=P, idx_dtype=fm.IDX_I32, topk=2, ld_expert=2,
+    a = dict(logits=P, dtype=fm.IN_FP32, tokens=1000, experts=8, ld_logits=8, mask=P, expert=P, idx_dtype=fm.IDX_I32, topk=2, ld_expert=2,
              loss=P, counts=P, slope=P, workspace=P, workspace_bytes=1 << 20, stream=0)
     a.update(kw)
     assert fm.fp8_moe_balance(**a) == code
