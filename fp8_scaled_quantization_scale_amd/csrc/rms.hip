@@ -102,7 +102,8 @@ __device__ __forceinline__ void put_codes(const RmsArgs& a, int64_t row, int col
   if (n > 0) store8(a.q + row * a.ld_q + col, n, safe ? encode8<FMT, true>(y, s) : encode8<FMT, false>(y, s));
 }
 
-template <typename T, int NT, int C, int OUT, int FMT>
+// AGAIN: t is read again by the launch that follows
+template <typename T, int NT, int C, int OUT, int FMT, bool PAST, bool AGAIN>
 __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) {
   constexpr int kRows = threads_of(NT) / NT;  // rows per workgroup at a time
   __shared__ float red[2][1][16];
@@ -119,8 +120,8 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
     if (at < a.rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        x[c].load(static_cast<const T*>(a.x) + at * a.ld_x + col[c], n[c]);
-        if (a.residual) r[c].load(static_cast<const T*>(a.residual) + at * a.ld_residual + col[c], n[c]);
+        x[c].template load<PAST>(static_cast<const T*>(a.x) + at * a.ld_x + col[c], n[c]);
+        if (a.residual) r[c].template load<PAST>(static_cast<const T*>(a.residual) + at * a.ld_residual + col[c], n[c]);
       }
     }
   };
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[c][e] += r[e];
         cx[c].set(v[c]);
-        cx[c].store(static_cast<T*>(a.total) + row * a.ld_total + col[c], n[c]);
+        cx[c].template store<PAST && !AGAIN>(static_cast<T*>(a.total) + row * a.ld_total + col[c], n[c]);
         cx[c].get(v[c]);
       }
 #pragma unroll
@@ -158,10 +159,10 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[c][e] = v[c][e] * rstd * w[c][e];
       if constexpr (OUT == OUT_VALUES) {
-        if (a.out) {
+        if (!AGAIN) {
           Chunk<T> o;
           o.set(v[c]);
-          o.store(static_cast<T*>(a.out) + row * a.ld_out + col[c], n[c]);
+          o.template store<PAST>(static_cast<T*>(a.out) + row * a.ld_out + col[c], n[c]);
         }
       } else {
         put_codes<OUT, FMT>(a, row, col[c], n[c], v[c]);
@@ -228,37 +229,49 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
 
 // ---------------------------------------------------------------------------
 // COL codes: the transposed tile, each column's blocks along its rows.  Rows
-// are staged in LDS as they were loaded; thread (cp, rq) then has rows 32 rq
-// .. of the column pair 2 cp, and the codes go back through LDS so that they
+// are staged in LDS as they were loaded; thread (cp, rq) then has 16 rows of the
+// column pair 2 cp, and the codes go back through LDS so that they
 // leave as whole 128-byte lines.
 // ---------------------------------------------------------------------------
-constexpr int kColThreads = 256;
+constexpr int kColThreads = 512, kColRows = kTile / (kColThreads / 64);  // rows of a wave
 
 template <typename T, int OUT, int FMT>
-__global__ __launch_bounds__(kColThreads) void rms_columns_kernel(RmsArgs a, int64_t tiles_x, int64_t tiles) {
+__global__ __launch_bounds__(kColThreads, sizeof(T) == 2 ? 6 : 4) void rms_columns_kernel(RmsArgs a, int tiles_x, int64_t tiles) {
+  constexpr int kLoads = kTile * 16 / kColThreads;  // chunks of a thread
   __shared__ __attribute__((aligned(16))) T tile[kTile * kTile];  // rows, then codes
-  __shared__ uint32_t colred[OUT == OUT_BLOCK ? 4 : 1][kTile];
+  __shared__ uint2 colred[kColThreads / 64][kTile / 2];
   __shared__ float rs[kTile];
   const int tid = threadIdx.x, g = tid >> 4, li = tid & 15;
   const int cp = tid & 63, rq = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
     const int64_t t = tiles - 1 - i;  // the rows written last are in the caches
-    const int64_t by = t / tiles_x, bx = t - by * tiles_x, row0 = by * kTile, col0 = bx * kTile;
-    const int64_t ccol = col0 + 8 * li;
-    Chunk<T> k[8];
+    const int64_t by = t / tiles_x, row0 = by * kTile;
+    const int col0 = (int)(t - by * tiles_x) * kTile;
+    const int ccol = col0 + 8 * li;
+    Chunk<T> k[kLoads];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t r = row0 + g + 16 * j;
+    for (int j = 0; j < kLoads; ++j) {
+      const int64_t r = row0 + g + kColThreads / 16 * j;
       k[j].load(static_cast<const T*>(a.x) + r * a.ld_x + ccol, r < a.rows ? a.cols - ccol : 0);
     }
-    const int64_t c0 = col0 + 2 * cp;
-    const float w0 = a.weight && c0 < a.cols ? (a.w_bf16 ? bf_lo(static_cast<const uint16_t*>(a.weight)[c0]) : static_cast<const float*>(a.weight)[c0]) : 1.0f;
-    const float w1 = a.weight && c0 + 1 < a.cols ? (a.w_bf16 ? bf_lo(static_cast<const uint16_t*>(a.weight)[c0 + 1]) : static_cast<const float*>(a.weight)[c0 + 1]) : 1.0f;
-    __syncthreads();  // the tile before is done with
-    if (tid < kTile) rs[tid] = row0 + tid < a.rows ? a.rstd[row0 + tid] : 0.0f;
+    const float rv = tid < kTile && row0 + tid < a.rows ? a.rstd[row0 + tid] : 0.0f;
+    const int c0 = col0 + 2 * cp;
+    float w0 = 1.0f, w1 = 1.0f;
+    if (a.weight) {
+      const int c1 = c0 + 1 < a.cols ? c0 + 1 : a.cols - 1, ca = c0 < a.cols ? c0 : a.cols - 1;
+      if (a.w_bf16) {
+        w0 = bf_lo(static_cast<const uint16_t*>(a.weight)[ca]);
+        w1 = bf_lo(static_cast<const uint16_t*>(a.weight)[c1]);
+      } else {
+        w0 = static_cast<const float*>(a.weight)[ca];
+        w1 = static_cast<const float*>(a.weight)[c1];
+      }
+    }
+    if (i != blockIdx.x) __syncthreads();  // the tile before is done with
+    if (tid < kTile) rs[tid] = rv;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      T* to = tile + (g + 16 * j) * kTile + 8 * li;
+    for (int j = 0; j < kLoads; ++j) {
+      T* to = tile + (g + kColThreads / 16 * j) * kTile + 8 * li;
       if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<uint4*>(to) = k[j].w;
       } else {
@@ -267,11 +280,11 @@ __global__ __launch_bounds__(kColThreads) void rms_columns_kernel(RmsArgs a, int
       }
     }
     __syncthreads();
-    float u0[32], u1[32];
+    float u0[kColRows], u1[kColRows];
     uint32_t k0 = 0, k1 = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int r = 32 * rq + j;
+    for (int j = 0; j < kColRows; ++j) {
+      const int r = kColRows * rq + j;
       if constexpr (sizeof(T) == 2) {
         const uint32_t p = reinterpret_cast<const uint32_t*>(tile)[r * (kTile / 2) + cp];
         u0[j] = bf_lo(p);
@@ -286,45 +299,49 @@ __global__ __launch_bounds__(kColThreads) void rms_columns_kernel(RmsArgs a, int
       k0 = umax32(k0, abs_key(u0[j]));
       k1 = umax32(k1, abs_key(u1[j]));
     }
-    float s0, s1;
-    bool safe0, safe1;
+    colred[rq][cp] = make_uint2(k0, k1);
+    __syncthreads();  // (every wave has read the rows, too)
     if constexpr (OUT == OUT_BLOCK) {
-      colred[rq][2 * cp] = k0;
-      colred[rq][2 * cp + 1] = k1;
-      __syncthreads();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        k0 = umax32(k0, colred[q][2 * cp]);
-        k1 = umax32(k1, colred[q][2 * cp + 1]);
+      for (int q = 0; q < kColThreads / 64; ++q) {
+        const uint2 o = colred[q][cp];
+        k0 = umax32(k0, o.x);
+        k1 = umax32(k1, o.y);
       }
-      const float am0 = key_to_float(k0), am1 = key_to_float(k1);
+    } else {
+      const uint2 o = colred[rq ^ 1][cp];  // the block's other 16 rows
+      k0 = umax32(k0, o.x);
+      k1 = umax32(k1, o.y);
+    }
+    const float am0 = key_to_float(k0), am1 = key_to_float(k1);
+    float s0, s1;
+    bool odd = false;  // a block may need the saturating encoder
+    if constexpr (OUT == OUT_BLOCK) {
       s0 = scale_from_amax<FMT>(am0, a.margin);
       s1 = scale_from_amax<FMT>(am1, a.margin);
-      safe0 = !is_finite(am0);
-      safe1 = !is_finite(am1);
+      const bool bad0 = !is_finite(am0), bad1 = !is_finite(am1);
+      odd = bad0 || bad1;
       if (rq == 0) {
         const int64_t gr = (a.rows + kTile - 1) / kTile;
         float* sc = static_cast<float*>(a.scales) + c0 * gr + by;
         if (c0 < a.cols) {
           sc[0] = recip_rn(s0);
-          if (safe0 && a.nonfinite) atomicAdd(a.nonfinite, 1);
+          if (bad0 && a.nonfinite) atomicAdd(a.nonfinite, 1);
         }
         if (c0 + 1 < a.cols) {
           sc[gr] = recip_rn(s1);
-          if (safe1 && a.nonfinite) atomicAdd(a.nonfinite, 1);
+          if (bad1 && a.nonfinite) atomicAdd(a.nonfinite, 1);
         }
       }
     } else {
-      const float am0 = key_to_float(k0), am1 = key_to_float(k1);
       const int b0 = a.floor_rule ? mx_scale_byte_floor<FMT>(am0) : mx_scale_byte<FMT>(am0);
       const int b1 = a.floor_rule ? mx_scale_byte_floor<FMT>(am1) : mx_scale_byte<FMT>(am1);
       s0 = b0 == 0xFF ? 1.0f : mx_inv_scale(b0);
       s1 = b1 == 0xFF ? 1.0f : mx_inv_scale(b1);
-      safe0 = b0 == 0xFF || a.floor_rule;
-      safe1 = b1 == 0xFF || a.floor_rule;
-      if (row0 + 32 * rq < a.rows) {
+      odd = a.floor_rule || b0 == 0xFF || b1 == 0xFF;
+      if ((rq & 1) == 0 && row0 + kColRows * rq < a.rows) {
         const int64_t gr = (a.rows + 31) / 32;
-        uint8_t* sc = static_cast<uint8_t*>(a.scales) + c0 * gr + 4 * by + rq;
+        uint8_t* sc = static_cast<uint8_t*>(a.scales) + c0 * gr + 4 * by + (rq >> 1);
         if (c0 < a.cols) {
           sc[0] = (uint8_t)b0;
           if (b0 == 0xFF && a.nonfinite) atomicAdd(a.nonfinite, 1);
@@ -335,32 +352,34 @@ __global__ __launch_bounds__(kColThreads) void rms_columns_kernel(RmsArgs a, int
         }
       }
     }
-    uint32_t pk[2][8];
+    // the two columns' codes of the wave's rows
+    uint32_t pk[2][kColRows / 4];
+    auto encode = [&](auto Safe) __attribute__((always_inline)) {
+      constexpr bool kSafe = decltype(Safe)::value;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      pk[0][q] = safe0 ? encode4<FMT, true>(u0[4 * q] * s0, u0[4 * q + 1] * s0, u0[4 * q + 2] * s0, u0[4 * q + 3] * s0)
-                       : encode4<FMT, false>(u0[4 * q] * s0, u0[4 * q + 1] * s0, u0[4 * q + 2] * s0, u0[4 * q + 3] * s0);
-      pk[1][q] = safe1 ? encode4<FMT, true>(u1[4 * q] * s1, u1[4 * q + 1] * s1, u1[4 * q + 2] * s1, u1[4 * q + 3] * s1)
-                       : encode4<FMT, false>(u1[4 * q] * s1, u1[4 * q + 1] * s1, u1[4 * q + 2] * s1, u1[4 * q + 3] * s1);
-    }
-    __syncthreads();  // every wave has read the rows
+      for (int q = 0; q < kColRows / 4; ++q) {
+        pk[0][q] = encode4<FMT, kSafe>(u0[4 * q] * s0, u0[4 * q + 1] * s0, u0[4 * q + 2] * s0, u0[4 * q + 3] * s0);
+        pk[1][q] = encode4<FMT, kSafe>(u1[4 * q] * s1, u1[4 * q + 1] * s1, u1[4 * q + 2] * s1, u1[4 * q + 3] * s1);
+      }
+    };
+    // (the saturating encoder gives the same codes where it is not needed)
+    if (__any(odd)) encode(std::true_type{});
+    else encode(std::false_type{});
     uint8_t* ct = reinterpret_cast<uint8_t*>(tile);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4* d = reinterpret_cast<uint4*>(ct + (2 * cp + half) * kCodeStride + 32 * rq);
-      d[0] = make_uint4(pk[half][0], pk[half][1], pk[half][2], pk[half][3]);
-      d[1] = make_uint4(pk[half][4], pk[half][5], pk[half][6], pk[half][7]);
-    }
+    for (int half = 0; half < 2; ++half)
+      *reinterpret_cast<uint4*>(ct + (2 * cp + half) * kCodeStride + kColRows * rq) =
+          make_uint4(pk[half][0], pk[half][1], pk[half][2], pk[half][3]);
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = (tid >> 3) + 32 * q, m = tid & 7;
+    for (int q = 0; q < kTile * 8 / kColThreads; ++q) {
+      const int c = (tid >> 3) + kColThreads / 8 * q, m = tid & 7;
       const int64_t left = a.rows - (row0 + 16 * m);
       if (col0 + c < a.cols && left > 0) {
         const uint4 v = *reinterpret_cast<const uint4*>(ct + c * kCodeStride + 16 * m);
         uint8_t* dst = a.q + (col0 + c) * a.ld_q + row0 + 16 * m;
         if (left >= 16) {
-          *reinterpret_cast<uint4*>(dst) = v;
+          __builtin_nontemporal_store(u32x4a2{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4a2*>(dst));
         } else {
           const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
           for (int j = 0; j < left; ++j) dst[j] = (uint8_t)(vw[j >> 2] >> (8 * (j & 3)));
@@ -373,7 +392,7 @@ __global__ __launch_bounds__(kColThreads) void rms_columns_kernel(RmsArgs a, int
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-template <typename T, int NT, int C, int AHEAD>
+template <typename T, int NT, int C, int AHEAD, bool PAST>
 __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a) {
   constexpr int kRows = threads_of(NT) / NT;
   __shared__ float red[2][1][16];
@@ -391,9 +410,9 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a)
     if (r < a.rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        ct[q][c].load(static_cast<const T*>(a.x) + r * a.ld_x + col[c], n[c]);
-        cy[q][c].load(static_cast<const T*>(a.dy) + r * a.ld_dy + col[c], n[c]);
-        if (a.residual) cd[q][c].load(static_cast<const T*>(a.residual) + r * a.ld_residual + col[c], n[c]);
+        ct[q][c].template load<PAST>(static_cast<const T*>(a.x) + r * a.ld_x + col[c], n[c]);
+        cy[q][c].template load<PAST>(static_cast<const T*>(a.dy) + r * a.ld_dy + col[c], n[c]);
+        if (a.residual) cd[q][c].template load<PAST>(static_cast<const T*>(a.residual) + r * a.ld_residual + col[c], n[c]);
       }
       rstd[q] = a.rstd[r];
     }
@@ -596,6 +615,17 @@ __global__ __launch_bounds__(1024) void rms_reduce_kernel(const float* partial, 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
+// Inputs that would not stay in the 256 MB Infinity Cache together are read past
+// it, and so is what the forward pass leaves of them written, but for the rows
+// that the launch for COL codes reads again: 8192 x 16384 with a residual 210 ->
+// 196 us, into codes 284 -> 246, backward 4096 x 16384 114 -> 103.  Smaller ones
+// may be there already from the kernel that made them: read past it, 4096 x 8192
+// into codes 43 -> 50, 3000 x 5120 FP32 backward 49 -> 54.
+bool past_caches(const RmsParams& p) {
+  const int64_t inputs = 1 + (p.residual != nullptr) + (p.dy != nullptr), es = p.x_dtype == kInBf16 ? 2 : 4;
+  return p.rows > (256LL << 20) / (inputs * es * p.cols);
+}
+
 RmsArgs args_of(const RmsParams& p) {
   RmsArgs a{};
   a.rows = p.rows;
@@ -620,27 +650,33 @@ RmsArgs args_of(const RmsParams& p) {
   return a;
 }
 
-template <typename T, int NT, int C, int OUT, int FMT>
+template <typename T, int NT, int C, int OUT, int FMT, bool PAST, bool AGAIN>
 hipError_t forward(const RmsArgs& a, hipStream_t st) {
   static std::atomic<int> occupancy{0};
-  auto k = rms_forward_kernel<T, NT, C, OUT, FMT>;
+  auto k = rms_forward_kernel<T, NT, C, OUT, FMT, PAST, AGAIN>;
   constexpr int threads = threads_of(NT), rows = threads / NT;
   const int64_t need = (a.rows + rows - 1) / rows, most = resident(k, threads, occupancy, st);
   k<<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int OUT, int FMT>
-hipError_t forward_any(const RmsArgs& a, hipStream_t st) {
-  if (a.cols <= 512) return forward<T, 64, 1, OUT, FMT>(a, st);
-  if (a.cols <= 1024) return forward<T, 64, 2, OUT, FMT>(a, st);
-  if (a.cols <= 2048) return forward<T, 256, 1, OUT, FMT>(a, st);
-  if (a.cols <= 4096) return forward<T, 256, 2, OUT, FMT>(a, st);
-  if (a.cols <= 8192) return forward<T, 512, 2, OUT, FMT>(a, st);
-  if (a.cols <= 16384) return forward<T, 1024, 2, OUT, FMT>(a, st);
+template <typename T, int OUT, int FMT, bool PAST, bool AGAIN>
+hipError_t forward_cols(const RmsArgs& a, hipStream_t st) {
+  if (a.cols <= 512) return forward<T, 64, 1, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= 1024) return forward<T, 64, 2, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= 2048) return forward<T, 256, 1, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= 4096) return forward<T, 256, 2, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= 8192) return forward<T, 512, 2, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= 16384) return forward<T, 1024, 2, OUT, FMT, PAST, AGAIN>(a, st);
   const int64_t most = 2 * (int64_t)cu_count(stream_device(st));
   rms_forward_long_kernel<T, OUT, FMT><<<(unsigned)(a.rows < most ? a.rows : most), 1024, 0, st>>>(a);
   return hipGetLastError();
+}
+
+// (codes alone and values are not read again: with those of both orientations t is)
+template <typename T, int OUT, int FMT, bool AGAIN>
+hipError_t forward_any(const RmsArgs& a, bool past, hipStream_t st) {
+  return past ? forward_cols<T, OUT, FMT, true, AGAIN>(a, st) : forward_cols<T, OUT, FMT, false, AGAIN>(a, st);
 }
 
 template <typename T, int OUT, int FMT>
@@ -649,7 +685,7 @@ hipError_t columns(const RmsArgs& a, hipStream_t st) {
   auto k = rms_columns_kernel<T, OUT, FMT>;
   const int64_t tiles_x = (a.cols + kTile - 1) / kTile, tiles = tiles_x * ((a.rows + kTile - 1) / kTile);
   const int64_t most = resident(k, kColThreads, occupancy, st), rounds = (tiles + most - 1) / most;
-  k<<<(unsigned)((tiles + rounds - 1) / rounds), kColThreads, 0, st>>>(a, tiles_x, tiles);
+  k<<<(unsigned)((tiles + rounds - 1) / rounds), kColThreads, 0, st>>>(a, (int)tiles_x, tiles);
   return hipGetLastError();
 }
 
@@ -659,8 +695,11 @@ hipError_t quantize(const RmsParams& p, hipStream_t st) {
   a.q = p.q.q_row;
   a.ld_q = p.q.ld_q_row;
   a.scales = p.q.s_row;
-  const hipError_t e = p.q.orient & 1 ? forward_any<T, OUT, FMT>(a, st) : forward_any<T, OUT_VALUES, kE4M3>(a, st);
-  if (e != hipSuccess || !(p.q.orient & 2)) return e;
+  const bool past = past_caches(p), col = p.q.orient & 2;
+  if (!col) return forward_any<T, OUT, FMT, false>(a, past, st);
+  const hipError_t e = p.q.orient & 1 ? forward_any<T, OUT, FMT, true>(a, past, st)
+                                      : forward_any<T, OUT_VALUES, kE4M3, true>(a, past, st);
+  if (e != hipSuccess) return e;
   if (p.residual) {
     a.x = p.total;
     a.ld_x = p.ld_total;
@@ -695,10 +734,10 @@ hipError_t reduce_any(const RmsParams& p, int parts, hipStream_t st) {
   return p.w_dtype == kInBf16 ? reduce<uint16_t>(p, parts, st) : reduce<float>(p, parts, st);
 }
 
-template <typename T, int NT, int C, int AHEAD>
+template <typename T, int NT, int C, int AHEAD, bool PAST>
 hipError_t backward(const RmsParams& p, hipStream_t st) {
   static std::atomic<int> occupancy{0};
-  auto k = rms_backward_kernel<T, NT, C, AHEAD>;
+  auto k = rms_backward_kernel<T, NT, C, AHEAD, PAST>;
   constexpr int threads = threads_of(NT);
   int64_t blocks = rms_partials(p.rows);
   const int64_t most = resident(k, threads, occupancy, st);
@@ -710,15 +749,20 @@ hipError_t backward(const RmsParams& p, hipStream_t st) {
   return e != hipSuccess ? e : reduce_any(p, (int)blocks, st);
 }
 
+template <typename T, bool PAST>
+hipError_t backward_cols(const RmsParams& p, hipStream_t st) {
+  if (p.cols <= 512) return backward<T, 64, 1, 1, PAST>(p, st);
+  if (p.cols <= 1024) return backward<T, 64, 2, 1, PAST>(p, st);
+  if (p.cols <= 2048) return backward<T, 256, 1, 2, PAST>(p, st);
+  if (p.cols <= 4096) return backward<T, 256, 2, 2, PAST>(p, st);
+  if (p.cols <= 8192) return backward<T, 512, 2, 2, PAST>(p, st);
+  return backward<T, 1024, 2, 0, PAST>(p, st);
+}
+
 template <typename T>
 hipError_t backward_any(const RmsParams& p, hipStream_t st) {
   if (p.rows == 0) return reduce_any(p, 0, st);
-  if (p.cols <= 512) return backward<T, 64, 1, 1>(p, st);
-  if (p.cols <= 1024) return backward<T, 64, 2, 1>(p, st);
-  if (p.cols <= 2048) return backward<T, 256, 1, 2>(p, st);
-  if (p.cols <= 4096) return backward<T, 256, 2, 2>(p, st);
-  if (p.cols <= 8192) return backward<T, 512, 2, 2>(p, st);
-  if (p.cols <= 16384) return backward<T, 1024, 2, 0>(p, st);
+  if (p.cols <= 16384) return past_caches(p) ? backward_cols<T, true>(p, st) : backward_cols<T, false>(p, st);
   const int64_t most = 2 * (int64_t)cu_count(stream_device(st));
   RmsArgs a = args_of(p);
   rms_backward_long_kernel<T><<<(unsigned)(p.rows < most ? p.rows : most), 1024, 0, st>>>(a);
@@ -741,7 +785,9 @@ int64_t rms_partials(int64_t rows) {
 
 hipError_t launch_rms_forward(const RmsParams& p, hipStream_t st) {
   const RmsArgs a = args_of(p);
-  return p.x_dtype == kInBf16 ? forward_any<uint16_t, OUT_VALUES, kE4M3>(a, st) : forward_any<float, OUT_VALUES, kE4M3>(a, st);
+  const bool past = past_caches(p);
+  return p.x_dtype == kInBf16 ? forward_any<uint16_t, OUT_VALUES, kE4M3, false>(a, past, st)
+                              : forward_any<float, OUT_VALUES, kE4M3, false>(a, past, st);
 }
 
 hipError_t launch_rms_quantize(const RmsParams& p, hipStream_t st) {

@@ -35,9 +35,12 @@ struct Chunk;
 template <>
 struct Chunk<uint16_t> {
   uint4 w;
+  template <bool NT = false>
   __device__ __forceinline__ void load(const uint16_t* p, int64_t n) {
     if (n >= 8) {
-      const u32x4a2 v = *reinterpret_cast<const u32x4a2*>(p);
+      u32x4a2 v;
+      if constexpr (NT) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4a2*>(p));
+      else v = *reinterpret_cast<const u32x4a2*>(p);
       w = make_uint4(v.x, v.y, v.z, v.w);
     } else {
       uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -79,9 +82,17 @@ struct Chunk<uint16_t> {
 template <>
 struct Chunk<float> {
   float4 lo, hi;
+  template <bool NT = false>
   __device__ __forceinline__ void load(const float* p, int64_t n) {
     if (n >= 8) {
-      const f32x4a4 a = reinterpret_cast<const f32x4a4*>(p)[0], b = reinterpret_cast<const f32x4a4*>(p)[1];
+      f32x4a4 a, b;
+      if constexpr (NT) {
+        a = __builtin_nontemporal_load(reinterpret_cast<const f32x4a4*>(p));
+        b = __builtin_nontemporal_load(reinterpret_cast<const f32x4a4*>(p) + 1);
+      } else {
+        a = reinterpret_cast<const f32x4a4*>(p)[0];
+        b = reinterpret_cast<const f32x4a4*>(p)[1];
+      }
       lo = make_float4(a.x, a.y, a.z, a.w);
       hi = make_float4(b.x, b.y, b.z, b.w);
     } else {
