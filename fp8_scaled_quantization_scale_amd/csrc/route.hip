@@ -101,25 +101,32 @@ __device__ __forceinline__ float weight_of(float v, float most) {
   return __builtin_amdgcn_exp2f((v - most) * 1.44269504088896340736f);
 }
 
-// V logits as they lie in memory, of which n are there
-template <typename T, int V>
+// V logits as they lie in memory, of which n are there.  EVEN: the number of
+// experts is a multiple of V, or of 8, so that no vector is cut.
+template <typename T, int V, bool EVEN>
 struct Logits {
   static constexpr int kChunks = V >= 8 ? V / 8 : 1;
-  typedef T vec __attribute__((ext_vector_type(V >= 8 ? 2 : (V < 2 ? 2 : V)), aligned(sizeof(T))));
-  Chunk<T> c[V >= 8 ? kChunks : 1];
+  typedef T vec __attribute__((ext_vector_type(V == 4 ? 4 : 2), aligned(sizeof(T))));
+  Chunk<T> c[kChunks];
   T e[V >= 8 ? 1 : V];
   __device__ __forceinline__ void load(const T* p, int n) {
     if constexpr (V >= 8) {
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) c[k].load(p + 8 * k, n - 8 * k);
+      for (int k = 0; k < kChunks; ++k) {
+        if constexpr (EVEN) {
+          if (n > 8 * k) c[k].load(p + 8 * k, 8);
+        } else {
+          c[k].load(p + 8 * k, n - 8 * k);
+        }
+      }
     } else if constexpr (V == 1) {
       if (n > 0) e[0] = p[0];
     } else {
-      if (n >= V) {
+      if (EVEN ? n > 0 : n >= V) {
         const vec v = *reinterpret_cast<const vec*>(p);
 #pragma unroll
         for (int i = 0; i < V; ++i) e[i] = v[i];
-      } else {
+      } else if constexpr (!EVEN) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (i < n) e[i] = p[i];
@@ -134,13 +141,13 @@ struct Logits {
         float w[8];
         c[k].get(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * k + i] = 8 * k + i < n ? w[i] : kNegInf;
+        for (int i = 0; i < 8; ++i) v[8 * k + i] = (EVEN ? 8 * k : 8 * k + i) < n ? w[i] : kNegInf;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (sizeof(T) == 2) v[i] = i < n ? bf_lo(e[i]) : kNegInf;
-        else v[i] = i < n ? e[i] : kNegInf;
+        if constexpr (sizeof(T) == 2) v[i] = (EVEN ? 0 : i) < n ? bf_lo(e[i]) : kNegInf;
+        else v[i] = (EVEN ? 0 : i) < n ? e[i] : kNegInf;
       }
     }
   }
@@ -152,22 +159,24 @@ __device__ __forceinline__ float logit_at(const T* row, int e) {
   else return row[e];
 }
 
-// A token's largest logit, to all its lanes (-inf where it has none; NaN is none
-// of the others).
+// v becomes e^(v - most) with a token's largest logit, most; s: their sum.  False,
+// and zeros, for a token of nothing but -inf (one with a NaN, too, has NaNs).
 template <int V>
-__device__ __forceinline__ float most_of(const float (&v)[V]) {
-  float m = v[0];
+__device__ __forceinline__ bool exponentials(float (&v)[V], float& most, float& s) {
+  most = v[0];
 #pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-  m = row16_fmax(m);
-  if (__any(m == kNegInf)) {  // nothing but -inf, or NaN beside it
-    float s = 0.0f;
+  for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
+  most = row16_fmax(most);
+  const float by = most == kNegInf ? 0.0f : most;
+  s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s = v[i] != v[i] ? v[i] : s;
-    s = row16_sum(s);
-    if (m == kNegInf && s != s) m = s;
+  for (int i = 0; i < V; ++i) {
+    v[i] = weight_of(v[i], by);
+    s += v[i];
   }
-  return m;
+  s = row16_sum(s);
+  if (s != s) most = s;
+  return most != kNegInf;
 }
 
 // The `last` (at most 16) next choices of a token, one for each lane to keep; -1
@@ -192,19 +201,20 @@ __device__ __forceinline__ int choose_exact(uint32_t (&key)[V], int last) {
   return mine;
 }
 
-// counts, slope and one token's loss of an expert with c choices and sum p
-__device__ __forceinline__ float settle(const RouteArgs& a, int e, int c, double p, int held) {
+// counts, slope and the part of the loss of an expert with c choices and sum p
+__device__ __forceinline__ float settle(const RouteArgs& a, int e, int c, float p, int held) {
   const double n = held;
   const float slope = held ? (float)c * (float)((double)a.experts / (n * n * (double)a.topk)) : 0.0f;
   a.counts[e] = c;
   a.slope[e] = slope;
-  return (float)((double)slope * p);
+  return slope * p;
 }
 
-template <typename T, int V, bool CHOSEN>
+template <typename T, int V, bool EVEN, bool CHOSEN>
 __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
   constexpr int NT = route_threads(V), kGroups = NT / 16, kWaves = NT / 64;
   constexpr int kBits = log2_of(16 * V);  // of an expert's number
+  constexpr uint32_t kLow = (1u << kBits) - 1;
   __shared__ int cnt[16 * V + 1];
   __shared__ float sums[kWaves][16 * V];
   const int tid = threadIdx.x, li = tid & 15, lane = tid & 63, wave = tid >> 6;
@@ -216,31 +226,31 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
   for (int i = 0; i < V; ++i) ps[i] = 0.0f;
   int held = 0;  // tokens counted
   const T* logits = static_cast<const T*>(a.logits);
-  const int64_t step = (int64_t)a.blocks * kGroups;
-  const int64_t t_first = (int64_t)blockIdx.x * kGroups + (tid >> 4);
+  const int tokens = (int)a.tokens, step = a.blocks * kGroups;  // (at most 2^30 tokens)
+  const int t_first = blockIdx.x * kGroups + (tid >> 4);
   const bool few = a.topk <= 16;
 
-  Logits<T, V> next;
-  bool next_real = t_first < a.tokens && (!a.mask || a.mask[t_first]);
+  Logits<T, V, EVEN> next;
+  bool next_real = t_first < tokens && (!a.mask || a.mask[t_first]);
   if (next_real) next.load(logits + t_first * a.ld + at, n);
   // (whole waves go round together: the lanes of a group are never apart)
-  for (int64_t t = t_first; __any(t < a.tokens); t += step) {
-    const bool there = t < a.tokens, real = next_real;
-    float v[V];
-    next.get(v, real ? n : 0);
-    const int64_t tn = t + step;
-    next_real = tn < a.tokens && (!a.mask || a.mask[tn]);
-    if (next_real) next.load(logits + tn * a.ld + at, n);
-
-    const float most = most_of<V>(v);
-    const bool live = most != kNegInf;
-    float e[V], s = 0.0f;
+  for (int t = t_first; __any(t < tokens); t += step) {
+    const bool there = t < tokens, real = next_real;
+    const T* row = logits + t * a.ld;
+    float e[V], most, s;
+    uint32_t pk[V];  // (few choices)
+    next.get(e, real ? n : 0);
+    next_real = t + step < tokens && (!a.mask || a.mask[t + step]);
+    if (next_real) next.load(row + step * a.ld + at, n);
+    if constexpr (!CHOSEN) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      e[i] = weight_of(v[i], live ? most : 0.0f);
-      s += e[i];
+      for (int i = 0; i < V; ++i) {
+        const uint32_t b = as_bits(e[i] + 0.0f);
+        const uint32_t k = __builtin_elementwise_sub_sat(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 0x007FFFFFu);
+        pk[i] = ((k & ~kLow) | (uint32_t)(16 * V - 1 - at)) ^ (uint32_t)i;  // (the expert's number from the top)
+      }
     }
-    s = row16_sum(s);
+    const bool live = exponentials<V>(e, most, s);
     const float inv = live ? 1.0f / s : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) ps[i] += e[i] * inv;
@@ -258,32 +268,31 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
       int mine = -1;  // this lane's choice of the first 16
       bool again = !few;
       if (few) {
-        uint32_t pk[V], best = 0, other = 0;
+        uint32_t best = pk[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const uint32_t b = as_bits(v[i] + 0.0f);
-          const uint32_t k = __builtin_elementwise_sub_sat(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 0x007FFFFFu);
-          pk[i] = ((k & ~((1u << kBits) - 1)) | (uint32_t)(16 * V - 1 - at)) ^ (uint32_t)i;  // (the expert's number from the top)
-          best = umax32(best, pk[i]);
-        }
+        for (int i = 1; i < V; ++i) best = umax32(best, pk[i]);
         best = row16_max(best);
         bool odd = s != s;
         for (int j = 0; j < a.topk; ++j) {
-          if (li == j) mine = 16 * V - 1 - (int)(best & ((1u << kBits) - 1));
-          odd = odd || best >> kBits == 0;
+          if (li == j) mine = (int)(~best & kLow);
+          odd = odd || best <= kLow;
           if (sizeof(T) == 2 && j + 1 == a.topk) break;  // (BF16: what was cut off is zero)
-          other = 0;
+          uint32_t other = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) other = umax32(other, pk[i] - best);
           other = row16_max(other) + best;
-          if (sizeof(T) == 4) odd = odd || (other ^ best) >> kBits == 0;
+          if (sizeof(T) == 4) odd = odd || (other ^ best) <= kLow;
           best = other;
         }
         again = __any(odd && live);
       }
-      const int64_t slot = t * a.topk;
+      const int slot = t * a.topk;
       if (again) {
+        Logits<T, V, EVEN> raw;
+        float v[V];
         uint32_t key[V];
+        if (real) raw.load(row + at, n);
+        raw.get(v, real ? n : 0);
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
         if (few) {
@@ -297,26 +306,33 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
       }
       // weights: few choices are one to a lane, others were just written by it
       float total = 0.0f;
-      for (int j = li; j < a.topk; j += 16) {
-        if (!there) break;
-        const int x = few ? (live ? mine : -1) : a.expert[slot + j];
+      if (few) {
         float w = 0.0f;
-        if (x >= 0) {
-          atomicAdd(&cnt[x], 1);
-          w = weight_of(logit_at(logits + t * a.ld, x), most);
-          total += w;
+        const bool has = live && li < a.topk && mine >= 0;
+        if (has) {
+          atomicAdd(&cnt[mine], 1);
+          w = weight_of(logit_at(row, mine), most);
         }
-        if (few) a.expert[slot + j] = x;
-        a.weights[slot + j] = few && a.normalize ? w : w * inv;
-        mine = x;
-      }
-      if (a.normalize) {
-        total = row16_sum(total);
-        const float by = 1.0f / total;
-        for (int j = li; j < a.topk; j += 16) {
-          if (!there) break;
-          const int x = few ? mine : a.expert[slot + j];
-          a.weights[slot + j] = x < 0 ? 0.0f : weight_of(logit_at(logits + t * a.ld, x), most) * by;
+        if (a.normalize) total = row16_sum(w);
+        if (there && li < a.topk) {
+          a.expert[slot + li] = has ? mine : -1;
+          a.weights[slot + li] = !has ? 0.0f : (a.normalize ? w / total : w * inv);
+        }
+      } else {
+        for (int pass = a.normalize ? 0 : 1; pass < 2; ++pass) {
+          const float by = a.normalize ? 1.0f / total : inv;
+          if (there)
+            for (int j = li; j < a.topk; j += 16) {
+              const int x = a.expert[slot + j];
+              const float w = x >= 0 ? weight_of(logit_at(row, x), most) : 0.0f;
+              if (pass == 0) {
+                total += w;
+              } else {
+                a.weights[slot + j] = x >= 0 ? w * by : 0.0f;
+                if (x >= 0) atomicAdd(&cnt[x], 1);
+              }
+            }
+          if (pass == 0) total = row16_sum(total);
         }
       }
     }
@@ -364,38 +380,54 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
 // Counts, slope and loss from the workgroups' sums: a workgroup takes 32 experts,
 // each of its 32 thread groups every 32nd sum; the last one to end adds up the
 // parts of the loss, in order.
-constexpr int kSumThreads = 1024, kSumExperts = 32;
+constexpr int kSumThreads = 1024, kSumExperts = 32, kSumGroups = kSumThreads / kSumExperts;
 __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
-  __shared__ int c_part[kSumThreads / kSumExperts][kSumExperts + 1];
-  __shared__ double p_part[kSumThreads / kSumExperts][kSumExperts + 1];
+  __shared__ int c_part[kSumGroups][kSumExperts + 1];
+  __shared__ float p_part[kSumGroups][kSumExperts + 1];
   __shared__ int tokens[kSumThreads / 64];
+  __shared__ float parts[kSumExperts];
   const int tid = threadIdx.x, x = tid & (kSumExperts - 1), g = tid / kSumExperts;
-  const int e = (int)blockIdx.x * kSumExperts + x;
+  const int first = (int)blockIdx.x * kSumExperts;
   int c = 0, n = tid < a.blocks ? a.held[tid] : 0;
-  double p = 0.0;
-  if (e < a.experts)
-    for (int b = g; b < a.blocks; b += kSumThreads / kSumExperts) {
-      c += a.hist[(int64_t)b * a.experts + e];
-      p += a.psum[(int64_t)b * a.experts + e];
-    }
+  float p = 0.0f;
+  constexpr int kMost = kRouteMaxBlocks / kSumGroups;
+  int cs[kMost];
+  float pq[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int b = g + i * kSumGroups;
+    const bool has = b < a.blocks && first + x < a.experts;
+    cs[i] = has ? a.hist[(int64_t)b * a.experts + first + x] : 0;
+    pq[i] = has ? a.psum[(int64_t)b * a.experts + first + x] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    c += cs[i];
+    p += pq[i];
+  }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, 64);
   if ((tid & 63) == 0) tokens[tid >> 6] = n;
   c_part[g][x] = c;
   p_part[g][x] = p;
   __syncthreads();
-  if (tid >= 64) return;
-  float loss = 0.0f;
-  if (tid < kSumExperts && e < a.experts) {
-    n = 0;
-    for (int w = 0; w < kSumThreads / 64; ++w) n += tokens[w];
-    for (int k = 1; k < kSumThreads / kSumExperts; ++k) {
-      c += c_part[k][x];
-      p += p_part[k][x];
-    }
-    loss = settle(a, e, c, p, n);
+  // from here on 32 lanes have an expert: its sums by group
+  c = c_part[x][g];
+  p = p_part[x][g];
+#pragma unroll
+  for (int off = kSumGroups / 2; off > 0; off >>= 1) {
+    c += __shfl_xor(c, off, 64);
+    p += __shfl_xor(p, off, 64);
   }
-  loss = wave_sum(loss);
+  if (x == 0) {
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kSumThreads / 64; ++w) n += tokens[w];
+    parts[g] = first + g < a.experts ? settle(a, first + g, c, p, n) : 0.0f;
+  }
+  __syncthreads();
+  if (tid >= 64) return;
+  float loss = wave_sum(tid < kSumExperts ? parts[tid] : 0.0f);
   if (tid != 0) return;
   if (gridDim.x > 1) {
     a.part[blockIdx.x] = loss;
@@ -410,7 +442,7 @@ __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
 
 constexpr int kRouteThreads = 256, kRouteGroups = kRouteThreads / 16;  // of the backward pass
 
-template <typename T, int V>
+template <typename T, int V, bool EVEN>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
   const int tid = threadIdx.x, li = tid & 15, lane = tid & 63, at = li * V;
   float slope[V];
@@ -427,20 +459,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
     const bool there = t < a.tokens;
     const bool real = there && (!a.mask || a.mask[t]);
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    Logits<T, V> raw;
+    Logits<T, V, EVEN> raw;
     if (real) raw.load(row + at, a.experts - at);
-    float v[V];
+    float v[V], most, s, dot = 0.0f;
     raw.get(v, real ? a.experts - at : 0);
-    const float most = most_of<V>(v);
-    const bool live = most != kNegInf;
-    float s = 0.0f, dot = 0.0f;
+    const bool live = exponentials<V>(v, most, s);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = weight_of(v[i], live ? most : 0.0f);
-      s += v[i];
-      dot += v[i] * slope[i];
-    }
-    s = row16_sum(s);
+    for (int i = 0; i < V; ++i) dot += v[i] * slope[i];
     dot = row16_sum(dot);
     const float inv = live ? 1.0f / s : 0.0f;
     dot *= inv;
@@ -542,28 +567,30 @@ RouteArgs args_of(const RouteParams& p) {
   return a;
 }
 
-template <typename T, int V>
+template <typename T, int V, bool EVEN>
 hipError_t route(const RouteArgs& a, bool given, hipStream_t st) {
-  if (given) route_kernel<T, V, true><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
-  else route_kernel<T, V, false><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
+  if (given) route_kernel<T, V, EVEN, true><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
+  else route_kernel<T, V, EVEN, false><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 1) return e;
   route_sum_kernel<<<(unsigned)((a.experts + kSumExperts - 1) / kSumExperts), kSumThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int V>
+template <typename T, int V, bool EVEN>
 hipError_t route_back(const RouteArgs& a, hipStream_t st) {
   const int64_t groups = (a.tokens + kRouteGroups - 1) / kRouteGroups, most = 8 * (int64_t)cu_count(stream_device(st));
-  route_backward_kernel<T, V><<<(unsigned)(groups < most ? groups : most), kRouteThreads, 0, st>>>(a);
+  route_backward_kernel<T, V, EVEN><<<(unsigned)(groups < most ? groups : most), kRouteThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, bool BACK>
 hipError_t route_any(const RouteArgs& a, bool given, hipStream_t st) {
   auto go = [&](auto v) {
-    if constexpr (BACK) return route_back<T, decltype(v)::value>(a, st);
-    else return route<T, decltype(v)::value>(a, given, st);
+    constexpr int V = decltype(v)::value;
+    const bool even = a.experts % (V < 8 ? V : 8) == 0;
+    if constexpr (BACK) return even ? route_back<T, V, true>(a, st) : route_back<T, V, false>(a, st);
+    else return even ? route<T, V, true>(a, given, st) : route<T, V, false>(a, given, st);
   };
   switch (per_lane(a.experts)) {
     case 1: return go(std::integral_constant<int, 1>{});
