@@ -440,29 +440,46 @@ __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
   *a.loss = loss;
 }
 
-constexpr int kRouteThreads = 256, kRouteGroups = kRouteThreads / 16;  // of the backward pass
+// The logits' gradient: the same lanes to a token.  What the weights add falls on
+// the topk chosen experts: each lane has a choice and adds it to a row in LDS
+// that is zero otherwise, and from which the lanes take their experts' parts.
+constexpr int kBackThreads = 256, kBackGroups = kBackThreads / 16;
 
 template <typename T, int V, bool EVEN>
-__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs a) {
-  const int tid = threadIdx.x, li = tid & 15, lane = tid & 63, at = li * V;
+__global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs a) {
+  __shared__ __attribute__((aligned(16))) float adds[kBackGroups][16 * V];
+  const int tid = threadIdx.x, li = tid & 15, at = li * V, n = a.experts - at;
+  float* add = adds[tid >> 4];
   float slope[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) slope[i] = 0.0f;
+  for (int i = 0; i < V; ++i) {
+    slope[i] = 0.0f;
+    add[at + i] = 0.0f;
+  }
   if (a.dloss) {
     const float d = *a.dloss;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (at + i < a.experts) slope[i] = d * a.slope[at + i];
+      if (i < n) slope[i] = d * a.slope[at + i];
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * kRouteGroups; t0 < a.tokens; t0 += (int64_t)gridDim.x * kRouteGroups) {
-    const int64_t t = t0 + (tid >> 4);
-    const bool there = t < a.tokens;
+  const int tokens = (int)a.tokens, step = (int)gridDim.x * kBackGroups;  // (at most 2^30 tokens)
+  for (int t = (int)blockIdx.x * kBackGroups + (tid >> 4); __any(t < tokens); t += step) {
+    const bool there = t < tokens;
     const bool real = there && (!a.mask || a.mask[t]);
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const int slot = t * a.topk;
     Logits<T, V, EVEN> raw;
-    if (real) raw.load(row + at, a.experts - at);
+    if (real) raw.load(row + at, n);
+    int mine = -1;  // the lane's first choice and its gradient
+    float dw = 0.0f, chosen = 0.0f;
+    if (a.dweights && real && li < a.topk) {
+      mine = a.expert[slot + li];
+      dw = a.dweights[slot + li];
+      if ((unsigned)mine < (unsigned)a.experts) chosen = logit_at(row, mine);
+      else mine = -1;
+    }
     float v[V], most, s, dot = 0.0f;
-    raw.get(v, real ? a.experts - at : 0);
+    raw.get(v, real ? n : 0);
     const bool live = exponentials<V>(v, most, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) dot += v[i] * slope[i];
@@ -470,66 +487,90 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
     const float inv = live ? 1.0f / s : 0.0f;
     dot *= inv;
 
-    // the weights' part: an addition to the chosen experts' elements each, and
-    // (where they are not normalized) one more dot product
-    float d[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.0f;
     if (a.dweights) {
-      float total = 0.0f, along = 0.0f;  // sums over the chosen of e^ and of e^ dw
-      for (int j = li; j < a.topk; j += 16) {
-        const int e = real ? a.expert[t * a.topk + j] : -1;
-        if (e >= 0 && e < a.experts) {
-          const float w = weight_of(logit_at(row, e), most);
-          total += w;
-          along += w * a.dweights[t * a.topk + j];
-        }
-      }
-      total = row16_sum(total);
-      along = row16_sum(along);
-      const float unit = !live || (a.normalize && total == 0.0f) ? 0.0f : (a.normalize ? 1.0f / total : inv);
-      along *= unit;
-      if (!a.normalize) dot += along;
-      for (int base = 0; base < a.topk; base += 16) {
-        int e = -1;
-        float add = 0.0f;
-        if (real && base + li < a.topk) {
-          e = a.expert[t * a.topk + base + li];
-          if (e >= 0 && e < a.experts) {
-            add = weight_of(logit_at(row, e), most) * unit * (a.dweights[t * a.topk + base + li] - (a.normalize ? along : 0.0f));
+      // the choices' e^, their sum and that of e^ dw
+      const float w = mine >= 0 ? weight_of(chosen, most) : 0.0f;
+      float total = w, along = w * dw;
+      if (mine < 0) along = 0.0f;
+      if (a.topk > 16 && real)
+        for (int j = li + 16; j < a.topk; j += 16) {
+          const int e = a.expert[slot + j];
+          if ((unsigned)e < (unsigned)a.experts) {
+            const float x = weight_of(logit_at(row, e), most);
+            total += x;
+            along += x * a.dweights[slot + j];
           }
         }
-        const int last = min(a.topk - base, 16);
-        for (int j = 0; j < last; ++j) {
-          const int ej = __shfl(e, (lane & 48) | j, 64);
-          const float aj = __shfl(add, (lane & 48) | j, 64);
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (at + i == ej) d[i] += aj;
+      along = row16_sum(along);
+      float unit = inv;  // e^ to weight
+      if (a.normalize) {
+        total = row16_sum(total);
+        unit = live && total != 0.0f ? 1.0f / total : 0.0f;
+      }
+      along *= unit;
+      if (!a.normalize) dot += along;
+      const float less = a.normalize ? along : 0.0f;
+      if (mine >= 0) atomicAdd(add + mine, w * unit * (dw - less));
+      if (a.topk > 16 && real)
+        for (int j = li + 16; j < a.topk; j += 16) {
+          const int e = a.expert[slot + j];
+          if ((unsigned)e < (unsigned)a.experts)
+            atomicAdd(add + e, weight_of(logit_at(row, e), most) * unit * (a.dweights[slot + j] - less));
         }
+      // (the group's lanes are in one wave, whose LDS operations stay in order)
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = v[i] * inv * (slope[i] - dot);
+      if (a.dweights) v[i] += add[at + i];
+      if (!live) v[i] = 0.0f;
+    }
+    if (a.dweights) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (mine >= 0) add[mine] = 0.0f;
+      if (a.topk > 16) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) add[at + i] = 0.0f;
       }
     }
     if (there) {
-      T* out = static_cast<T*>(a.dlogits) + t * a.ld_dlogits;
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = live ? d[i] + v[i] * inv * (slope[i] - dot) : 0.0f;
+      T* out = static_cast<T*>(a.dlogits) + t * a.ld_dlogits + at;
       if constexpr (V >= 8) {
 #pragma unroll
         for (int c = 0; c < V / 8; ++c) {
           Chunk<T> k;
           float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = d[8 * c + e];
+          for (int e = 0; e < 8; ++e) w[e] = v[8 * c + e];
           k.set(w);
-          k.store(out + at + 8 * c, a.experts - at - 8 * c);
+          if constexpr (EVEN) {
+            if (n > 8 * c) k.store(out + 8 * c, 8);
+          } else {
+            k.store(out + 8 * c, n - 8 * c);
+          }
         }
       } else {
+        T o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at + i < a.experts) {
-            if constexpr (sizeof(T) == 2) out[at + i] = __builtin_bit_cast(uint16_t, (__bf16)d[i]);
-            else out[at + i] = d[i];
-          }
+        for (int i = 0; i < V; ++i) {
+          if constexpr (sizeof(T) == 2) o[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+          else o[i] = v[i];
+        }
+        if constexpr (EVEN && V > 1) {
+          typename Logits<T, V, EVEN>::vec x;
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] = o[i];
+          if (n > 0) *reinterpret_cast<typename Logits<T, V, EVEN>::vec*>(out) = x;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i < n) out[i] = o[i];
+        }
       }
     }
   }
@@ -579,8 +620,8 @@ hipError_t route(const RouteArgs& a, bool given, hipStream_t st) {
 
 template <typename T, int V, bool EVEN>
 hipError_t route_back(const RouteArgs& a, hipStream_t st) {
-  const int64_t groups = (a.tokens + kRouteGroups - 1) / kRouteGroups, most = 8 * (int64_t)cu_count(stream_device(st));
-  route_backward_kernel<T, V, EVEN><<<(unsigned)(groups < most ? groups : most), kRouteThreads, 0, st>>>(a);
+  const int64_t groups = (a.tokens + kBackGroups - 1) / kBackGroups, most = 8 * (int64_t)cu_count(stream_device(st));
+  route_backward_kernel<T, V, EVEN><<<(unsigned)(groups < most ? groups : most), kBackThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
