@@ -7,8 +7,9 @@
 //   slope_e = d loss / d p_te = experts f_e / n (the counts have no gradient),
 //   dp = dloss slope + (the weights' part), dl = p (dp - <p, dp>).
 //
-// 16 lanes own a token, V neighbouring experts each, so that a maximum or a sum
-// over the experts is one of V registers and four DPP rotations; the next
+// G lanes own a token (16 up to 256 experts, so that a maximum or a sum over them
+// is one of V registers and four DPP rotations; above, a wave), V experts each, in
+// vectors of at most 16 bytes of which the lanes' lie side by side.  The next
 // token's logits are on their way while one is worked on.
 //
 // The choice.  Logits are compared as integers that order like them, with the
@@ -35,15 +36,16 @@ namespace {
 constexpr int kRouteMaxBlocks = 256;
 constexpr int kRouteOneBlock = 4;  // tokens per group of lanes up to which there is one workgroup, and one launch
 
-// threads of the forward pass: as many as the registers of V experts allow
-constexpr int route_threads(int v) { return v <= 16 ? 1024 : (v <= 32 ? 512 : 256); }
-// experts per lane: the power of two that 16 lanes hold them with
+// lanes that own a token, and the experts of a lane: the power of two that they
+// hold them with
+constexpr int lanes_of(int64_t experts) { return experts <= 256 ? 16 : 64; }
 constexpr int per_lane(int64_t experts) {
   int v = 1;
-  while (16 * v < experts) v *= 2;
+  while (lanes_of(experts) * v < experts) v *= 2;
   return v;
 }
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+constexpr int kRouteThreads = 1024;
 
 struct RouteArgs {
   const void* logits;
@@ -73,17 +75,40 @@ struct RouteArgs {
 __device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
 __device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
 
-__device__ __forceinline__ float row16_sum(float v) {
+// over the G lanes of a token; all of them get it
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
   v += as_float(dpp<0x128>(as_bits(v)));
   v += as_float(dpp<0x124>(as_bits(v)));
   v += as_float(dpp<0x122>(as_bits(v)));
-  return v + as_float(dpp<0x121>(as_bits(v)));
+  v += as_float(dpp<0x121>(as_bits(v)));
+  if constexpr (G == 64) {
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+  }
+  return v;
 }
-__device__ __forceinline__ float row16_fmax(float v) {
+template <int G>
+__device__ __forceinline__ float lanes_fmax(float v) {
   v = fmaxf(v, as_float(dpp<0x128>(as_bits(v))));
   v = fmaxf(v, as_float(dpp<0x124>(as_bits(v))));
   v = fmaxf(v, as_float(dpp<0x122>(as_bits(v))));
-  return fmaxf(v, as_float(dpp<0x121>(as_bits(v))));
+  v = fmaxf(v, as_float(dpp<0x121>(as_bits(v))));
+  if constexpr (G == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    v = fmaxf(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = row16_max(v);
+  if constexpr (G == 64) {  // (the four rows' are scalars)
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    v = umax32(umax32(a, b), umax32(c, d));
+  }
+  return v;
 }
 
 constexpr float kNegInf = -__builtin_inff();
@@ -101,54 +126,47 @@ __device__ __forceinline__ float weight_of(float v, float most) {
   return __builtin_amdgcn_exp2f((v - most) * 1.44269504088896340736f);
 }
 
-// V logits as they lie in memory, of which n are there.  EVEN: the number of
-// experts is a multiple of V, or of 8, so that no vector is cut.
-template <typename T, int V, bool EVEN>
+// A lane's experts: vectors of kWide, G lanes of them and then the next.  expert()
+// is the number of the i-th without the lane's part, which is lane() and shares
+// no bit with it.
+template <typename T, int G, int V>
+struct Own {
+  static constexpr int kWide = V < 16 / (int)sizeof(T) ? V : 16 / (int)sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(kWide < 2 ? 2 : kWide), aligned(sizeof(T))));
+  static constexpr __host__ __device__ int expert(int i) { return i / kWide * G * kWide + i % kWide; }
+  static __device__ __forceinline__ int lane() { return (threadIdx.x & (G - 1)) * kWide; }
+};
+
+// V logits as they lie in memory, of which those below n - lane() are there.
+// EVEN: the number of experts is a multiple of kWide, so that no vector is cut.
+template <typename T, int G, int V, bool EVEN>
 struct Logits {
-  static constexpr int kChunks = V >= 8 ? V / 8 : 1;
-  typedef T vec __attribute__((ext_vector_type(V == 4 ? 4 : 2), aligned(sizeof(T))));
-  Chunk<T> c[kChunks];
-  T e[V >= 8 ? 1 : V];
+  using O = Own<T, G, V>;
+  typename O::vec c[V / O::kWide];
   __device__ __forceinline__ void load(const T* p, int n) {
-    if constexpr (V >= 8) {
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        if constexpr (EVEN) {
-          if (n > 8 * k) c[k].load(p + 8 * k, 8);
-        } else {
-          c[k].load(p + 8 * k, n - 8 * k);
-        }
-      }
-    } else if constexpr (V == 1) {
-      if (n > 0) e[0] = p[0];
-    } else {
-      if (EVEN ? n > 0 : n >= V) {
-        const vec v = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = v[i];
+    for (int k = 0; k < V / O::kWide; ++k) {
+      const T* q = p + O::expert(k * O::kWide);
+      const int left = n - O::expert(k * O::kWide);
+      if constexpr (O::kWide == 1) {
+        if (left > 0) c[k][0] = *q;
+      } else if (EVEN ? left > 0 : left >= O::kWide) {
+        c[k] = *reinterpret_cast<const typename O::vec*>(q);
       } else if constexpr (!EVEN) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < n) e[i] = p[i];
+        for (int i = 0; i < O::kWide; ++i)
+          if (i < left) c[k][i] = q[i];
       }
     }
   }
   // -inf past the end
   __device__ __forceinline__ void get(float (&v)[V], int n) const {
-    if constexpr (V >= 8) {
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        float w[8];
-        c[k].get(w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * k + i] = (EVEN ? 8 * k : 8 * k + i) < n ? w[i] : kNegInf;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (sizeof(T) == 2) v[i] = (EVEN ? 0 : i) < n ? bf_lo(e[i]) : kNegInf;
-        else v[i] = (EVEN ? 0 : i) < n ? e[i] : kNegInf;
-      }
+    for (int i = 0; i < V; ++i) {
+      const bool has = O::expert(EVEN ? i / O::kWide * O::kWide : i) < n;
+      const T e = c[i / O::kWide][i % O::kWide];
+      if constexpr (sizeof(T) == 2) v[i] = has ? bf_lo(e) : kNegInf;
+      else v[i] = has ? e : kNegInf;
     }
   }
 };
@@ -161,12 +179,12 @@ __device__ __forceinline__ float logit_at(const T* row, int e) {
 
 // v becomes e^(v - most) with a token's largest logit, most; s: their sum.  False,
 // and zeros, for a token of nothing but -inf (one with a NaN, too, has NaNs).
-template <int V>
+template <int G, int V>
 __device__ __forceinline__ bool exponentials(float (&v)[V], float& most, float& s) {
   most = v[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
-  most = row16_fmax(most);
+  most = lanes_fmax<G>(most);
   const float by = most == kNegInf ? 0.0f : most;
   s = 0.0f;
 #pragma unroll
@@ -174,28 +192,29 @@ __device__ __forceinline__ bool exponentials(float (&v)[V], float& most, float& 
     v[i] = weight_of(v[i], by);
     s += v[i];
   }
-  s = row16_sum(s);
+  s = lanes_sum<G>(s);
   if (s != s) most = s;
   return most != kNegInf;
 }
 
 // The `last` (at most 16) next choices of a token, one for each lane to keep; -1
 // for none.  key: 0 where taken or not to be chosen.
-template <int V>
+template <typename T, int G, int V>
 __device__ __forceinline__ int choose_exact(uint32_t (&key)[V], int last) {
-  const int li = threadIdx.x & 15, at = li * V;
+  using O = Own<T, G, V>;
+  const int li = threadIdx.x & (G - 1), at = O::lane();
   int mine = -1;
   for (int j = 0; j < last; ++j) {
     uint32_t best = key[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) best = umax32(best, key[i]);
-    best = row16_max(best);
+    best = lanes_max<G>(best);
     int e = 0x4000;  // the lowest expert that has it
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i) e = key[i] == best ? i : e;
-    e = 0x7FFF - (int)row16_max((uint32_t)(0x7FFF - at - e));
+    for (int i = V - 1; i >= 0; --i) e = key[i] == best ? O::expert(i) : e;
+    e = 0x7FFF - (int)lanes_max<G>((uint32_t)(0x7FFF - at - e));
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = e - at == i ? 0 : key[i];
+    for (int i = 0; i < V; ++i) key[i] = e - at == O::expert(i) ? 0 : key[i];
     if (li == j) mine = best ? e : -1;
   }
   return mine;
@@ -210,27 +229,29 @@ __device__ __forceinline__ float settle(const RouteArgs& a, int e, int c, float 
   return slope * p;
 }
 
-template <typename T, int V, bool EVEN, bool CHOSEN>
-__global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
-  constexpr int NT = route_threads(V), kGroups = NT / 16, kWaves = NT / 64;
-  constexpr int kBits = log2_of(16 * V);  // of an expert's number
+template <typename T, int G, int V, bool EVEN, bool CHOSEN>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+  constexpr int NT = kRouteThreads, kGroups = NT / G, kWaves = NT / 64;
+  constexpr int kAll = G * V;              // experts that there is room for
+  constexpr int kBits = log2_of(kAll);     // of an expert's number
   constexpr uint32_t kLow = (1u << kBits) - 1;
-  __shared__ int cnt[16 * V + 1];
-  __shared__ float sums[kWaves][16 * V];
-  const int tid = threadIdx.x, li = tid & 15, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e <= 16 * V; e += NT) cnt[e] = 0;
+  __shared__ int cnt[kAll + 1];
+  __shared__ float sums[kWaves][kAll];
+  const int tid = threadIdx.x, li = tid & (G - 1), lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e <= kAll; e += NT) cnt[e] = 0;
   __syncthreads();
-  const int at = li * V, n = a.experts - at;  // this lane's experts, of which n are there
-  float ps[V];                                // sums of p
+  using O = Own<T, G, V>;
+  const int at = O::lane(), n = a.experts - at;
+  float ps[V];  // sums of p
 #pragma unroll
   for (int i = 0; i < V; ++i) ps[i] = 0.0f;
   int held = 0;  // tokens counted
   const T* logits = static_cast<const T*>(a.logits);
   const int tokens = (int)a.tokens, step = a.blocks * kGroups;  // (at most 2^30 tokens)
-  const int t_first = blockIdx.x * kGroups + (tid >> 4);
+  const int t_first = blockIdx.x * kGroups + tid / G;
   const bool few = a.topk <= 16;
 
-  Logits<T, V, EVEN> next;
+  Logits<T, G, V, EVEN> next{};
   bool next_real = t_first < tokens && (!a.mask || a.mask[t_first]);
   if (next_real) next.load(logits + t_first * a.ld + at, n);
   // (whole waves go round together: the lanes of a group are never apart)
@@ -243,14 +264,16 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
     next_real = t + step < tokens && (!a.mask || a.mask[t + step]);
     if (next_real) next.load(row + step * a.ld + at, n);
     if constexpr (!CHOSEN) {
+      uint32_t from_top = kAll - 1 - at;
+      asm volatile("" : "+v"(from_top));  // (or V registers would hold the experts' numbers from token to token)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const uint32_t b = as_bits(e[i] + 0.0f);
         const uint32_t k = __builtin_elementwise_sub_sat(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 0x007FFFFFu);
-        pk[i] = ((k & ~kLow) | (uint32_t)(16 * V - 1 - at)) ^ (uint32_t)i;  // (the expert's number from the top)
+        pk[i] = ((k & ~kLow) | from_top) ^ (uint32_t)O::expert(i);  // (the expert's number from the top)
       }
     }
-    const bool live = exponentials<V>(e, most, s);
+    const bool live = exponentials<G, V>(e, most, s);
     const float inv = live ? 1.0f / s : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) ps[i] += e[i] * inv;
@@ -258,7 +281,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
 
     if constexpr (CHOSEN) {
       if (live)
-        for (int j = li; j < a.topk; j += 16) {
+        for (int j = li; j < a.topk; j += G) {
           int64_t x;
           if (a.wide) x = static_cast<const int64_t*>(a.chosen)[t * a.ld_chosen + j];
           else x = static_cast<const int32_t*>(a.chosen)[t * a.ld_chosen + j];
@@ -271,7 +294,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
         uint32_t best = pk[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) best = umax32(best, pk[i]);
-        best = row16_max(best);
+        best = lanes_max<G>(best);
         bool odd = s != s;
         for (int j = 0; j < a.topk; ++j) {
           if (li == j) mine = (int)(~best & kLow);
@@ -280,7 +303,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
           uint32_t other = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) other = umax32(other, pk[i] - best);
-          other = row16_max(other) + best;
+          other = lanes_max<G>(other) + best;
           if (sizeof(T) == 4) odd = odd || (other ^ best) <= kLow;
           best = other;
         }
@@ -288,7 +311,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
       }
       const int slot = t * a.topk;
       if (again) {
-        Logits<T, V, EVEN> raw;
+        Logits<T, G, V, EVEN> raw{};
         float v[V];
         uint32_t key[V];
         if (real) raw.load(row + at, n);
@@ -296,11 +319,11 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
         if (few) {
-          mine = choose_exact<V>(key, a.topk);
+          mine = choose_exact<T, G, V>(key, a.topk);
         } else {
           for (int base = 0; base < a.topk; base += 16) {
-            mine = choose_exact<V>(key, min(a.topk - base, 16));
-            if (there && base + li < a.topk) a.expert[slot + base + li] = mine;
+            mine = choose_exact<T, G, V>(key, min(a.topk - base, 16));
+            if (there && li < 16 && base + li < a.topk) a.expert[slot + base + li] = mine;
           }
         }
       }
@@ -313,7 +336,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
           atomicAdd(&cnt[mine], 1);
           w = weight_of(logit_at(row, mine), most);
         }
-        if (a.normalize) total = row16_sum(w);
+        if (a.normalize) total = lanes_sum<G>(w);
         if (there && li < a.topk) {
           a.expert[slot + li] = has ? mine : -1;
           a.weights[slot + li] = !has ? 0.0f : (a.normalize ? w / total : w * inv);
@@ -321,7 +344,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
       } else {
         for (int pass = a.normalize ? 0 : 1; pass < 2; ++pass) {
           const float by = a.normalize ? 1.0f / total : inv;
-          if (there)
+          if (there && li < 16)
             for (int j = li; j < a.topk; j += 16) {
               const int x = a.expert[slot + j];
               const float w = x >= 0 ? weight_of(logit_at(row, x), most) : 0.0f;
@@ -332,20 +355,22 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
                 if (x >= 0) atomicAdd(&cnt[x], 1);
               }
             }
-          if (pass == 0) total = row16_sum(total);
+          if (pass == 0) total = lanes_sum<G>(total);
         }
       }
     }
   }
 
-  // the workgroup's sums: the four groups of a wave, then the waves
+  // the workgroup's sums: the groups of a wave, then the waves
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    ps[i] += __shfl_xor(ps[i], 16, 64);
-    ps[i] += __shfl_xor(ps[i], 32, 64);
-    if (lane < 16) sums[wave][at + i] = ps[i];
+    if constexpr (G == 16) {
+      ps[i] += __shfl_xor(ps[i], 16, 64);
+      ps[i] += __shfl_xor(ps[i], 32, 64);
+    }
+    if (lane < G) sums[wave][at + O::expert(i)] = ps[i];
   }
-  if (li == 0 && held) atomicAdd(&cnt[16 * V], held);
+  if (li == 0 && held) atomicAdd(&cnt[kAll], held);
   __syncthreads();
   auto sum_of = [&](int e) {
     float p = 0.0f;
@@ -356,7 +381,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
   if (a.blocks == 1) {  // all there is
     __shared__ float parts[kWaves];
     float loss = 0.0f;
-    for (int e = tid; e < a.experts; e += NT) loss += settle(a, e, cnt[e], sum_of(e), cnt[16 * V]);
+    for (int e = tid; e < a.experts; e += NT) loss += settle(a, e, cnt[e], sum_of(e), cnt[kAll]);
     loss = wave_sum(loss);
     if (lane == 0) parts[wave] = loss;
     __syncthreads();
@@ -372,7 +397,7 @@ __global__ __launch_bounds__(route_threads(V)) void route_kernel(RouteArgs a) {
     a.hist[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
   }
   if (tid == 0) {
-    a.held[blockIdx.x] = cnt[16 * V];
+    a.held[blockIdx.x] = cnt[kAll];
     if (blockIdx.x == 0) *a.ticket = 0;
   }
 }
@@ -443,32 +468,34 @@ __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
 // The logits' gradient: the same lanes to a token.  What the weights add falls on
 // the topk chosen experts: each lane has a choice and adds it to a row in LDS
 // that is zero otherwise, and from which the lanes take their experts' parts.
-constexpr int kBackThreads = 256, kBackGroups = kBackThreads / 16;
+constexpr int kBackThreads = 256, kBackBlocks = 4;  // workgroups per compute unit
 
-template <typename T, int V, bool EVEN>
+template <typename T, int G, int V, bool EVEN>
 __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs a) {
-  __shared__ __attribute__((aligned(16))) float adds[kBackGroups][16 * V];
-  const int tid = threadIdx.x, li = tid & 15, at = li * V, n = a.experts - at;
-  float* add = adds[tid >> 4];
+  constexpr int kGroups = kBackThreads / G;
+  __shared__ __attribute__((aligned(16))) float adds[kGroups][G * V];
+  using O = Own<T, G, V>;
+  const int tid = threadIdx.x, li = tid & (G - 1), at = O::lane(), n = a.experts - at;
+  float* add = adds[tid / G];
   float slope[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     slope[i] = 0.0f;
-    add[at + i] = 0.0f;
+    add[at + O::expert(i)] = 0.0f;
   }
   if (a.dloss) {
     const float d = *a.dloss;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < n) slope[i] = d * a.slope[at + i];
+      if (O::expert(i) < n) slope[i] = d * a.slope[at + O::expert(i)];
   }
-  const int tokens = (int)a.tokens, step = (int)gridDim.x * kBackGroups;  // (at most 2^30 tokens)
-  for (int t = (int)blockIdx.x * kBackGroups + (tid >> 4); __any(t < tokens); t += step) {
+  const int tokens = (int)a.tokens, step = (int)gridDim.x * kGroups;  // (at most 2^30 tokens)
+  Logits<T, G, V, EVEN> raw{};
+  for (int t = (int)blockIdx.x * kGroups + tid / G; __any(t < tokens); t += step) {
     const bool there = t < tokens;
     const bool real = there && (!a.mask || a.mask[t]);
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     const int slot = t * a.topk;
-    Logits<T, V, EVEN> raw;
     if (real) raw.load(row + at, n);
     int mine = -1;  // the lane's first choice and its gradient
     float dw = 0.0f, chosen = 0.0f;
@@ -480,10 +507,10 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
     }
     float v[V], most, s, dot = 0.0f;
     raw.get(v, real ? n : 0);
-    const bool live = exponentials<V>(v, most, s);
+    const bool live = exponentials<G, V>(v, most, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) dot += v[i] * slope[i];
-    dot = row16_sum(dot);
+    dot = lanes_sum<G>(dot);
     const float inv = live ? 1.0f / s : 0.0f;
     dot *= inv;
 
@@ -492,8 +519,8 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
       const float w = mine >= 0 ? weight_of(chosen, most) : 0.0f;
       float total = w, along = w * dw;
       if (mine < 0) along = 0.0f;
-      if (a.topk > 16 && real)
-        for (int j = li + 16; j < a.topk; j += 16) {
+      if (a.topk > G && real)
+        for (int j = li + G; j < a.topk; j += G) {
           const int e = a.expert[slot + j];
           if ((unsigned)e < (unsigned)a.experts) {
             const float x = weight_of(logit_at(row, e), most);
@@ -501,18 +528,18 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
             along += x * a.dweights[slot + j];
           }
         }
-      along = row16_sum(along);
+      along = lanes_sum<G>(along);
       float unit = inv;  // e^ to weight
       if (a.normalize) {
-        total = row16_sum(total);
+        total = lanes_sum<G>(total);
         unit = live && total != 0.0f ? 1.0f / total : 0.0f;
       }
       along *= unit;
       if (!a.normalize) dot += along;
       const float less = a.normalize ? along : 0.0f;
       if (mine >= 0) atomicAdd(add + mine, w * unit * (dw - less));
-      if (a.topk > 16 && real)
-        for (int j = li + 16; j < a.topk; j += 16) {
+      if (a.topk > G && real)
+        for (int j = li + G; j < a.topk; j += G) {
           const int e = a.expert[slot + j];
           if ((unsigned)e < (unsigned)a.experts)
             atomicAdd(add + e, weight_of(logit_at(row, e), most) * unit * (a.dweights[slot + j] - less));
@@ -525,7 +552,7 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       v[i] = v[i] * inv * (slope[i] - dot);
-      if (a.dweights) v[i] += add[at + i];
+      if (a.dweights) v[i] += add[at + O::expert(i)];
       if (!live) v[i] = 0.0f;
     }
     if (a.dweights) {
@@ -533,43 +560,33 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       if (mine >= 0) add[mine] = 0.0f;
-      if (a.topk > 16) {
+      if (a.topk > G) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) add[at + i] = 0.0f;
+        for (int i = 0; i < V; ++i) add[at + O::expert(i)] = 0.0f;
       }
     }
     if (there) {
       T* out = static_cast<T*>(a.dlogits) + t * a.ld_dlogits + at;
-      if constexpr (V >= 8) {
 #pragma unroll
-        for (int c = 0; c < V / 8; ++c) {
-          Chunk<T> k;
-          float w[8];
+      for (int c = 0; c < V; c += O::kWide) {
+        T o[O::kWide];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = v[8 * c + e];
-          k.set(w);
-          if constexpr (EVEN) {
-            if (n > 8 * c) k.store(out + 8 * c, 8);
-          } else {
-            k.store(out + 8 * c, n - 8 * c);
-          }
+        for (int i = 0; i < O::kWide; ++i) {
+          if constexpr (sizeof(T) == 2) o[i] = __builtin_bit_cast(uint16_t, (__bf16)v[c + i]);
+          else o[i] = v[c + i];
         }
-      } else {
-        T o[V];
+        const int left = n - O::expert(c);
+        if constexpr (O::kWide == 1) {
+          if (left > 0) out[O::expert(c)] = o[0];
+        } else if (EVEN ? left > 0 : left >= O::kWide) {
+          typename O::vec x;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if constexpr (sizeof(T) == 2) o[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
-          else o[i] = v[i];
-        }
-        if constexpr (EVEN && V > 1) {
-          typename Logits<T, V, EVEN>::vec x;
+          for (int i = 0; i < O::kWide; ++i) x[i] = o[i];
+          *reinterpret_cast<typename O::vec*>(out + O::expert(c)) = x;
+        } else if constexpr (!EVEN) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[i] = o[i];
-          if (n > 0) *reinterpret_cast<typename Logits<T, V, EVEN>::vec*>(out) = x;
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i < n) out[i] = o[i];
+          for (int i = 0; i < O::kWide; ++i)
+            if (i < left) out[O::expert(c) + i] = o[i];
         }
       }
     }
@@ -608,47 +625,50 @@ RouteArgs args_of(const RouteParams& p) {
   return a;
 }
 
-template <typename T, int V, bool EVEN>
+template <typename T, int G, int V, bool EVEN>
 hipError_t route(const RouteArgs& a, bool given, hipStream_t st) {
-  if (given) route_kernel<T, V, EVEN, true><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
-  else route_kernel<T, V, EVEN, false><<<(unsigned)a.blocks, route_threads(V), 0, st>>>(a);
+  if (given) route_kernel<T, G, V, EVEN, true><<<(unsigned)a.blocks, kRouteThreads, 0, st>>>(a);
+  else route_kernel<T, G, V, EVEN, false><<<(unsigned)a.blocks, kRouteThreads, 0, st>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 1) return e;
   route_sum_kernel<<<(unsigned)((a.experts + kSumExperts - 1) / kSumExperts), kSumThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int V, bool EVEN>
+template <typename T, int G, int V, bool EVEN>
 hipError_t route_back(const RouteArgs& a, hipStream_t st) {
-  const int64_t groups = (a.tokens + kBackGroups - 1) / kBackGroups, most = 8 * (int64_t)cu_count(stream_device(st));
-  route_backward_kernel<T, V, EVEN><<<(unsigned)(groups < most ? groups : most), kBackThreads, 0, st>>>(a);
+  constexpr int kGroups = kBackThreads / G;
+  const int64_t need = (a.tokens + kGroups - 1) / kGroups, most = kBackBlocks * (int64_t)cu_count(stream_device(st));
+  route_backward_kernel<T, G, V, EVEN><<<(unsigned)(need < most ? need : most), kBackThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, bool BACK>
 hipError_t route_any(const RouteArgs& a, bool given, hipStream_t st) {
-  auto go = [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    const bool even = a.experts % (V < 8 ? V : 8) == 0;
-    if constexpr (BACK) return even ? route_back<T, V, true>(a, st) : route_back<T, V, false>(a, st);
-    else return even ? route<T, V, true>(a, given, st) : route<T, V, false>(a, given, st);
+  auto go = [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    const bool even = a.experts % Own<T, G, V>::kWide == 0;
+    if constexpr (BACK) return even ? route_back<T, G, V, true>(a, st) : route_back<T, G, V, false>(a, st);
+    else return even ? route<T, G, V, true>(a, given, st) : route<T, G, V, false>(a, given, st);
   };
+  const std::integral_constant<int, 16> row;
+  const std::integral_constant<int, 64> wave;
+  const std::integral_constant<int, 8> v8;
+  const std::integral_constant<int, 16> v16;
   switch (per_lane(a.experts)) {
-    case 1: return go(std::integral_constant<int, 1>{});
-    case 2: return go(std::integral_constant<int, 2>{});
-    case 4: return go(std::integral_constant<int, 4>{});
-    case 8: return go(std::integral_constant<int, 8>{});
-    case 16: return go(std::integral_constant<int, 16>{});
-    case 32: return go(std::integral_constant<int, 32>{});
+    case 1: return go(row, std::integral_constant<int, 1>{});
+    case 2: return go(row, std::integral_constant<int, 2>{});
+    case 4: return go(row, std::integral_constant<int, 4>{});
+    case 8: return lanes_of(a.experts) == 16 ? go(row, v8) : go(wave, v8);
   }
-  return go(std::integral_constant<int, 64>{});
+  return lanes_of(a.experts) == 16 ? go(row, v16) : go(wave, v16);
 }
 
 }  // namespace
 
 // workgroups of the forward pass
 int64_t route_blocks(int64_t tokens, int64_t experts) {
-  const int64_t groups = route_threads(per_lane(experts)) / 16;
+  const int64_t groups = kRouteThreads / lanes_of(experts);
   if (tokens <= kRouteOneBlock * groups) return 1;
   const int64_t n = (tokens + groups - 1) / groups;
   return n < kRouteMaxBlocks ? n : kRouteMaxBlocks;
