@@ -27,9 +27,13 @@ namespace fp8mi {
 
 namespace {
 
-// workgroups that leave column sums, as in the layer norm
+// Workgroups that leave column sums: each set is 4 bytes per column, written and
+// read again, so they are no more than fill the GPU, and each takes 4 rows at
+// least, fewer where that leaves compute units without work (64 x 2560: 1 row 6.5
+// us, 2 7.8, 4 10.8; 256 x 4096: 8.8, 8.5, 10.2; 1000 x 4000 FP32: 16.7, 15.1,
+// 15.6).
 constexpr int kMaxPartials = 512;
-constexpr int kRowsPerPartial = 4;
+constexpr int rows_per_partial(int64_t rows) { return rows <= 128 ? 1 : (rows <= 1024 ? 2 : 4); }
 
 struct RmsArgs {
   const void* x;         // backward: t
@@ -754,7 +758,9 @@ hipError_t backward_cols(const RmsParams& p, hipStream_t st) {
   if (p.cols <= 512) return backward<T, 64, 1, 1, PAST>(p, st);
   if (p.cols <= 1024) return backward<T, 64, 2, 1, PAST>(p, st);
   if (p.cols <= 2048) return backward<T, 256, 1, 2, PAST>(p, st);
-  if (p.cols <= 4096) return backward<T, 256, 2, 2, PAST>(p, st);
+  // (a row of 4096 FP32: 8192 rows 83 us by 256 threads of two chunks, 80 by 512 of
+  // one; BF16 50.7 and 54.7)
+  if (p.cols <= 4096) return backward<T, sizeof(T) == 4 ? 512 : 256, sizeof(T) == 4 ? 1 : 2, 2, PAST>(p, st);
   if (p.cols <= 8192) return backward<T, 512, 2, 2, PAST>(p, st);
   return backward<T, 1024, 2, 0, PAST>(p, st);
 }
@@ -779,7 +785,7 @@ hipError_t backward_any(const RmsParams& p, hipStream_t st) {
 
 // sets of column sums that a backward pass over `rows` rows may leave
 int64_t rms_partials(int64_t rows) {
-  const int64_t n = (rows + kRowsPerPartial - 1) / kRowsPerPartial;
+  const int64_t per = rows_per_partial(rows), n = (rows + per - 1) / per;
   return n < 1 ? 1 : (n < kMaxPartials ? n : kMaxPartials);
 }
 
