@@ -109,7 +109,7 @@ def load(path: str = LIB_PATH):
     lib.fp8_rms_norm_forward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, i64, vp, vp]
     lib.fp8_rms_norm_quantize.restype = i32
     lib.fp8_rms_norm_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, i32, i32, i32, i32,
-                                          vp, i64, vp, vp, i64, vp, vp, vp]
+                                          vp, i64, vp, vp, i64, vp, vp, vp, vp, vp]
     lib.fp8_rms_norm_workspace.restype = i64
     lib.fp8_rms_norm_workspace.argtypes = [i64, i64]
     lib.fp8_rms_norm_backward.restype = i32
@@ -282,12 +282,12 @@ def fp8_rms_norm_forward(x, x_dtype, rows, cols, ld_x, residual, ld_residual, we
 
 
 def fp8_rms_norm_quantize(x, x_dtype, rows, cols, ld_x, residual, ld_residual, weight, w_dtype, eps, total, ld_total, rstd,
-                          recipe, fmt, orient, margin, q_row, ld_q_row, s_row, q_col, ld_q_col, s_col, nonfinite,
-                          stream=None) -> int:
+                          recipe, fmt, orient, margin, q_row, ld_q_row, s_row, q_col, ld_q_col, s_col, scale, amax,
+                          nonfinite, stream=None) -> int:
     return load().fp8_rms_norm_quantize(_p(x), x_dtype, rows, cols, ld_x, _p(residual), ld_residual, _p(weight), w_dtype,
                                         eps, _p(total), ld_total, _p(rstd), recipe, fmt, orient, margin, _p(q_row),
-                                        ld_q_row, _p(s_row), _p(q_col), ld_q_col, _p(s_col), _p(nonfinite),
-                                        _stream(stream))
+                                        ld_q_row, _p(s_row), _p(q_col), ld_q_col, _p(s_col), _p(scale), _p(amax),
+                                        _p(nonfinite), _stream(stream))
 
 
 def fp8_rms_norm_workspace(rows, cols) -> int:

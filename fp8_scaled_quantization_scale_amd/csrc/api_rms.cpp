@@ -84,14 +84,15 @@ int fp8_rms_norm_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols
                           int64_t ld_residual, const void* weight, int w_dtype, float eps, void* total,
                           int64_t ld_total, float* rstd, int recipe, int fmt, int orient, int margin, uint8_t* q_row,
                           int64_t ld_q_row, void* s_row, uint8_t* q_col, int64_t ld_q_col, void* s_col,
-                          int32_t* nonfinite, void* stream) {
+                          const float* scale, float* amax, int32_t* nonfinite, void* stream) {
   int st = check_common(x_dtype, w_dtype, rows, cols);
   if (st != FP8MI_OK) return st;
   if (recipe < FP8MI_TENSOR_CURRENT || recipe > FP8MI_MX_1x32_OCP) return FP8MI_ERR_ENUM;
   if (fmt != FP8MI_E4M3 && fmt != FP8MI_E5M2) return FP8MI_ERR_ENUM;
   if (orient != FP8MI_ROW && orient != FP8MI_COL && orient != FP8MI_ROW_AND_COL) return FP8MI_ERR_ENUM;
-  // scales that are local to a row's or a column's block only
-  if (recipe != FP8MI_BLOCK_1x128 && recipe != FP8MI_MX_1x32 && recipe != FP8MI_MX_1x32_OCP)
+  // scales that are local to a row's or a column's block, or known beforehand
+  const bool delayed = recipe == FP8MI_TENSOR_DELAYED;
+  if (!delayed && recipe != FP8MI_BLOCK_1x128 && recipe != FP8MI_MX_1x32 && recipe != FP8MI_MX_1x32_OCP)
     return FP8MI_ERR_UNSUPPORTED;
   if (!(eps >= 0.0f) || margin < 0 || margin > 64) return FP8MI_ERR_SHAPE;
   if (rows == 0) return FP8MI_OK;
@@ -99,17 +100,19 @@ int fp8_rms_norm_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols
                          rstd)) != FP8MI_OK)
     return st;
   const bool row = orient & FP8MI_ROW, col = orient & FP8MI_COL;
-  if ((row && (!q_row || !s_row)) || (col && (!q_col || !s_col))) return FP8MI_ERR_NULL;
+  if ((row && !q_row) || (col && !q_col)) return FP8MI_ERR_NULL;
+  if (delayed ? !scale || !amax : (row && !s_row) || (col && !s_col)) return FP8MI_ERR_NULL;
   if ((row && (ld_q_row < cols || !span_ok(rows, ld_q_row, 1))) || (col && (ld_q_col < rows || !span_ok(cols, ld_q_col, 1))))
     return FP8MI_ERR_SHAPE;
   const int64_t ss = recipe == FP8MI_BLOCK_1x128 ? 4 : 1;
   if ((row && (!aligned_to(q_row, 16) || ld_q_row % 16 || !aligned_to(s_row, ss))) ||
-      (col && (!aligned_to(q_col, 16) || ld_q_col % 16 || !aligned_to(s_col, ss))) || !aligned_to(nonfinite, 4))
+      (col && (!aligned_to(q_col, 16) || ld_q_col % 16 || !aligned_to(s_col, ss))) || !aligned_to(nonfinite, 4) || !aligned_to(scale, 4) ||
+      !aligned_to(amax, 4))
     return FP8MI_ERR_ALIGN;
   fp8mi::RmsParams p =
       params(x, x_dtype, rows, cols, ld_x, residual, ld_residual, weight, w_dtype, eps, total, ld_total, rstd);
   p.q = fp8mi::QuantParams{nullptr, x_dtype, rows, cols, 0, recipe, fmt, orient, margin, q_row, ld_q_row, s_row,
-                           q_col, ld_q_col, s_col, nullptr, nullptr, nullptr, nonfinite};
+                           q_col, ld_q_col, s_col, const_cast<float*>(scale), nullptr, amax, nonfinite};
   return fp8mi::hip_status(fp8mi::launch_rms_quantize(p, (hipStream_t)stream));
 }
 

@@ -110,6 +110,7 @@ int fp8_moe_route_backward(const void* logits, int dtype, int64_t tokens, int64_
                            void* stream) {
   int st = check_routing(dtype, tokens, experts, topk);
   if (st != FP8MI_OK) return st;
+  if (dweights && topk > experts) return FP8MI_ERR_SHAPE;
   if (tokens == 0) return FP8MI_OK;
   if ((st = check_matrix(logits, tokens, experts, ld_logits, in_size(dtype))) != FP8MI_OK) return st;
   if ((st = check_matrix(dlogits, tokens, experts, ld_dlogits, in_size(dtype))) != FP8MI_OK) return st;
@@ -123,7 +124,7 @@ int fp8_moe_route_backward(const void* logits, int dtype, int64_t tokens, int64_
   p.experts = experts;
   p.ld = ld_logits;
   p.mask = mask;
-  p.topk = topk;
+  p.topk = dweights ? topk : 1;
   p.normalize = normalize != 0;
   p.expert = const_cast<int32_t*>(expert);
   p.slope = const_cast<float*>(slope);

@@ -220,15 +220,6 @@ struct Raw<float> {
   }
 };
 
-// Delayed scaling: the convert-only encoder is exact for a chunk whose
-// largest magnitude m is finite with fl32(m * s) <= max (every product then
-// rounds to at most max); anything else takes the saturating encoder.
-template <int FMT>
-__device__ __forceinline__ bool fits(uint32_t key, float s) {
-  const float m = key_to_float(key);
-  return m <= kFltMax && m * s <= Fmt<FMT>::kMax;
-}
-
 // Persistent workgroups: each walks tiles blockIdx.x, blockIdx.x + gridDim.x,
 // ... and prefetches the next tile's raw words into registers while the
 // current one is processed, so every workgroup always has a tile in flight.

@@ -54,9 +54,11 @@ struct RmsArgs {
   int64_t ld_q;
   int margin, floor_rule;
   int32_t* nonfinite;
+  const float* scale;  // delayed: the tensor's, and a slot of |y|'s maximum per workgroup
+  uint32_t* amax;
 };
 
-enum : int { OUT_VALUES = 0, OUT_BLOCK = 1, OUT_MX = 2 };  // what a forward kernel leaves
+enum : int { OUT_VALUES = 0, OUT_BLOCK = 1, OUT_MX = 2, OUT_TENSOR = 3 };  // what a forward kernel leaves
 
 // 8 weights as floats (1 without one; 0 past the end)
 __device__ __forceinline__ void load_weight(float (&v)[8], const RmsArgs& a, int col, int n) {
@@ -76,12 +78,17 @@ __device__ __forceinline__ void load_weight(float (&v)[8], const RmsArgs& a, int
 
 // Codes and scale of a lane's 8 elements of row `row` from column `col` on, n
 // of them in the row (zeros past its end); every lane of the block calls it.
+// `s` and `most`: the tensor's scale and the largest |y| so far (OUT_TENSOR).
 template <int OUT, int FMT>
-__device__ __forceinline__ void put_codes(const RmsArgs& a, int64_t row, int col, int n, const float (&y)[8]) {
+__device__ __forceinline__ void put_codes(const RmsArgs& a, int64_t row, int col, int n, const float (&y)[8], float s,
+                                          uint32_t& most) {
   uint32_t key = max8_key(y);
-  float s;
   bool safe;
-  if constexpr (OUT == OUT_BLOCK) {
+  if constexpr (OUT == OUT_TENSOR) {
+    if (n > 0) most = umax32(most, key);
+    safe = !fits<FMT>(key, s);
+    if (!a.q) return;
+  } else if constexpr (OUT == OUT_BLOCK) {
     key = row16_max(key);
     const float am = key_to_float(key);
     s = scale_from_amax<FMT>(am, a.margin);
@@ -107,6 +114,19 @@ __device__ __forceinline__ void put_codes(const RmsArgs& a, int64_t row, int col
 }
 
 // AGAIN: t is read again by the launch that follows
+// OUT_TENSOR: the workgroup's largest |y| into its slot (one workgroup's alone:
+// the grid is no more than there are slots), beside what is there.
+__device__ __forceinline__ void put_amax(const RmsArgs& a, uint32_t most) {
+  __shared__ uint32_t red[16];
+  most = group_max_u32<64>(most);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (unsigned w = 1; w < blockDim.x / 64; ++w) most = umax32(most, red[w]);
+    a.amax[blockIdx.x] = umax32(a.amax[blockIdx.x], most);
+  }
+}
+
 template <typename T, int NT, int C, int OUT, int FMT, bool PAST, bool AGAIN>
 __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) {
   constexpr int kRows = threads_of(NT) / NT;  // rows per workgroup at a time
@@ -119,6 +139,8 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
 
   int col[C], n[C];
   float w[C][8];
+  const float scale = OUT == OUT_TENSOR ? *a.scale : 1.0f;
+  uint32_t most = 0;
   Chunk<T> cx[C], cr[C], nx[C], nr[C];
   auto fetch = [&](Chunk<T>(&x)[C], Chunk<T>(&r)[C], int64_t at) __attribute__((always_inline)) {
     if (at < a.rows) {
@@ -169,12 +191,13 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
           o.template store<PAST>(static_cast<T*>(a.out) + row * a.ld_out + col[c], n[c]);
         }
       } else {
-        put_codes<OUT, FMT>(a, row, col[c], n[c], v[c]);
+        put_codes<OUT, FMT>(a, row, col[c], n[c], v[c], scale, most);
       }
       cx[c] = nx[c];
       cr[c] = nr[c];
     }
   }
+  if constexpr (OUT == OUT_TENSOR) put_amax(a, most);
 }
 
 // Rows too long for registers: a second pass over each, from the caches.
@@ -184,6 +207,8 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
   __shared__ float red[2][1][16];
   int turn = 0;
   const float inv = 1.0f / (float)a.cols;
+  const float scale = OUT == OUT_TENSOR ? *a.scale : 1.0f;
+  uint32_t most = 0;
   // (whole turns of the workgroup: the lanes of a block go together)
   const int end = (a.cols + NT * 8 - 1) / (NT * 8) * (NT * 8);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -225,10 +250,11 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
         k.set(v);
         k.store(static_cast<T*>(a.out) + row * a.ld_out + col, a.cols - col);
       } else {
-        put_codes<OUT, FMT>(a, row, col, a.cols - col, v);
+        put_codes<OUT, FMT>(a, row, col, a.cols - col, v, scale, most);
       }
     }
   }
+  if constexpr (OUT == OUT_TENSOR) put_amax(a, most);
 }
 
 // ---------------------------------------------------------------------------
@@ -247,6 +273,7 @@ __global__ __launch_bounds__(kColThreads, sizeof(T) == 2 ? 6 : 4) void rms_colum
   __shared__ float rs[kTile];
   const int tid = threadIdx.x, g = tid >> 4, li = tid & 15;
   const int cp = tid & 63, rq = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const float scale = OUT == OUT_TENSOR ? *a.scale : 1.0f;
   for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
     const int64_t t = tiles - 1 - i;  // the rows written last are in the caches
     const int64_t by = t / tiles_x, row0 = by * kTile;
@@ -303,7 +330,7 @@ __global__ __launch_bounds__(kColThreads, sizeof(T) == 2 ? 6 : 4) void rms_colum
       k0 = umax32(k0, abs_key(u0[j]));
       k1 = umax32(k1, abs_key(u1[j]));
     }
-    colred[rq][cp] = make_uint2(k0, k1);
+    if constexpr (OUT != OUT_TENSOR) colred[rq][cp] = make_uint2(k0, k1);
     __syncthreads();  // (every wave has read the rows, too)
     if constexpr (OUT == OUT_BLOCK) {
 #pragma unroll
@@ -312,7 +339,7 @@ __global__ __launch_bounds__(kColThreads, sizeof(T) == 2 ? 6 : 4) void rms_colum
         k0 = umax32(k0, o.x);
         k1 = umax32(k1, o.y);
       }
-    } else {
+    } else if constexpr (OUT == OUT_MX) {
       const uint2 o = colred[rq ^ 1][cp];  // the block's other 16 rows
       k0 = umax32(k0, o.x);
       k1 = umax32(k1, o.y);
@@ -320,7 +347,10 @@ __global__ __launch_bounds__(kColThreads, sizeof(T) == 2 ? 6 : 4) void rms_colum
     const float am0 = key_to_float(k0), am1 = key_to_float(k1);
     float s0, s1;
     bool odd = false;  // a block may need the saturating encoder
-    if constexpr (OUT == OUT_BLOCK) {
+    if constexpr (OUT == OUT_TENSOR) {
+      s0 = s1 = scale;
+      odd = !fits<FMT>(umax32(k0, k1), scale);
+    } else if constexpr (OUT == OUT_BLOCK) {
       s0 = scale_from_amax<FMT>(am0, a.margin);
       s1 = scale_from_amax<FMT>(am1, a.margin);
       const bool bad0 = !is_finite(am0), bad1 = !is_finite(am1);
@@ -651,6 +681,8 @@ RmsArgs args_of(const RmsParams& p) {
   a.margin = p.q.margin;
   a.floor_rule = p.q.recipe == kRecipeMx1x32Ocp;
   a.nonfinite = p.q.nonfinite;
+  a.scale = p.q.scale;
+  a.amax = reinterpret_cast<uint32_t*>(p.q.amax);
   return a;
 }
 
@@ -659,7 +691,9 @@ hipError_t forward(const RmsArgs& a, hipStream_t st) {
   static std::atomic<int> occupancy{0};
   auto k = rms_forward_kernel<T, NT, C, OUT, FMT, PAST, AGAIN>;
   constexpr int threads = threads_of(NT), rows = threads / NT;
-  const int64_t need = (a.rows + rows - 1) / rows, most = resident(k, threads, occupancy, st);
+  const int64_t need = (a.rows + rows - 1) / rows;
+  int64_t most = resident(k, threads, occupancy, st);
+  if (OUT == OUT_TENSOR && most > kAmaxSlots) most = kAmaxSlots;
   k<<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -672,7 +706,8 @@ hipError_t forward_cols(const RmsArgs& a, hipStream_t st) {
   if (a.cols <= 4096) return forward<T, 256, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 8192) return forward<T, 512, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 16384) return forward<T, 1024, 2, OUT, FMT, PAST, AGAIN>(a, st);
-  const int64_t most = 2 * (int64_t)cu_count(stream_device(st));
+  int64_t most = 2 * (int64_t)cu_count(stream_device(st));
+  if (OUT == OUT_TENSOR && most > kAmaxSlots) most = kAmaxSlots;
   rms_forward_long_kernel<T, OUT, FMT><<<(unsigned)(a.rows < most ? a.rows : most), 1024, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -696,13 +731,14 @@ hipError_t columns(const RmsArgs& a, hipStream_t st) {
 template <typename T, int OUT, int FMT>
 hipError_t quantize(const RmsParams& p, hipStream_t st) {
   RmsArgs a = args_of(p);
-  a.q = p.q.q_row;
+  a.q = p.q.orient & 1 ? p.q.q_row : nullptr;
   a.ld_q = p.q.ld_q_row;
   a.scales = p.q.s_row;
   const bool past = past_caches(p), col = p.q.orient & 2;
   if (!col) return forward_any<T, OUT, FMT, false>(a, past, st);
-  const hipError_t e = p.q.orient & 1 ? forward_any<T, OUT, FMT, true>(a, past, st)
-                                      : forward_any<T, OUT_VALUES, kE4M3, true>(a, past, st);
+  // (delayed scaling takes the maximum of y whatever the orientation)
+  const hipError_t e = p.q.orient & 1 || OUT == OUT_TENSOR ? forward_any<T, OUT, FMT, true>(a, past, st)
+                                                           : forward_any<T, OUT_VALUES, kE4M3, true>(a, past, st);
   if (e != hipSuccess) return e;
   if (p.residual) {
     a.x = p.total;
@@ -717,6 +753,8 @@ hipError_t quantize(const RmsParams& p, hipStream_t st) {
 template <typename T>
 hipError_t quantize_any(const RmsParams& p, hipStream_t st) {
   const bool block = p.q.recipe == kRecipeBlock1x128;
+  if (p.q.recipe == kRecipeTensorDelayed)
+    return p.q.fmt == kE4M3 ? quantize<T, OUT_TENSOR, kE4M3>(p, st) : quantize<T, OUT_TENSOR, kE5M2>(p, st);
   if (p.q.fmt == kE4M3) return block ? quantize<T, OUT_BLOCK, kE4M3>(p, st) : quantize<T, OUT_MX, kE4M3>(p, st);
   return block ? quantize<T, OUT_BLOCK, kE5M2>(p, st) : quantize<T, OUT_MX, kE5M2>(p, st);
 }

@@ -61,6 +61,15 @@ __device__ __forceinline__ uint32_t max8_key(const float v[8]) {
   return k;
 }
 
+// Delayed scaling: the convert-only encoder is exact for a chunk whose
+// largest magnitude m is finite with fl32(m * s) <= max (every product then
+// rounds to at most max); anything else takes the saturating encoder.
+template <int FMT>
+__device__ __forceinline__ bool fits(uint32_t key, float s) {
+  const float m = key_to_float(key);
+  return m <= kFltMax && m * s <= Fmt<FMT>::kMax;
+}
+
 // max |x| key of 8 BF16 values packed in a uint4: packed 16-bit max of the
 // sign-cleared halves (non-negative BF16 orders like its bits, NaN on top).
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));

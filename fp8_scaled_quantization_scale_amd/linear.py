@@ -191,11 +191,20 @@ class _Role:
     def cast(self, x2d: torch.Tensor, orient: int, interval: int):
         st = self.state
         q = quantize(x2d, TENSOR_DELAYED, st.fmt, orient, st.margin, scale=st.scale, amax=st.amax)
-        q.scale_inv = st.scale_inv.clone()  # the pair this cast used; an update replaces it
+        self._paced(q, interval)
+        return q
+
+    def norm_cast(self, x2d, norm_weight, residual, eps, orient: int, interval: int):
+        st = self.state
+        out = _norm.rms_norm_quantize(x2d, TENSOR_DELAYED, st.fmt, orient, norm_weight, residual, eps, st.margin, st.scale, st.amax)
+        self._paced(out[0], interval)
+        return out
+
+    def _paced(self, q, interval: int):
+        q.scale_inv = self.state.scale_inv.clone()  # the pair this cast used; an update replaces it
         self.casts += 1
         if self.casts % interval == 0:
-            st.update()
-        return q
+            self.state.update()
 
 
 def _cast(role: str, x2d, orient, p: Plan, states, interval):
@@ -324,74 +333,82 @@ class Linear(torch.nn.Module):
         self._roles, self._roles_key = roles, state["key"]
 
 
+def _norm_cast(x2d, norm_weight, residual, eps, orient, p: Plan, states, interval):
+    """The norm straight into the codes of role x: (Quantized, total, rstd)."""
+    rec, fmt = p.quant["x"]
+    if rec == TENSOR_DELAYED:
+        return states["x"].norm_cast(x2d, norm_weight, residual, eps, orient, interval)
+    return _norm.rms_norm_quantize(x2d, rec, fmt, orient, norm_weight, residual, eps, p.margin)
+
+
 class _RmsNormLinearFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x2d, residual, norm_weight, weight, eps, p: Plan, need_dx, need_dw):
+    def forward(ctx, x2d, residual, norm_weight, weight, eps, p: Plan, states, interval, need_dx, need_dw):
         ctx.set_materialize_grads(False)
         M, K = x2d.shape
         N = weight.shape[0]
-        (rx, fx), (rw, fw) = p.quant["x"], p.quant["w"]
-        qx, total, rstd = _norm.rms_norm_quantize(x2d, rx, fx, ROW | (COL if need_dw else 0), norm_weight, residual, eps)
-        qw = quantize(weight, rw, fw, ROW | (COL if need_dx else 0))
-        y = gemm(qx.q_row, fx, qx.s_row, qw.q_row, fw, qw.s_row, p.gemm["fprop"], K,
+        rx, rw = p.quant["x"][0], p.quant["w"][0]
+        qx, total, rstd = _norm_cast(x2d, norm_weight, residual, eps, ROW | (COL if need_dw else 0), p, states, interval)
+        qw = _cast("w", weight, ROW | (COL if need_dx else 0), p, states, interval)
+        y = gemm(qx.q_row, qx.fmt, _scales(qx, rx, ROW), qw.q_row, qw.fmt, _scales(qw, rw, ROW), p.gemm["fprop"], K,
                  torch.float32 if x2d.dtype == torch.float32 else torch.bfloat16, M=M, N=N)
-        ctx.p, ctx.need, ctx.shape, ctx.dtypes = p, (need_dx, need_dw), (M, N, K), (x2d.dtype, weight.dtype)
-        ctx.save_for_backward(total, norm_weight, rstd, *((qx.q_col, qx.s_col) if need_dw else (None, None)),
-                              *((qw.q_col, qw.s_col) if need_dx else (None, None)))
+        ctx.p, ctx.states, ctx.interval, ctx.need = p, states, interval, (need_dx, need_dw)
+        ctx.shape, ctx.dtypes, ctx.fmts = (M, N, K), (x2d.dtype, weight.dtype), (qx.fmt, qw.fmt)
+        ctx.save_for_backward(total, norm_weight, rstd, *((qx.q_col, _scales(qx, rx, COL)) if need_dw else (None, None)),
+                              *((qw.q_col, _scales(qw, rw, COL)) if need_dx else (None, None)))
         return y if residual is None else (y, total)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dtotal=None):
         total, norm_weight, rstd, qxt, sxt, qwt, swt = ctx.saved_tensors
-        p, (need_dx, need_dw), (M, N, K) = ctx.p, ctx.need, ctx.shape
+        p, (need_dx, need_dw), (M, N, K), (fx, fw) = ctx.p, ctx.need, ctx.shape, ctx.fmts
         need = ctx.needs_input_grad
         dn = dw = None
         if dy is not None:
-            (_, fx), (_, fw), (rg, fg) = p.quant["x"], p.quant["w"], p.quant["g"]
             dy = _dense(dy)
             if dy.dtype not in (torch.bfloat16, torch.float32):
                 dy = dy.float()
-            qg = quantize(dy, rg, fg, (ROW if need_dx else 0) | (COL if need_dw else 0))
+            qg = _cast("g", dy, (ROW if need_dx else 0) | (COL if need_dw else 0), p, ctx.states, ctx.interval)
+            rg = p.quant["g"][0]
             if need_dx:  # the norm's output gradient [M x K]
-                dn = gemm(qg.q_row, fg, qg.s_row, qwt, fw, swt, p.gemm["dgrad"], N,
+                dn = gemm(qg.q_row, qg.fmt, _scales(qg, rg, ROW), qwt, fw, swt, p.gemm["dgrad"], N,
                           torch.float32 if ctx.dtypes[0] == torch.float32 else torch.bfloat16, M=M, N=K)
             if need_dw:
-                dw = gemm(qg.q_col, fg, qg.s_col, qxt, fx, sxt, p.gemm["wgrad"], M,
+                dw = gemm(qg.q_col, qg.fmt, _scales(qg, rg, COL), qxt, fx, sxt, p.gemm["wgrad"], M,
                           torch.float32 if ctx.dtypes[1] == torch.float32 else torch.bfloat16, M=N, N=K)
         elif need_dw:
             dw = torch.zeros(N, K, dtype=ctx.dtypes[1], device=total.device)
         dx = dnw = None
         if need_dx:
             dx, dnw = _norm._rms_norm_grads(dn, total, norm_weight, rstd, dtotal, need[0] or need[1], need[2])
-        return dx if need[0] else None, dx if need[1] else None, dnw, dw, None, None, None, None
+        return dx if need[0] else None, dx if need[1] else None, dnw, dw, None, None, None, None, None, None
 
 
-class RMSNormLinear(torch.nn.Module):
+class RMSNormLinear(Linear):
     """RMS norm and the FP8 linear layer after it: y = norm(x) W^T, with the norm's
     output cast to FP8 as it is made, so that it is neither written nor rounded to
     x's type.  ``forward(x)`` gives y; ``forward(x, residual)`` gives (y of x +
     residual, x + residual).  Several layers on one norm are one ``weight`` with
     their rows one after the other.  The recipes are those whose scales stay inside
-    a block (Float8BlockScaling and MXFP8BlockScaling); sizes as for Linear."""
+    a block or are known beforehand (Float8BlockScaling, MXFP8BlockScaling and
+    DelayedScaling); sizes and state as for Linear."""
 
     def __init__(self, in_features: int, out_features: int, eps: float = 1e-6, recipe=None, device=None,
                  dtype=torch.bfloat16):
-        super().__init__()
-        if in_features < 16 or in_features % 16 or out_features % 16:
-            raise Fp8Error("in_features and out_features must be multiples of 16")
-        self.in_features, self.out_features, self.eps, self.recipe = in_features, out_features, eps, recipe
+        if in_features < 16:
+            raise Fp8Error("in_features must be positive")
+        super().__init__(in_features, out_features, recipe=recipe, device=device, dtype=dtype)
+        self.eps = eps
         self.norm_weight = torch.nn.Parameter(torch.ones(in_features, device=device, dtype=dtype))
-        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
-        torch.nn.init.kaiming_uniform_(self.weight, a=5 ** 0.5)
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
         r = active_recipe() or self.recipe
         if r is None:
             raise Fp8Error("no FP8 recipe: pass recipe= or call inside fp8_autocast")
         p = plan(r)
-        if not isinstance(r, (Float8BlockScaling, MXFP8BlockScaling)):
-            raise Fp8Error("the norm's output is cast by the block recipes only: other scales need all of it first")
+        if not isinstance(r, (Float8BlockScaling, MXFP8BlockScaling, DelayedScaling)):
+            raise Fp8Error("the norm's output is cast by the block recipes and delayed scaling: other scales need all of it first")
         _norm._check_layer_input(x, residual, self.weight, self.in_features)
         if not self.norm_weight.is_cuda or self.norm_weight.dtype not in (torch.bfloat16, torch.float32):
             raise Fp8Error("weights are BF16 or FP32, on the GPU")
@@ -403,7 +420,10 @@ class RMSNormLinear(torch.nn.Module):
         need_dw = grad and self.weight.requires_grad
         if need_dw and x2d.shape[0] % 16:
             raise Fp8Error("the token count must be a multiple of 16 when the weight needs a gradient")
-        out = _RmsNormLinearFn.apply(x2d, r2d, self.norm_weight, self.weight.contiguous(), self.eps, p, need_dx, need_dw)
+        states = self._delayed_states(r, p, x.device) if isinstance(r, DelayedScaling) else None
+        interval = r.interval if isinstance(r, DelayedScaling) else 1
+        out = _RmsNormLinearFn.apply(x2d, r2d, self.norm_weight, self.weight.contiguous(), self.eps, p, states, interval, need_dx,
+                                     need_dw)
         if residual is None:
             return out.reshape(*lead, self.out_features)
         return out[0].reshape(*lead, self.out_features), out[1].reshape(x.shape)

@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (BLOCK_1x128, COL, IN_BF16, IN_FP32, MX_1x32, MX_1x32_OCP, ROW, Fp8Error, Quantized, _at, _check, _dense,
+from . import (AMAX_SLOTS, BLOCK_1x128, COL, IN_BF16, IN_FP32, MX_1x32, MX_1x32_OCP, ROW, TENSOR_DELAYED, Fp8Error, Quantized, _at, _check, _dense,
                _here, _is_matrix, _is_vector, _ld, _matrix, _one_device, _pad16, _scope, _vector, load, scale_grid_shape)
 
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
@@ -177,10 +177,11 @@ def rms_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, residu
 
 def rms_norm_quantize(x: torch.Tensor, recipe: int, fmt: int, orient: int = ROW, weight: torch.Tensor | None = None,
                       residual: torch.Tensor | None = None, eps: float = 1e-6, margin: int = 0,
+                      scale: torch.Tensor | None = None, amax: torch.Tensor | None = None,
                       nonfinite: torch.Tensor | None = None, stream=None):
     """(Quantized, total, rstd): rms_norm_forward with the FP8 codes and scales of
-    y in its place, cast from the FP32 y.  recipe: BLOCK_1x128, MX_1x32 or
-    MX_1x32_OCP."""
+    y in its place, cast from the FP32 y.  recipe: BLOCK_1x128, MX_1x32, MX_1x32_OCP,
+    or TENSOR_DELAYED with the scale and the amax accumulator of quantize."""
     _check_x(x)
     _like("residual", residual, x)
     if nonfinite is not None:
@@ -188,9 +189,12 @@ def rms_norm_quantize(x: torch.Tensor, recipe: int, fmt: int, orient: int = ROW,
     rows, cols = x.shape
     w_dtype = _params(cols, weight, None)
     _one_device(x, weight, residual, nonfinite)
-    if recipe not in (BLOCK_1x128, MX_1x32, MX_1x32_OCP):
-        raise Fp8Error("the norm takes the recipes BLOCK_1x128, MX_1x32 and MX_1x32_OCP: the others' scales need the whole "
-                       "matrix before the first code")
+    delayed = recipe == TENSOR_DELAYED
+    if not delayed and recipe not in (BLOCK_1x128, MX_1x32, MX_1x32_OCP):
+        raise Fp8Error("the norm takes the recipes BLOCK_1x128, MX_1x32, MX_1x32_OCP and TENSOR_DELAYED: the others' scales "
+                       "need the whole matrix before the first code")
+    if not delayed and (scale is not None or amax is not None):
+        raise Fp8Error("scale and amax belong to TENSOR_DELAYED")
     dev = x.device
     out = Quantized(fmt=fmt, recipe=recipe, nonfinite=nonfinite)
     ld_r, ld_c = _pad16(cols), _pad16(rows)
@@ -198,18 +202,26 @@ def rms_norm_quantize(x: torch.Tensor, recipe: int, fmt: int, orient: int = ROW,
         if orient & ROW:
             out.q_row = torch.empty(rows, ld_r, dtype=torch.uint8, device=dev)
             shp, dt = scale_grid_shape(recipe, rows, cols, ROW)
-            out.s_row = torch.empty(shp, dtype=dt, device=dev)
+            if not delayed:
+                out.s_row = torch.empty(shp, dtype=dt, device=dev)
         if orient & COL:
             out.q_col = torch.empty(cols, ld_c, dtype=torch.uint8, device=dev)
             shp, dt = scale_grid_shape(recipe, rows, cols, COL)
-            out.s_col = torch.empty(shp, dtype=dt, device=dev)
+            if not delayed:
+                out.s_col = torch.empty(shp, dtype=dt, device=dev)
+        if delayed:
+            out.scale = torch.ones(1, dtype=torch.float32, device=dev) if scale is None else scale
+            out.amax = torch.zeros(AMAX_SLOTS, dtype=torch.float32, device=dev) if amax is None else amax
+            _vector("scale", out.scale, torch.float32, 1)
+            _vector("amax", out.amax, torch.float32, AMAX_SLOTS)
+            _one_device(x, out.scale, out.amax)
         total = x if residual is None else torch.empty(rows, cols, dtype=x.dtype, device=dev)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
         st = load().fp8_rms_norm_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, _ld(x), _at(residual),
                                           0 if residual is None else _ld(residual), _at(weight), _DTYPES[w_dtype], eps,
                                           None if residual is None else total.data_ptr(), cols, rstd.data_ptr(), recipe, fmt,
                                           orient, margin, _at(out.q_row), ld_r, _at(out.s_row), _at(out.q_col), ld_c,
-                                          _at(out.s_col), _at(nonfinite), _here(dev))
+                                          _at(out.s_col), _at(out.scale), _at(out.amax), _at(nonfinite), _here(dev))
     _check(st, "fp8_rms_norm_quantize")
     return out, total, rstd
 

@@ -326,7 +326,9 @@ int fp8_rms_norm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols,
 
 /* fp8_rms_norm_quantize -- the FP8 codes and scales of y in place of y: as
  * fp8_quantize of a [rows x cols] matrix that holds y in FP32 (y is not rounded
- * to x's type first).  recipe: BLOCK_1x128, MX_1x32 or MX_1x32_OCP (others:
+ * to x's type first).  recipe: BLOCK_1x128, MX_1x32, MX_1x32_OCP, or
+ * TENSOR_DELAYED, whose scale and amax (FP8MI_AMAX_SLOTS floats) are as for
+ * fp8_quantize and not used by the others (other recipes:
  * FP8MI_ERR_UNSUPPORTED).  x, residual and total need the alignment of their
  * element only; outputs, scale layouts, alignment and nonfinite as for
  * fp8_quantize; total, rstd and the other arguments as for
@@ -336,7 +338,7 @@ int fp8_rms_norm_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols
                           const void* residual, int64_t ld_residual, const void* weight, int w_dtype, float eps,
                           void* total, int64_t ld_total, float* rstd, int recipe, int fmt, int orient, int margin,
                           uint8_t* q_row, int64_t ld_q_row, void* s_row, uint8_t* q_col, int64_t ld_q_col, void* s_col,
-                          int32_t* nonfinite, void* stream);
+                          const float* scale, float* amax, int32_t* nonfinite, void* stream);
 
 /* fp8_rms_norm_workspace -- bytes of device memory that the weight's gradient
  * needs (each workgroup's column sums); negative: an error. */

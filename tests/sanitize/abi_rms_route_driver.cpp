@@ -89,7 +89,7 @@ int rms_forward(const Args& a) {  // rows, cols, ld_x, ld_residual, ld_total, ld
 }
 int rms_quantize(const Args& a) {  // rows, cols, ld_x, ld_residual, ld_total, ld_q_row, ld_q_col, margin
   return fp8_rms_norm_quantize(P, FP8MI_IN_BF16, a[0], a[1], a[2], P, a[3], P, FP8MI_IN_FP32, 1e-6f, P, a[4], F, FP8MI_MX_1x32,
-                               FP8MI_E5M2, FP8MI_ROW_AND_COL, (int)a[7], U, a[5], U, U, a[6], U, I, nullptr);
+                               FP8MI_E5M2, FP8MI_ROW_AND_COL, (int)a[7], U, a[5], U, U, a[6], U, nullptr, nullptr, I, nullptr);
 }
 int rms_backward(const Args& a) {  // rows, cols, ld_dy, ld_total, ld_dtotal, ld_dx, workspace_bytes
   return fp8_rms_norm_backward(P, a[2], P, FP8MI_IN_BF16, a[0], a[1], a[3], P, FP8MI_IN_FP32, F, P, a[4], P, a[5], P, P, a[6], nullptr);

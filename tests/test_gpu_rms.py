@@ -15,7 +15,7 @@ import torch
 
 import fp8_scaled_quantization_scale_amd as fm
 from fp8_scaled_quantization_scale_amd import linear, norm
-from gpu_util import need_gpu
+from gpu_util import acc_amax, need_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -137,6 +137,36 @@ def test_codes(rows, cols, ld, dt, wdt, recipe):
         assert (q.q_row is None) == (orient == fm.COL) and (q.q_col is None) == (orient == fm.ROW)
 
 
+@pytest.mark.parametrize("rows,cols,ld,dt,wdt", QUANT, ids=[f"{r}x{c}" for r, c, *_ in QUANT])
+def test_codes_of_delayed_scaling(rows, cols, ld, dt, wdt):
+    """Under a scale known beforehand (some values beyond the format's largest): the
+    cast's codes of the FP32 product, and its largest magnitude beside what the
+    accumulator holds, in every orientation."""
+    need_gpu()
+    x, res, w, _, _ = _inputs(rows, cols, ld, dt, wdt)
+    fmt = (fm.E4M3, fm.E5M2)[(rows + cols) % 2]
+    scale = torch.tensor([150.0 if fmt == fm.E4M3 else 20000.0], device="cuda")
+    for orient, res_ in ((fm.ROW_AND_COL, res), (fm.ROW, None), (fm.COL, res)):
+        amax = torch.zeros(fm.AMAX_SLOTS, device="cuda")
+        q, total, rstd = norm.rms_norm_quantize(x, fm.TENSOR_DELAYED, fmt, orient, w, res_, scale=scale, amax=amax)
+        prod = _product(total, rstd, w)
+        want = fm.quantize(prod, fm.TENSOR_DELAYED, fmt, orient, scale=scale)
+        if orient & fm.ROW:
+            assert torch.equal(q.q_row[:, :cols], want.q_row[:, :cols])
+        if orient & fm.COL:
+            assert torch.equal(q.q_col[:, :rows], want.q_col[:, :rows])
+        assert q.amax is amax and acc_amax(amax) == acc_amax(want.amax) == prod.abs().max().item()
+        norm.rms_norm_quantize(0.5 * x, fm.TENSOR_DELAYED, fmt, orient, None, None, scale=scale, amax=amax)
+        assert acc_amax(amax) >= acc_amax(want.amax)
+    bad = x.clone()
+    bad[rows // 2, cols // 2] = float("nan")
+    amax = torch.zeros(fm.AMAX_SLOTS, device="cuda")
+    q, _, rstd = norm.rms_norm_quantize(bad, fm.TENSOR_DELAYED, fmt, fm.ROW_AND_COL, w, None, scale=scale, amax=amax)
+    want = fm.quantize(_product(bad, rstd, w), fm.TENSOR_DELAYED, fmt, fm.ROW_AND_COL, scale=scale)
+    assert torch.equal(q.q_row[:, :cols], want.q_row[:, :cols]) and torch.equal(q.q_col[:, :rows], want.q_col[:, :rows])
+    assert acc_amax(amax) != acc_amax(amax)
+
+
 @pytest.mark.parametrize("fmt,u,least", [(fm.E4M3, 2.0 ** -4, 2.0 ** -10), (fm.E5M2, 2.0 ** -3, 2.0 ** -17)])
 def test_codes_stand_for_the_norm(fmt, u, least):
     """Codes times scales against y in 64 bits: half a step of the code's value, or
@@ -171,7 +201,7 @@ def test_neighbours_are_left_alone():
         nr, nc = rows * -(-cols // per), cols * -(-rows // per)
         sr, sc = (torch.full((n + 8,), 7, device="cuda").to(dtype) for n in (nr, nc))
         assert fm.fp8_rms_norm_quantize(x, fm.IN_BF16, rows, cols, ld, res, ld, w, fm.IN_FP32, 1e-6, out[0, 1:], ld, st[1:],
-                                        recipe, fm.E4M3, fm.ROW_AND_COL, 0, cr[1:], 1056, sr[4:], cc[1:], 64, sc[4:], None) == fm.OK
+                                        recipe, fm.E4M3, fm.ROW_AND_COL, 0, cr[1:], 1056, sr[4:], cc[1:], 64, sc[4:], None, None, None) == fm.OK
         assert torch.equal(cr[1:-1, :cols], q.q_row[:, :cols]) and torch.equal(cc[1:-1, :rows], q.q_col[:, :rows])
         assert (cr[1:-1, cols:] == 7).all() and (cr[0] == 7).all() and (cr[-1] == 7).all()
         assert (cc[1:-1, rows:] == 7).all() and (cc[0] == 7).all() and (cc[-1] == 7).all()
@@ -336,6 +366,43 @@ def test_norm_linear(recipe, dt):
         assert torch.equal(layer(x, res)[0], y) and torch.equal(layer(total), y)
 
 
+@pytest.mark.parametrize("interval", [1, 2])
+def test_norm_linear_delayed_scaling(interval):
+    """The same under delayed scaling, over steps that update the scales; the state
+    travels with the module."""
+    need_gpu()
+    rec = linear.DelayedScaling(interval=interval, amax_history_len=4)
+    torch.manual_seed(1)
+    layer = linear.RMSNormLinear(256, 128, recipe=rec, device="cuda")
+    length, margin, fwd, bwd = 4, 0, fm.E4M3, fm.E5M2
+    sx, sw, sg = (fm.DelayedState(f, length, margin) for f in (fwd, fwd, bwd))
+    w, nw = layer.weight.detach(), layer.norm_weight.detach()
+    for step in range(1, 6):
+        x = (step * torch.randn(64, 256, device="cuda")).bfloat16().requires_grad_()
+        res, dtotal = (torch.randn(64, 256, device="cuda").bfloat16() for _ in range(2))
+        dy = (1e-3 * torch.randn(64, 128, device="cuda")).bfloat16()
+        layer.weight.grad = layer.norm_weight.grad = None
+        y, total = layer(x, res)
+        torch.autograd.backward([y, total], [dy, dtotal])
+        q, t2, rstd = norm.rms_norm_quantize(x.detach(), fm.TENSOR_DELAYED, fwd, fm.ROW_AND_COL, nw, res, layer.eps, scale=sx.scale,
+                                             amax=sx.amax)
+        ix = sx.scale_inv.clone()
+        qw, qg = sw.quantize(w, fm.ROW_AND_COL), sg.quantize(dy, fm.ROW_AND_COL)
+        assert torch.equal(total, t2) and torch.equal(y, fm.gemm(q.q_row, fwd, ix, qw.q_row, fwd, qw.scale_inv, fm.GEMM_TENSOR, 256))
+        dn = fm.gemm(qg.q_row, bwd, qg.scale_inv, qw.q_col, fwd, qw.scale_inv, fm.GEMM_TENSOR, 128, M=64, N=256)
+        dw = fm.gemm(qg.q_col, bwd, qg.scale_inv, q.q_col, fwd, ix, fm.GEMM_TENSOR, 64, M=128, N=256)
+        dx, dnw = norm.rms_norm_backward(dn, t2, nw, rstd, dtotal)
+        assert torch.equal(x.grad, dx) and torch.equal(layer.weight.grad, dw) and torch.equal(layer.norm_weight.grad, dnw)
+        if step % interval == 0:
+            for s in (sx, sw, sg):
+                s.update()
+    assert sx.scale.item() != 1.0
+    other = linear.RMSNormLinear(256, 128, recipe=rec, device="cuda")
+    other.load_state_dict(layer.state_dict())
+    with torch.no_grad():
+        assert torch.equal(other(x, res)[0], layer(x, res)[0])
+
+
 def test_norm_linear_grad_of_total_alone_and_frozen_weight():
     need_gpu()
     layer = linear.RMSNormLinear(128, 64, recipe=linear.Float8BlockScaling(), device="cuda")
@@ -443,7 +510,10 @@ def test_refusals():
                 lambda: norm.RMSNorm(0), lambda: norm.RMSNorm(64)(x), lambda: norm.RMSNorm(32, device="cuda")(x),
                 lambda: norm.RMSNorm(64, device="cuda")(x, res.float()), lambda: norm.RMSNorm(64, device="cuda")(x, res[:4]),
                 lambda: linear.RMSNormLinear(40, 64), lambda: linear.RMSNormLinear(64, 64, device="cuda")(x),
-                lambda: linear.RMSNormLinear(64, 64, recipe=linear.DelayedScaling(), device="cuda")(x),
+                lambda: linear.RMSNormLinear(64, 64, recipe=linear.Float8CurrentScaling(), device="cuda")(x),
+                lambda: linear.RMSNormLinear(64, 64, recipe=linear.Float8ChannelScaling(), device="cuda")(x),
+                lambda: quant(x, block, fm.E4M3, scale=rstd), lambda: quant(x, fm.TENSOR_DELAYED, fm.E4M3, amax=rstd),
+                lambda: quant(x, fm.TENSOR_DELAYED, fm.E4M3, scale=rstd.double()),
                 lambda: layer(x), lambda: layer(x[:, :32]), lambda: layer(x, res[:4])):
         with pytest.raises(fm.Fp8Error):
             bad()

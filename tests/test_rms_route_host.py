@@ -34,15 +34,16 @@ def test_rms_forward(kw, code):
 def _quant(**kw):
     a = dict(x=P, x_dtype=fm.IN_BF16, rows=8, cols=64, ld_x=64, residual=P, ld_residual=64, weight=P, w_dtype=fm.IN_FP32, eps=1e-6,
              total=P, ld_total=64, rstd=P, recipe=fm.BLOCK_1x128, fmt=fm.E4M3, orient=fm.ROW_AND_COL, margin=0, q_row=P, ld_q_row=64,
-             s_row=P, q_col=P, ld_q_col=16, s_col=P, nonfinite=None, stream=0)
+             s_row=P, q_col=P, ld_q_col=16, s_col=P, scale=None, amax=None, nonfinite=None, stream=0)
     a.update(kw)
     return fm.fp8_rms_norm_quantize(**a)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x_dtype=2), fm.ERR_ENUM), (dict(recipe=9), fm.ERR_ENUM), (dict(fmt=2), fm.ERR_ENUM), (dict(orient=0), fm.ERR_ENUM),
-    (dict(recipe=fm.TENSOR_CURRENT), fm.ERR_UNSUPPORTED), (dict(recipe=fm.TENSOR_DELAYED), fm.ERR_UNSUPPORTED),
-    (dict(recipe=fm.BLOCK_128x128), fm.ERR_UNSUPPORTED), (dict(recipe=fm.CHANNEL), fm.ERR_UNSUPPORTED), (dict(margin=65), fm.ERR_SHAPE),
+    (dict(recipe=fm.TENSOR_CURRENT), fm.ERR_UNSUPPORTED), (dict(recipe=fm.TENSOR_DELAYED, amax=P), fm.ERR_NULL),
+    (dict(recipe=fm.TENSOR_DELAYED, scale=P), fm.ERR_NULL), (dict(recipe=fm.TENSOR_DELAYED, scale=P, amax=P + 2), fm.ERR_ALIGN),
+    (dict(recipe=fm.TENSOR_DELAYED, scale=P + 1, amax=P), fm.ERR_ALIGN), (dict(recipe=fm.BLOCK_128x128), fm.ERR_UNSUPPORTED), (dict(recipe=fm.CHANNEL), fm.ERR_UNSUPPORTED), (dict(margin=65), fm.ERR_SHAPE),
     (dict(margin=-1), fm.ERR_SHAPE), (dict(eps=-1.0), fm.ERR_SHAPE), (dict(rows=-1), fm.ERR_SHAPE), (dict(x=None), fm.ERR_NULL),
     (dict(total=None), fm.ERR_NULL), (dict(rstd=None), fm.ERR_NULL), (dict(q_row=None), fm.ERR_NULL), (dict(s_row=None), fm.ERR_NULL),
     (dict(q_col=None), fm.ERR_NULL), (dict(s_col=None), fm.ERR_NULL), (dict(ld_q_row=48), fm.ERR_SHAPE),
@@ -113,8 +114,8 @@ def test_balance(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=2), fm.ERR_ENUM), (dict(tokens=-1), fm.ERR_SHAPE), (dict(topk=0), fm.ERR_SHAPE), (dict(experts=1025), fm.ERR_UNSUPPORTED),
-    (dict(logits=None), fm.ERR_NULL), (dict(dlogits=None), fm.ERR_NULL), (dict(expert=None), fm.ERR_NULL), (dict(slope=None), fm.ERR_NULL),
+    (dict(dtype=2), fm.ERR_ENUM), (dict(tokens=-1), fm.ERR_SHAPE), (dict(topk=0), fm.ERR_SHAPE), (dict(topk=9), fm.ERR_SHAPE),
+    (dict(experts=1025), fm.ERR_UNSUPPORTED), (dict(logits=None), fm.ERR_NULL), (dict(dlogits=None), fm.ERR_NULL), (dict(expert=None), fm.ERR_NULL), (dict(slope=None), fm.ERR_NULL),
     (dict(ld_logits=7), fm.ERR_SHAPE), (dict(ld_dlogits=7), fm.ERR_SHAPE), (dict(dlogits=P + 2), fm.ERR_ALIGN), (dict(dloss=P + 2), fm.ERR_ALIGN),
     (dict(expert=P + 2), fm.ERR_ALIGN), (dict(dweights=P + 1), fm.ERR_ALIGN), (dict(slope=P + 1), fm.ERR_ALIGN), (dict(tokens=0, logits=None), fm.OK),
 ])
