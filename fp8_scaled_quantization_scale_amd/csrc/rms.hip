@@ -12,14 +12,23 @@
 // Bound by memory.  As in the layer norm a row is read once and held in
 // registers by the NT threads that own it (C chunks of 8 elements each),
 // workgroups are persistent, and the next row's words are on their way while
-// one row is reduced.  y is worked out in FP32 and rounded once: for codes too,
-// whose scales are those of the FP32 y.
+// one row is reduced.  y is worked out in FP32, t r first and then w, and rounded
+// once: for codes too, whose scales are those of the FP32 y.
 //
 // Codes with their blocks along the columns (ROW) leave from the same
 // registers: a 1x128 block is 16 neighbouring lanes' chunks, an MX block four
 // lanes'.  Codes with their blocks along the rows (COL) need 128 rows'
 // statistics before their first element, so a second launch reads t again, in
-// 128 x 128 tiles.
+// 128 x 128 tiles.  (Rows in parts of 16 to 128 MB, each with both launches, so
+// that t would still be in the Infinity Cache: 8192 x 16384 takes 411 to 289 us
+// against 280 in one part; the launches' ends cost more than the cache gives.)
+//
+// Measured (MI355X, BF16 with a residual): forward 8192 x 16384 187 us (5.7
+// TB/s); into 1x128 codes of both orientations 164 + 83 us (5.2 TB/s of the 1.29
+// GB that the two launches move), 8192 x 4096 39 + 19 us; backward 8192 x 4096 41
+// us (6.5 TB/s, a part of it from the Infinity Cache) and 4.8 of the weight's
+// sums, 4096 x 16384 104 us in all (5.2 TB/s).  Over 16384 columns the rows are
+// read again from the caches.
 #include "norm.hpp"
 #include "tile.hpp"
 

@@ -25,6 +25,12 @@
 // Sums over the tokens are taken in registers, then over the workgroup and, by a
 // second launch in a fixed order, over all workgroups; only integers are counted
 // with atomics.
+//
+// Measured (MI355X): forward 65536 x 256 BF16 to 8 22.6 + 5.4 us, bound by
+// instructions (605 per four tokens, 300 of them the choice; the logits' 34 MB
+// would take 7 us; choosing by marking what is taken, in the same lanes: 49 us);
+// 16384 x 64 FP32 to 4 5.7 + 4.4 us and 128 x 8 to 2 4.4 us (one launch), latency.
+// Gradient 65536 x 256 FP32 31 us (4.4 TB/s), 16384 x 64 5.2 us.
 #include "launch.hpp"
 #include "rows.hpp"
 #include "tile.hpp"
@@ -34,7 +40,9 @@ namespace fp8mi {
 namespace {
 
 constexpr int kRouteMaxBlocks = 256;
-constexpr int kRouteOneBlock = 4;  // tokens per group of lanes up to which there is one workgroup, and one launch
+// Tokens per group of lanes up to which there is one workgroup, and one launch
+// (128 x 8: 4.8 us; of 64 tokens each with the second launch 11.4).
+constexpr int kRouteOneBlock = 4;
 
 // lanes that own a token, and the experts of a lane: the power of two that they
 // hold them with
@@ -468,7 +476,9 @@ __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
 // The logits' gradient: the same lanes to a token.  What the weights add falls on
 // the topk chosen experts: each lane has a choice and adds it to a row in LDS
 // that is zero otherwise, and from which the lanes take their experts' parts.
-constexpr int kBackThreads = 256, kBackBlocks = 4;  // workgroups per compute unit
+// 4 workgroups per compute unit: what one sets up is used for more tokens (65536 x
+// 256 FP32: 44.5 us, 8 49.7, 32 71.6).
+constexpr int kBackThreads = 256, kBackBlocks = 4;
 
 template <typename T, int G, int V, bool EVEN>
 __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs a) {

@@ -489,6 +489,27 @@ def test_offsets_past_32_bits():
     _within(dw, s, (rows + 8) * E32 * a, "dweight")
 
 
+def test_more_columns_than_one_launch_adds():
+    """From 2^26 columns on the weight's sums go out as several launches."""
+    need_gpu()
+    rows, cols = 2, (1 << 26) + 43
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, dy = (torch.randn(rows, cols, generator=g, device="cuda", dtype=B) for _ in range(2))
+    w = (torch.rand(cols, generator=g, device="cuda") + 0.5).to(B)
+    y, _, rstd = norm.rms_norm_forward(x, w)
+    assert ((rstd.double() ** -2 - 1e-6) / torch.stack([r.double().square().mean() for r in x]) - 1).abs().max() <= 2 * _steps(cols)
+    dx, dw = norm.rms_norm_backward(dy, x, w, rstd)
+    r = rstd.double()[:, None]
+    mean = sum(((dy[:, i:i + (1 << 24)].double() * w[i:i + (1 << 24)].double()) * (x[:, i:i + (1 << 24)].double() * r)).sum(1, keepdim=True)
+               for i in range(0, cols, 1 << 24)) / cols
+    for at in (slice(0, 1000), slice((1 << 26) - 500, cols)):
+        n, d, wd = x[:, at].double() * r, dy[:, at].double(), w[at].double()
+        _within(y[:, at], n * wd, (n * wd).abs() * _steps(cols), "y")
+        _within(dw[at], (d * n).sum(0), (rows + 8) * E32 * (d * n).abs().sum(0), "dweight")
+        # the mean's own error is a part of its terms' mean size, 1 here, which dominates it
+        _within(dx[:, at], r * (d * wd - n * mean), (128 + cols / 8192) * E32 * r * ((d * wd).abs() + n.abs()), "dx")
+
+
 def test_refusals():
     need_gpu()
     x, res, w, dy, _ = _inputs(8, 64, 64, B, F)
