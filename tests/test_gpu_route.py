@@ -266,6 +266,27 @@ def test_autograd():
         assert torch.equal(l.grad, moe.route_backward(l.detach(), r.expert, one, None, None))
 
 
+@pytest.mark.parametrize("experts,topk", [(16, 4), (64, 20), (300, 4)])
+def test_gradients_of_choices_that_are_none(experts, topk):
+    """What stands in dweights beside a choice of -1 is not used."""
+    need_gpu()
+    l = _logits(50, experts, F, 3)
+    mask = torch.rand(50, generator=_gen(1), device="cuda") < 0.7
+    l[4, 2:] = -INF
+    for normalize in (True, False):
+        r = moe.route(l, topk, normalize, mask)
+        dw = torch.randn(50, topk, generator=_gen(2), device="cuda")
+        want = moe.route_backward(l, r.expert, torch.where(r.expert >= 0, dw, 0.0), r.slope, r.loss, normalize, mask)
+        for odd in (float("nan"), INF):
+            assert torch.equal(moe.route_backward(l, r.expert, torch.where(r.expert >= 0, dw, odd), r.slope, r.loss, normalize, mask), want)
+        assert want.isfinite().all()
+        # a choice dropped afterwards has no gradient by its weight, and none where it was a token's only one
+        e = r.expert.clone()
+        e[::2] = -1
+        d = moe.route_backward(l, e, dw, None, None, False, mask)
+        assert not d[::2].any()
+
+
 def test_gradient_against_differences():
     """In 64 bits, of the definition (the choices and counts held still)."""
     need_gpu()
