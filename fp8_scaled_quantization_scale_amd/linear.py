@@ -29,6 +29,9 @@ Recipes (the objects the guide's sec. 2.1-2.2 examples pass to
   transposed operand ("Mastering FP8 LLM training", Fig. 1 discussion of
   channel-wise scaling).  Name chosen here; the pages print none.
 
+``RMSNormLinear`` is the layer with an RMS norm before it, whose output goes
+straight into the codes of the first product.
+
 ``Format.HYBRID`` puts activations and weights in E4M3 and gradients in E5M2
 (guide sec. 2.1 hybrid format; "FP8 training support", "Why FP8?").  The
 backward treats the casts as identity: gradients flow through the quantizer

@@ -169,6 +169,31 @@ def test_nan_and_inf_logits(experts, topk):
     assert d[keep].isfinite().all() and d[4].isnan().all() and d[13].isnan().all()
 
 
+@pytest.mark.parametrize("experts,topk", [(8, 2), (64, 8), (256, 20), (1024, 4)])
+def test_a_token_does_not_depend_on_its_neighbours(experts, topk):
+    """Beside tokens of huge, equal, infinite and no logits, and alone."""
+    need_gpu()
+    for dt in (F, B):
+        l = _logits(24, experts, dt)
+        l[3], l[6], l[9, 0], l[12] = 1e30, -1e5, INF, -INF
+        l[15] *= 3e4
+        l[18] = 1.0 + 1e-7 * torch.arange(experts, device="cuda")
+        r = moe.route(l, topk)
+        dw = torch.randn(24, topk, generator=_gen(2), device="cuda")
+        d = moe.route_backward(l, r.expert, dw, r.slope.nan_to_num(), None)
+        for t in range(24):
+            if t == 9:
+                continue
+            one = moe.route(l[t:t + 1].clone(), topk)
+            assert torch.equal(one.expert[0], r.expert[t]) and torch.equal(one.weights[0], r.weights[t]), t
+            assert torch.equal(moe.route_backward(l[t:t + 1].clone(), one.expert, dw[t:t + 1], None, None)[0], d[t]), t
+        # far from 0 the weights are those of the differences
+        for t in (6, 15):
+            w = torch.softmax(l[t].double(), 0)[r.expert[t].long()]
+            w = w / w.sum()
+            assert ((r.weights[t].double() - w).abs() <= (4 * 150 + 160) * E32 * w + TINY).all()
+
+
 def test_no_tokens():
     need_gpu()
     l = torch.zeros(0, 8, device="cuda", requires_grad=True)
