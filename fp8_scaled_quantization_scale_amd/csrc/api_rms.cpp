@@ -119,7 +119,7 @@ int fp8_rms_norm_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols
 int64_t fp8_rms_norm_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1) return FP8MI_ERR_SHAPE;
   if (cols > (1LL << 28)) return FP8MI_ERR_UNSUPPORTED;
-  return fp8mi::rms_partials(rows) * cols * (int64_t)sizeof(float);
+  return fp8mi::rms_partials(rows, cols) * cols * (int64_t)sizeof(float);
 }
 
 int fp8_rms_norm_backward(const void* dy, int64_t ld_dy, const void* total, int x_dtype, int64_t rows, int64_t cols,

@@ -229,7 +229,7 @@ int64_t norm_partials(int64_t rows);
 hipError_t launch_rms_forward(const RmsParams& p, hipStream_t st);
 hipError_t launch_rms_quantize(const RmsParams& p, hipStream_t st);
 hipError_t launch_rms_backward(const RmsParams& p, hipStream_t st);
-int64_t rms_partials(int64_t rows);
+int64_t rms_partials(int64_t rows, int64_t cols);
 hipError_t launch_route(const RouteParams& p, hipStream_t st);
 hipError_t launch_route_backward(const RouteParams& p, hipStream_t st);
 int64_t route_blocks(int64_t tokens, int64_t experts);

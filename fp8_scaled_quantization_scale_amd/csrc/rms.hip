@@ -40,8 +40,11 @@ namespace {
 // read again, so they are no more than fill the GPU, and each takes 4 rows at
 // least, fewer where that leaves compute units without work (64 x 2560: 1 row 6.5
 // us, 2 7.8, 4 10.8; 256 x 4096: 8.8, 8.5, 10.2; 1000 x 4000 FP32: 16.7, 15.1,
-// 15.6).
-constexpr int kMaxPartials = 512;
+// 15.6).  Rows of up to 256 columns are so short that 512 workgroups wait for
+// their loads, and their sums so few that four times as many cost little: from 4096
+// rows on, 8 rows each (BF16, 512 or 2048 of them: 16384 x 200 18.7 or 15.9 us,
+// 65536 x 256 69 or 41; 16384 x 1000 has 36 or 33, 65536 x 1024 93 or 98).
+constexpr int64_t kMaxPartials = 512;
 constexpr int rows_per_partial(int64_t rows) { return rows <= 128 ? 1 : (rows <= 1024 ? 2 : 4); }
 
 struct RmsArgs {
@@ -66,6 +69,29 @@ struct RmsArgs {
   const float* scale;  // delayed: the tensor's, and a slot of |y|'s maximum per workgroup
   uint32_t* amax;
 };
+
+// Sum over the NT threads of a row, to all of them.  red: two sets of one word
+// per wave, used in turn, so that one barrier is enough (a set is written again
+// only after the barrier of the other).  Within a wave by rotations, whose latency
+// is a fraction of the shuffles' (128 x 512 forward 2.9 us by shuffles, 2.7 by
+// rotations; 8192 x 5120 backward 88.7, 84.5; 16384 x 200 19.7, 18.5).  SHUFFLE is
+// the backward pass over FP32 rows of up to 4096 columns, the one place where
+// shuffles measured faster (1000 x 4000 15.2 us, rotations 16.4; 8192 x 4096 78.9,
+// 81.1).
+template <int NT, bool SHUFFLE = false>
+__device__ __forceinline__ float sum_of_row(float v, float (&red)[2][16], int& turn) {
+  if constexpr (SHUFFLE) v = wave_sum(v);
+  else v = wave_total(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) v += red[turn][w];
+    turn ^= 1;
+  }
+  return v;
+}
 
 enum : int { OUT_VALUES = 0, OUT_BLOCK = 1, OUT_MX = 2, OUT_TENSOR = 3 };  // what a forward kernel leaves
 
@@ -139,7 +165,7 @@ __device__ __forceinline__ void put_amax(const RmsArgs& a, uint32_t most) {
 template <typename T, int NT, int C, int OUT, int FMT, bool PAST, bool AGAIN>
 __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) {
   constexpr int kRows = threads_of(NT) / NT;  // rows per workgroup at a time
-  __shared__ float red[2][1][16];
+  __shared__ float red[2][16];
   int turn = 0;
   const int tid = threadIdx.x % NT;
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -170,7 +196,7 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
   for (int c = 0; c < C; ++c) load_weight(w[c], a, col[c], n[c]);
   for (; row < a.rows; row += step) {
     fetch(nx, nr, row + step);
-    float v[C][8], s[1] = {0.0f};
+    float v[C][8], s = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       cx[c].get(v[c]);
@@ -184,10 +210,10 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
         cx[c].get(v[c]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[c][e] * v[c][e];  // zeros past the row's end
+      for (int e = 0; e < 8; ++e) s += v[c][e] * v[c][e];  // zeros past the row's end
     }
-    row_sum<NT>(s, red, turn);
-    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    s = sum_of_row<NT>(s, red, turn);
+    const float rstd = 1.0f / sqrtf(s * inv + a.eps);
     if (tid == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -213,7 +239,7 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
 template <typename T, int OUT, int FMT>
 __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
   constexpr int NT = 1024;
-  __shared__ float red[2][1][16];
+  __shared__ float red[2][16];
   int turn = 0;
   const float inv = 1.0f / (float)a.cols;
   const float scale = OUT == OUT_TENSOR ? *a.scale : 1.0f;
@@ -223,7 +249,7 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
     T* t = static_cast<T*>(a.total) + row * a.ld_total;
-    float s[1] = {0.0f};
+    float s = 0.0f;
     for (int col = threadIdx.x * 8; col < a.cols; col += NT * 8) {
       Chunk<T> k;
       float v[8];
@@ -240,10 +266,10 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
         k.get(v);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[e] * v[e];
+      for (int e = 0; e < 8; ++e) s += v[e] * v[e];
     }
-    row_sum<NT>(s, red, turn);
-    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    s = sum_of_row<NT>(s, red, turn);
+    const float rstd = 1.0f / sqrtf(s * inv + a.eps);
     if (threadIdx.x == 0) a.rstd[row] = rstd;
     if (OUT == OUT_VALUES && !a.out) continue;
     if (a.residual) x = t;  // (each thread reads what it wrote)
@@ -438,7 +464,7 @@ __global__ __launch_bounds__(kColThreads, sizeof(T) == 2 ? 6 : 4) void rms_colum
 template <typename T, int NT, int C, int AHEAD, bool PAST>
 __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a) {
   constexpr int kRows = threads_of(NT) / NT;
-  __shared__ float red[2][1][16];
+  __shared__ float red[2][16];
   int turn = 0;
   const int tid = threadIdx.x % NT;
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -475,7 +501,7 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a)
   }
   for (; row < a.rows; row += step) {
     fetch(AHEAD, row + AHEAD * step);
-    float s[1] = {0.0f};  // sum of g n (dy is zero past the row's end)
+    float s = 0.0f;  // sum of g n (dy is zero past the row's end)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float t[8], y[8];
@@ -484,12 +510,12 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float p = y[e] * (t[e] * rstd[0]);
-        s[0] += p * w[c][e];
+        s += p * w[c][e];
         dw[c][e] += p;
       }
     }
-    row_sum<NT>(s, red, turn);
-    const float m = s[0] * inv;
+    s = sum_of_row<NT, sizeof(T) == 4 && NT == 512 && C == 1>(s, red, turn);
+    const float m = s * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float t[8], y[8], o[8];
@@ -547,14 +573,14 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a)
 template <typename T>
 __global__ __launch_bounds__(1024) void rms_backward_long_kernel(RmsArgs a) {
   constexpr int NT = 1024;
-  __shared__ float red[2][1][16];
+  __shared__ float red[2][16];
   int turn = 0;
   const float inv = 1.0f / (float)a.cols;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* tr = static_cast<const T*>(a.x) + row * a.ld_x;
     const T* yr = static_cast<const T*>(a.dy) + row * a.ld_dy;
     const float rstd = a.rstd[row];
-    float s[1] = {0.0f};
+    float s = 0.0f;
     for (int pass = 0; pass < 2; ++pass) {
       for (int col = threadIdx.x * 8; col < a.cols; col += NT * 8) {
         Chunk<T> kt, ky;
@@ -566,10 +592,10 @@ __global__ __launch_bounds__(1024) void rms_backward_long_kernel(RmsArgs a) {
         ky.get(y);
         if (pass == 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] += y[e] * (t[e] * rstd) * w[e];
+          for (int e = 0; e < 8; ++e) s += y[e] * (t[e] * rstd) * w[e];
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = rstd * (y[e] * w[e] - t[e] * rstd * s[0]);
+          for (int e = 0; e < 8; ++e) o[e] = rstd * (y[e] * w[e] - t[e] * rstd * s);
           if (a.residual) {
             float d[8];
             kt.load(static_cast<const T*>(a.residual) + row * a.ld_residual + col, a.cols - col);
@@ -582,8 +608,8 @@ __global__ __launch_bounds__(1024) void rms_backward_long_kernel(RmsArgs a) {
         }
       }
       if (pass == 0) {
-        row_sum<NT>(s, red, turn);
-        s[0] *= inv;
+        s = sum_of_row<NT>(s, red, turn);
+        s *= inv;
       }
     }
   }
@@ -790,7 +816,7 @@ hipError_t backward(const RmsParams& p, hipStream_t st) {
   static std::atomic<int> occupancy{0};
   auto k = rms_backward_kernel<T, NT, C, AHEAD, PAST>;
   constexpr int threads = threads_of(NT);
-  int64_t blocks = rms_partials(p.rows);
+  int64_t blocks = rms_partials(p.rows, p.cols);
   const int64_t most = resident(k, threads, occupancy, st);
   blocks = blocks < most ? blocks : most;
   RmsArgs a = args_of(p);
@@ -822,7 +848,7 @@ hipError_t backward_any(const RmsParams& p, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.dweight) return e;
   a.partial = p.workspace;
-  const int64_t parts = rms_partials(p.rows);
+  const int64_t parts = rms_partials(p.rows, p.cols);
   rms_column_sums_kernel<T><<<dim3((unsigned)((p.cols + 511) / 512), (unsigned)parts), 64, 0, st>>>(a);
   e = hipGetLastError();
   return e != hipSuccess ? e : reduce_any(p, (int)parts, st);
@@ -831,9 +857,12 @@ hipError_t backward_any(const RmsParams& p, hipStream_t st) {
 }  // namespace
 
 // sets of column sums that a backward pass over `rows` rows may leave
-int64_t rms_partials(int64_t rows) {
+int64_t rms_partials(int64_t rows, int64_t cols) {
   const int64_t per = rows_per_partial(rows), n = (rows + per - 1) / per;
-  return n < 1 ? 1 : (n < kMaxPartials ? n : kMaxPartials);
+  if (n < 1) return 1;
+  if (n <= kMaxPartials) return n;
+  if (cols > 256 || rows <= 8 * kMaxPartials) return kMaxPartials;
+  return rows < 32 * kMaxPartials ? (rows + 7) / 8 : 4 * kMaxPartials;
 }
 
 hipError_t launch_rms_forward(const RmsParams& p, hipStream_t st) {

@@ -42,7 +42,7 @@ STUB(launch_rms_backward, RmsParams, g_rms)
 STUB(launch_route, RouteParams, g_route)
 STUB(launch_route_backward, RouteParams, g_route)
 // the most that these say
-int64_t rms_partials(int64_t) { return 512; }
+int64_t rms_partials(int64_t, int64_t cols) { return cols <= 1024 ? 2048 : 512; }
 int64_t route_workspace(int64_t, int64_t experts) { return 4 * (256 * (2 * experts + 1) + 33); }
 int hip_status(hipError_t e) { return e == hipSuccess ? FP8MI_OK : FP8MI_ERR_HIP; }
 }  // namespace fp8mi

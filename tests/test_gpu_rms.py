@@ -97,6 +97,24 @@ def test_backward(rows, cols, ld, dt, wdt):
         assert none is None and torch.equal(only, dx)
 
 
+@pytest.mark.parametrize("rows,cols,dt", [(4096, 64, B), (4097, 256, B), (9001, 200, F), (16383, 24, B), (20000, 255, F), (4097, 257, B), (1000, 4000, F)])
+def test_backward_of_many_short_rows(rows, cols, dt):
+    """The numbers of weight-gradient sums on both sides of each change, in a workspace of just the size that is asked for."""
+    need_gpu()
+    ld = (cols + 7) // 8 * 8
+    test_backward(rows, cols, ld, dt, F)
+    x, _, w, dy, dt_ = _inputs(rows, cols, ld, dt, F)
+    rstd = torch.rand(rows, device="cuda") + 0.5
+    dx, dw = norm.rms_norm_backward(dy, x, w, rstd, dt_)
+    size = fm.fp8_rms_norm_workspace(rows, cols)
+    ws = torch.full((size // 4 + 64,), 7.0, device="cuda")
+    got, gw = torch.empty_like(dx), torch.empty_like(dw)
+    code = fm.IN_BF16 if dt == B else fm.IN_FP32
+    assert fm.fp8_rms_norm_backward(dy, dy.stride(0), x, code, rows, cols, x.stride(0), w, fm.IN_FP32, rstd, dt_, dt_.stride(0),
+                                    got, got.stride(0), gw, ws, size) == fm.OK
+    assert torch.equal(got, dx) and torch.equal(gw, dw) and (ws[size // 4:] == 7).all()
+
+
 def _product(total, rstd, w):
     """The FP32 y in a matrix whose rows the cast takes (16-byte multiples)."""
     y = total.float() * rstd[:, None] * (1.0 if w is None else w.float())
