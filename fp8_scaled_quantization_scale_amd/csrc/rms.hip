@@ -40,12 +40,15 @@ namespace {
 // read again, so they are no more than fill the GPU, and each takes 4 rows at
 // least, fewer where that leaves compute units without work (64 x 2560: 1 row 6.5
 // us, 2 7.8, 4 10.8; 256 x 4096: 8.8, 8.5, 10.2; 1000 x 4000 FP32: 16.7, 15.1,
-// 15.6).  Rows of up to 256 columns are so short that 512 workgroups wait for
-// their loads, and their sums so few that four times as many cost little: from 4096
-// rows on, 8 rows each (BF16, 512 or 2048 of them: 16384 x 200 18.7 or 15.9 us,
-// 65536 x 256 69 or 41; 16384 x 1000 has 36 or 33, 65536 x 1024 93 or 98).
-constexpr int64_t kMaxPartials = 512;
-constexpr int rows_per_partial(int64_t rows) { return rows <= 128 ? 1 : (rows <= 1024 ? 2 : 4); }
+// 15.6).  Rows of up to 256 columns go 16 at a time through a workgroup, which
+// takes so many at least, and their sums are so few that twice as many sets cost
+// little (BF16, 512 or 1024 sets: 262144 x 64 41.7 or 29.6 us, 262144 x 128 44.1 or
+// 39.8, 65536 x 256 26.9 or 28.4; wider rows lose, 65536 x 1024 93 or 98).
+constexpr int64_t kMaxPartials = 512, kMaxShortPartials = 1024;
+constexpr int64_t kShort = 256, kShortRows = 16;
+constexpr int64_t rows_per_partial(int64_t rows, int64_t cols) {
+  return cols <= kShort ? kShortRows : (rows <= 128 ? 1 : (rows <= 1024 ? 2 : 4));
+}
 
 struct RmsArgs {
   const void* x;         // backward: t
@@ -74,13 +77,14 @@ struct RmsArgs {
 // per wave, used in turn, so that one barrier is enough (a set is written again
 // only after the barrier of the other).  Within a wave by rotations, whose latency
 // is a fraction of the shuffles' (128 x 512 forward 2.9 us by shuffles, 2.7 by
-// rotations; 8192 x 5120 backward 88.7, 84.5; 16384 x 200 19.7, 18.5).  SHUFFLE is
+// rotations; 8192 x 5120 backward 88.7, 84.5); four rows to a wave for NT = 16.  SHUFFLE is
 // the backward pass over FP32 rows of up to 4096 columns, the one place where
 // shuffles measured faster (1000 x 4000 15.2 us, rotations 16.4; 8192 x 4096 78.9,
 // 81.1).
 template <int NT, bool SHUFFLE = false>
 __device__ __forceinline__ float sum_of_row(float v, float (&red)[2][16], int& turn) {
-  if constexpr (SHUFFLE) v = wave_sum(v);
+  if constexpr (NT == 16) v = row16_total(v);
+  else if constexpr (SHUFFLE) v = wave_sum(v);
   else v = wave_total(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
@@ -733,8 +737,13 @@ hipError_t forward(const RmsArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Threads of a row, chunks of 8 columns of a thread.  Short rows by 16 lanes, four
+// of them in a wave: 262144 x 128 BF16 60.9 -> 22.5 us against a wave per row, into
+// codes 75 -> 22, backward 104 -> 40; 131072 x 256 33.9 -> 22.5, 41.6 -> 21.1, 63 -> 39.
 template <typename T, int OUT, int FMT, bool PAST, bool AGAIN>
 hipError_t forward_cols(const RmsArgs& a, hipStream_t st) {
+  if (a.cols <= 128) return forward<T, 16, 1, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= kShort) return forward<T, 16, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 512) return forward<T, 64, 1, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 1024) return forward<T, 64, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 2048) return forward<T, 256, 1, OUT, FMT, PAST, AGAIN>(a, st);
@@ -828,6 +837,8 @@ hipError_t backward(const RmsParams& p, hipStream_t st) {
 
 template <typename T, bool PAST>
 hipError_t backward_cols(const RmsParams& p, hipStream_t st) {
+  if (p.cols <= 128) return backward<T, 16, 1, 1, PAST>(p, st);
+  if (p.cols <= kShort) return backward<T, 16, 2, 1, PAST>(p, st);
   if (p.cols <= 512) return backward<T, 64, 1, 1, PAST>(p, st);
   if (p.cols <= 1024) return backward<T, 64, 2, 1, PAST>(p, st);
   if (p.cols <= 2048) return backward<T, 256, 1, 2, PAST>(p, st);
@@ -858,11 +869,9 @@ hipError_t backward_any(const RmsParams& p, hipStream_t st) {
 
 // sets of column sums that a backward pass over `rows` rows may leave
 int64_t rms_partials(int64_t rows, int64_t cols) {
-  const int64_t per = rows_per_partial(rows), n = (rows + per - 1) / per;
-  if (n < 1) return 1;
-  if (n <= kMaxPartials) return n;
-  if (cols > 256 || rows <= 8 * kMaxPartials) return kMaxPartials;
-  return rows < 32 * kMaxPartials ? (rows + 7) / 8 : 4 * kMaxPartials;
+  const int64_t per = rows_per_partial(rows, cols), n = (rows + per - 1) / per;
+  const int64_t most = cols <= kShort ? kMaxShortPartials : kMaxPartials;
+  return n < 1 ? 1 : (n < most ? n : most);
 }
 
 hipError_t launch_rms_forward(const RmsParams& p, hipStream_t st) {

@@ -104,16 +104,17 @@ __device__ __forceinline__ float row16_lane(float v) {
   return __builtin_bit_cast(float, dpp<0x150 + N>(__builtin_bit_cast(uint32_t, v)));
 }
 
-// sum over the 64 lanes of a wave, to all of them: rotations within the rows of
-// 16, whose sums are then scalars (a fifth of the latency of six shuffles)
+// sum over a row of 16 lanes, to all of them, by rotations
+__device__ __forceinline__ float row16_total(float v) {
+  v += __builtin_bit_cast(float, dpp<0x128>(__builtin_bit_cast(uint32_t, v)));
+  v += __builtin_bit_cast(float, dpp<0x124>(__builtin_bit_cast(uint32_t, v)));
+  v += __builtin_bit_cast(float, dpp<0x122>(__builtin_bit_cast(uint32_t, v)));
+  return v + __builtin_bit_cast(float, dpp<0x121>(__builtin_bit_cast(uint32_t, v)));
+}
+
+// sum over the 64 lanes of a wave, to all of them: the rows' sums as scalars
 __device__ __forceinline__ float wave_total(float v) {
-  auto turned = [](float x, auto ctrl) __attribute__((always_inline)) {
-    return __builtin_bit_cast(float, dpp<decltype(ctrl)::value>(__builtin_bit_cast(uint32_t, x)));
-  };
-  v += turned(v, std::integral_constant<int, 0x128>{});
-  v += turned(v, std::integral_constant<int, 0x124>{});
-  v += turned(v, std::integral_constant<int, 0x122>{});
-  v += turned(v, std::integral_constant<int, 0x121>{});
+  v = row16_total(v);
   auto row = [&](int lane) __attribute__((always_inline)) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
   };

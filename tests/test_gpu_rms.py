@@ -97,7 +97,8 @@ def test_backward(rows, cols, ld, dt, wdt):
         assert none is None and torch.equal(only, dx)
 
 
-@pytest.mark.parametrize("rows,cols,dt", [(4096, 64, B), (4097, 256, B), (9001, 200, F), (16383, 24, B), (20000, 255, F), (4097, 257, B), (1000, 4000, F)])
+@pytest.mark.parametrize("rows,cols,dt", [(4096, 64, B), (4097, 256, B), (9001, 200, F), (16383, 24, B), (20000, 255, F), (4097, 257, B), (1000, 4000, F),
+                                          (16, 128, B), (17, 129, F)])
 def test_backward_of_many_short_rows(rows, cols, dt):
     """The numbers of weight-gradient sums on both sides of each change, in a workspace of just the size that is asked for."""
     need_gpu()
@@ -183,6 +184,18 @@ def test_codes_of_delayed_scaling(rows, cols, ld, dt, wdt):
     want = fm.quantize(_product(bad, rstd, w), fm.TENSOR_DELAYED, fmt, fm.ROW_AND_COL, scale=scale)
     assert torch.equal(q.q_row[:, :cols], want.q_row[:, :cols]) and torch.equal(q.q_col[:, :rows], want.q_col[:, :rows])
     assert acc_amax(amax) != acc_amax(amax)
+
+
+@pytest.mark.parametrize("rows,cols,ld,dt,wdt", [(1, 128, 128, B, F), (17, 129, 136, F, B), (33, 255, 261, B, B), (31, 127, 129, F, F),
+                                                 (70001, 128, 128, B, B), (35000, 256, 256, F, F), (40003, 72, 80, B, F)])
+def test_rows_of_a_quarter_wave(rows, cols, ld, dt, wdt):
+    """Four rows to a wave: each path at the widths where the split changes, and with more rows than are held at once, so that
+    the last round leaves some of a wave's rows without work."""
+    test_forward(rows, cols, ld, dt, wdt)
+    test_backward(rows, cols, ld, dt, wdt)
+    for recipe in (fm.BLOCK_1x128, fm.MX_1x32, fm.MX_1x32_OCP):
+        test_codes(rows, cols, ld, dt, wdt, recipe)
+    test_codes_of_delayed_scaling(rows, cols, ld, dt, wdt)
 
 
 @pytest.mark.parametrize("fmt,u,least", [(fm.E4M3, 2.0 ** -4, 2.0 ** -10), (fm.E5M2, 2.0 ** -3, 2.0 ** -17)])
