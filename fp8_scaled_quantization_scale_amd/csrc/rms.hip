@@ -75,12 +75,12 @@ struct RmsArgs {
 
 // Sum over the NT threads of a row, to all of them.  red: two sets of one word
 // per wave, used in turn, so that one barrier is enough (a set is written again
-// only after the barrier of the other).  Within a wave by rotations, whose latency
-// is a fraction of the shuffles' (128 x 512 forward 2.9 us by shuffles, 2.7 by
-// rotations; 8192 x 5120 backward 88.7, 84.5); four rows to a wave for NT = 16.  SHUFFLE is
-// the backward pass over FP32 rows of up to 4096 columns, the one place where
-// shuffles measured faster (1000 x 4000 15.2 us, rotations 16.4; 8192 x 4096 78.9,
-// 81.1).
+// only after the barrier of the other).  Within a wave by rotations (four rows to
+// a wave for NT = 16), whose latency is a fraction of the shuffles' (128 x 512
+// forward 2.9 us by shuffles, 2.7 by rotations; 8192 x 5120 backward 88.7, 84.5).
+// SHUFFLE is the backward pass over FP32 rows of up to 4096 columns, the one place
+// where shuffles measured faster (1000 x 4000 15.2 us, rotations 16.4; 8192 x 4096
+// 78.9, 81.1).
 template <int NT, bool SHUFFLE = false>
 __device__ __forceinline__ float sum_of_row(float v, float (&red)[2][16], int& turn) {
   if constexpr (NT == 16) v = row16_total(v);
@@ -869,7 +869,7 @@ hipError_t backward_any(const RmsParams& p, hipStream_t st) {
 
 // sets of column sums that a backward pass over `rows` rows may leave
 int64_t rms_partials(int64_t rows, int64_t cols) {
-  const int64_t per = rows_per_partial(rows, cols), n = (rows + per - 1) / per;
+  const int64_t per = rows_per_partial(rows, cols), n = rows / per + (rows % per != 0);
   const int64_t most = cols <= kShort ? kMaxShortPartials : kMaxPartials;
   return n < 1 ? 1 : (n < most ? n : most);
 }
