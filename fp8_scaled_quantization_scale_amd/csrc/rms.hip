@@ -23,11 +23,11 @@
 // that t would still be in the Infinity Cache: 8192 x 16384 takes 411 to 289 us
 // against 280 in one part; the launches' ends cost more than the cache gives.)
 //
-// Measured (MI355X, BF16 with a residual): forward 8192 x 16384 187 us (5.7
-// TB/s); into 1x128 codes of both orientations 164 + 83 us (5.2 TB/s of the 1.29
-// GB that the two launches move), 8192 x 4096 39 + 19 us; backward 8192 x 4096 41
-// us (6.5 TB/s, a part of it from the Infinity Cache) and 4.8 of the weight's
-// sums, 4096 x 16384 104 us in all (5.2 TB/s).  Over 16384 columns the rows are
+// Measured (MI355X, BF16 with a residual): forward 8192 x 16384 182 us (5.9
+// TB/s); into 1x128 codes of both orientations 154 + 79 us (5.5 TB/s of the 1.29
+// GB that the two launches move), 8192 x 4096 42 + 20 us; backward 8192 x 4096 46
+// us (5.8 TB/s, a part of it from the Infinity Cache) and 4.7 of the weight's
+// sums, 4096 x 16384 103 us in all (5.2 TB/s).  Over 16384 columns the rows are
 // read again from the caches.
 #include "norm.hpp"
 #include "tile.hpp"
