@@ -348,6 +348,7 @@ class _RmsNormLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x2d, residual, norm_weight, weight, eps, p: Plan, states, interval, need_dx, need_dw):
         ctx.set_materialize_grads(False)
+        ctx.apart = _norm._apart(x2d, residual)
         M, K = x2d.shape
         N = weight.shape[0]
         rx, rw = p.quant["x"][0], p.quant["w"][0]
@@ -385,7 +386,8 @@ class _RmsNormLinearFn(torch.autograd.Function):
         dx = dnw = None
         if need_dx:
             dx, dnw = _norm._rms_norm_grads(dn, total, norm_weight, rstd, dtotal, need[0] or need[1], need[2])
-        return dx if need[0] else None, dx if need[1] else None, dnw, dw, None, None, None, None, None, None
+        dx, dres = _norm._to_both(dx, need[0], need[1], ctx.apart)
+        return dx, dres, dnw, dw, None, None, None, None, None, None
 
 
 class RMSNormLinear(Linear):

@@ -277,18 +277,40 @@ def _grad_of(d, like: torch.Tensor):
 
 
 def _rms_norm_grads(dy, total, weight, rstd, dtotal, need_dx: bool, need_dw: bool):
-    """dx and dweight where y or total may have no gradient."""
+    """dx and dweight where y or total may have no gradient.  dx is always a tensor of its own."""
     if dy is None:
         dw = torch.zeros_like(weight) if need_dw and weight is not None else None
-        return dtotal if need_dx else None, dw
+        return dtotal.clone() if need_dx and dtotal is not None else None, dw
     dx, dw = rms_norm_backward(_grad_of(dy, total), total, weight, rstd, _grad_of(dtotal, total), need_dw)
     return dx if need_dx else None, dw
+
+
+def _read_only(t: torch.Tensor) -> bool:
+    """t's gradient goes, through views at most, to a backward pass of this
+    package: these read it and hand on tensors of their own."""
+    if t.grad_fn is None:
+        return False
+    made_by = getattr(type((t._base if t._is_view() else t).grad_fn), "_forward_cls", None)
+    return made_by is not None and made_by.__module__.partition(".")[0] == __name__.partition(".")[0]
+
+
+def _apart(x: torch.Tensor, residual: torch.Tensor | None) -> bool:
+    """The two need gradients in memory of their own.  Autograd takes a gradient
+    over as a leaf's .grad, which later passes and users write to, where it sees no
+    other holder of the tensor; behind a view it does not see that of the other's."""
+    return residual is not None and x.requires_grad and residual.requires_grad and not (_read_only(x) or _read_only(residual))
+
+
+def _to_both(dx, need_x: bool, need_residual: bool, apart: bool):
+    """dx as the gradient of x and of the residual."""
+    return dx if need_x else None, (dx.clone() if apart and dx is not None else dx) if need_residual else None
 
 
 class _RMSNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
+        ctx.apart = _apart(x, residual)
         y, total, rstd = rms_norm_forward(x, weight, residual, eps)
         ctx.save_for_backward(total, weight, rstd)
         return y if residual is None else (y, total)
@@ -299,7 +321,8 @@ class _RMSNormFn(torch.autograd.Function):
         total, weight, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx, dw = _rms_norm_grads(dy, total, weight, rstd, dtotal, need[0] or need[2], need[1])
-        return dx if need[0] else None, dw, dx if need[2] else None, None
+        dx, dres = _to_both(dx, need[0], need[2], ctx.apart)
+        return dx, dw, dres, None
 
 
 class RMSNorm(torch.nn.Module):
