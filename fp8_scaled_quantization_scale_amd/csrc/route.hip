@@ -132,7 +132,10 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 // e^d with d = v - most, at most 0: d log2(e) = n + r with n whole, at least -126,
 // and 2^r 2^n.  r is rounded as the small number that it is (log2(e) in two parts,
 // the second as an fma), so that the result is off by 2.4 half steps, and what v -
-// most loses, at any distance.  Below 2^-126 r takes the rest, and the product is
+// most loses, at any distance (2^(d log2(e)) with the product rounded to FP32 takes a
+// third of the instructions and 65536 x 256 from 28.5 to 26 us, but is off by 32 half
+// steps at 20 to 40 below the largest, which a weight, a gradient and the loss of
+// choices that lie there show).  Below 2^-126 r takes the rest, and the product is
 // denormal; -inf is 0.
 __device__ __forceinline__ float weight_of(float v, float most) {
   constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kWhole = 0x1.8p+23f;
@@ -141,16 +144,6 @@ __device__ __forceinline__ float weight_of(float v, float most) {
   const float n = t - kWhole;
   const float r = __builtin_fmaf(d, kRest, __builtin_fmaf(d, kLog2e, -n));
   return __builtin_amdgcn_exp2f(r) * as_float((as_bits(t) << 23) + 0x3F800000u);
-}
-
-// The same in a third of the instructions, off by 1.3 |d| + 2 half steps, for the
-// sums of a token that makes its own choices: over the experts, and of the loss,
-// where its largest is among the chosen.  What is far from that weighs little: the
-// mean of |d| over a softmax of E experts is at most W(E / e), 4.4 for 1024, so such
-// a sum is off by 6 half steps more at the worst (a weight would be by 32 at 20 to 40
-// below the largest).  With weight_of for these too 65536 x 256 takes 28.5 us, not 26.
-__device__ __forceinline__ float term_of(float v, float most) {
-  return __builtin_amdgcn_exp2f((v - most) * 1.44269504088896340736f);
 }
 
 // A lane's experts: vectors of kWide, G lanes of them and then the next.  expert()
@@ -204,10 +197,9 @@ __device__ __forceinline__ float logit_at(const T* row, int e) {
   else return row[e];
 }
 
-// v becomes e^(v - most) with a token's largest logit, most; s: their sum (SUMS:
-// that is what they are for).  False, and zeros, for a token of nothing but -inf
-// (one with a NaN, too, has NaNs).
-template <int G, int V, bool SUMS>
+// v becomes e^(v - most) with a token's largest logit, most; s: their sum.  False,
+// and zeros, for a token of nothing but -inf (one with a NaN, too, has NaNs).
+template <int G, int V>
 __device__ __forceinline__ bool exponentials(float (&v)[V], float& most, float& s) {
   most = v[0];
 #pragma unroll
@@ -217,7 +209,7 @@ __device__ __forceinline__ bool exponentials(float (&v)[V], float& most, float& 
   s = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    v[i] = SUMS ? term_of(v[i], by) : weight_of(v[i], by);
+    v[i] = weight_of(v[i], by);
     s += v[i];
   }
   s = lanes_sum<G>(s);
@@ -301,7 +293,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         pk[i] = ((k & ~kLow) | from_top) ^ (uint32_t)O::expert(i);  // (the expert's number from the top)
       }
     }
-    const bool live = exponentials<G, V, !CHOSEN>(e, most, s);  // (choices given may all lie far below the largest)
+    const bool live = exponentials<G, V>(e, most, s);
     const float inv = live ? 1.0f / s : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) ps[i] += e[i] * inv;
@@ -537,7 +529,7 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
     }
     float v[V], most, s, dot = 0.0f;
     raw.get(v, real ? n : 0);
-    const bool live = exponentials<G, V, false>(v, most, s);
+    const bool live = exponentials<G, V>(v, most, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) dot += v[i] * slope[i];
     dot = lanes_sum<G>(dot);
