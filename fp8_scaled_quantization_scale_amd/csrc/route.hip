@@ -559,12 +559,25 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
       along *= unit;
       if (!a.normalize) dot += along;
       const float less = a.normalize ? along : 0.0f;
-      if (mine >= 0) atomicAdd(add + mine, w * unit * (dw - less));
+      float rest = 0.0f;
+      if (a.normalize) {
+        // <w, dw - less> is what less is off by, which is all there is of dw - less
+        // where one expert has nearly all the weight: it is taken out, too
+        if (mine >= 0) rest = w * unit * (dw - less);
+        if (a.topk > G && real)
+          for (int j = li + G; j < a.topk; j += G) {
+            const int e = a.expert[slot + j];
+            if ((unsigned)e < (unsigned)a.experts)
+              rest += weight_of(logit_at(row, e), most) * unit * (a.dweights[slot + j] - less);
+          }
+        rest = lanes_sum<G>(rest);
+      }
+      if (mine >= 0) atomicAdd(add + mine, w * unit * (dw - less - rest));
       if (a.topk > G && real)
         for (int j = li + G; j < a.topk; j += G) {
           const int e = a.expert[slot + j];
           if ((unsigned)e < (unsigned)a.experts)
-            atomicAdd(add + e, weight_of(logit_at(row, e), most) * unit * (a.dweights[slot + j] - less));
+            atomicAdd(add + e, weight_of(logit_at(row, e), most) * unit * (a.dweights[slot + j] - less - rest));
         }
       // (the group's lanes are in one wave, whose LDS operations stay in order)
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

@@ -91,3 +91,29 @@ def test_loss_of_choices_far_below(dt):
         loss, _, _ = moe.balance(l, expert)
         want = 2.0 * torch.softmax(l.double(), 1)[0, 1].item()
         assert abs(loss.item() - want) <= (2 * EXP + _adds(2) + 2 + 4) * E32 * want, d
+
+
+@pytest.mark.parametrize("far", [4, 12, 30])
+@pytest.mark.parametrize("experts,topk", [(2, 2), (8, 2), (8, 8), (64, 8), (64, 40), (256, 16), (300, 8), (300, 100)])
+def test_normalized_weights_where_one_expert_has_nearly_all(experts, topk, far):
+    """dl = w (dw - c), c = <w, dw>, where dw - c is small for the expert whose weight
+    is near 1.  A weight is off by W = 2 EXP + ADDS + 2 steps, the mean of dw - c that
+    is taken out at the end by 2 W + ADDS + 6 of the mean of |dw - c|; what c itself is
+    off by enters by its rounding alone, a step of a step of |dw|."""
+    need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(experts + far)
+    l = -far - torch.randint(0, 10 * 64, (400, experts), generator=g, device="cuda").double() / 64
+    l[torch.arange(400, device="cuda"), torch.randint(0, experts, (400,), generator=g, device="cuda")] = 0.0
+    l = l.float()
+    r = moe.route(l, topk, True)
+    dw = torch.randn(400, topk, generator=g, device="cuda")
+    got = moe.route_backward(l, r.expert, dw, r.slope, None, normalize=True)
+    at = r.expert.long()
+    w = torch.softmax(l.double().gather(1, at), 1)
+    off = dw.double() - (w * dw.double()).sum(1, keepdim=True)
+    off = off - (w * off).sum(1, keepdim=True)  # (64 bits have the same trouble)
+    adds = _adds(experts) + -(-topk // 16)
+    c = 2 * (2 * EXP + adds + 2) + adds + 6
+    tol = w * (c * E32 * (off.abs() + (w * off.abs()).sum(1, keepdim=True)) + (c * E32) ** 2 * dw.abs().amax(1, keepdim=True)) + 2 * DENORMAL
+    bad = (got.double().gather(1, at) - w * off).abs() > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}"
