@@ -56,6 +56,7 @@ struct RmsArgs {
   const void* dy;
   int64_t rows, ld_x, ld_residual, ld_dy, ld_total, ld_out;
   int cols;
+  double inv;  // 1 / cols
   const void* weight;
   int w_bf16;
   float eps;
@@ -73,7 +74,16 @@ struct RmsArgs {
   uint32_t* amax;
 };
 
-// Sum over the NT threads of a row, to all of them.  red: two sets of one word
+// sum of N numbers, a power of two, in pairs
+template <int N, typename S>
+__device__ __forceinline__ S paired_sum(const float* v) {
+  if constexpr (N == 1) return v[0];
+  else return paired_sum<N / 2, S>(v) + paired_sum<N / 2, S>(v + N / 2);
+}
+
+// Sum over the NT threads of a row, to all of them, the waves' sums in 64 bits (one
+// after the other in FP32 they cost rstd a fifth of its error at 16384 columns; no
+// time in either form).  red: two sets of one word
 // per wave, used in turn, so that one barrier is enough (a set is written again
 // only after the barrier of the other).  Within a wave by rotations (four rows to
 // a wave for NT = 16), whose latency is a fraction of the shuffles' (128 x 512
@@ -82,20 +92,31 @@ struct RmsArgs {
 // where shuffles measured faster (1000 x 4000 15.2 us, rotations 16.4; 8192 x 4096
 // 78.9, 81.1).
 template <int NT, bool SHUFFLE = false>
-__device__ __forceinline__ float sum_of_row(float v, float (&red)[2][16], int& turn) {
+__device__ __forceinline__ double sum_of_row(float v, float (&red)[2][16], int& turn) {
   if constexpr (NT == 16) v = row16_total(v);
   else if constexpr (SHUFFLE) v = wave_sum(v);
   else v = wave_total(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) v += red[turn][w];
     turn ^= 1;
+    return paired_sum<NT / 64, double>(red[turn ^ 1]);
   }
   return v;
 }
+
+// v / cols, rounded once
+__device__ __forceinline__ float mean_of(double v, double inv) { return (float)(v * inv); }
+
+// Sums of squares: eight partial sums, so that few roundings follow one another
+struct Squares {
+  float s[8] = {};
+  __device__ __forceinline__ void add(const float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += v[e] * v[e];
+  }
+  __device__ __forceinline__ float total() const { return paired_sum<8, float>(s); }
+};
 
 enum : int { OUT_VALUES = 0, OUT_BLOCK = 1, OUT_MX = 2, OUT_TENSOR = 3 };  // what a forward kernel leaves
 
@@ -174,7 +195,6 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
   const int tid = threadIdx.x % NT;
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
-  const float inv = 1.0f / (float)a.cols;
 
   int col[C], n[C];
   float w[C][8];
@@ -200,7 +220,8 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
   for (int c = 0; c < C; ++c) load_weight(w[c], a, col[c], n[c]);
   for (; row < a.rows; row += step) {
     fetch(nx, nr, row + step);
-    float v[C][8], s = 0.0f;
+    float v[C][8];
+    Squares squares;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       cx[c].get(v[c]);
@@ -213,11 +234,10 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) 
         cx[c].template store<PAST && !AGAIN>(static_cast<T*>(a.total) + row * a.ld_total + col[c], n[c]);
         cx[c].get(v[c]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[c][e] * v[c][e];  // zeros past the row's end
+      squares.add(v[c]);  // zeros past the row's end
     }
-    s = sum_of_row<NT>(s, red, turn);
-    const float rstd = 1.0f / sqrtf(s * inv + a.eps);
+    const double s = sum_of_row<NT>(squares.total(), red, turn);
+    const float rstd = 1.0f / sqrtf(mean_of(s, a.inv) + a.eps);
     if (tid == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -245,7 +265,6 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
   constexpr int NT = 1024;
   __shared__ float red[2][16];
   int turn = 0;
-  const float inv = 1.0f / (float)a.cols;
   const float scale = OUT == OUT_TENSOR ? *a.scale : 1.0f;
   uint32_t most = 0;
   // (whole turns of the workgroup: the lanes of a block go together)
@@ -253,7 +272,7 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
     T* t = static_cast<T*>(a.total) + row * a.ld_total;
-    float s = 0.0f;
+    Squares squares;
     for (int col = threadIdx.x * 8; col < a.cols; col += NT * 8) {
       Chunk<T> k;
       float v[8];
@@ -269,11 +288,10 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
         k.store(t + col, a.cols - col);
         k.get(v);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[e] * v[e];
+      squares.add(v);
     }
-    s = sum_of_row<NT>(s, red, turn);
-    const float rstd = 1.0f / sqrtf(s * inv + a.eps);
+    const double s = sum_of_row<NT>(squares.total(), red, turn);
+    const float rstd = 1.0f / sqrtf(mean_of(s, a.inv) + a.eps);
     if (threadIdx.x == 0) a.rstd[row] = rstd;
     if (OUT == OUT_VALUES && !a.out) continue;
     if (a.residual) x = t;  // (each thread reads what it wrote)
@@ -473,7 +491,6 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a)
   const int tid = threadIdx.x % NT;
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
-  const float inv = 1.0f / (float)a.cols;
 
   int col[C], n[C];
   float w[C][8], dw[C][8];
@@ -518,8 +535,7 @@ __global__ __launch_bounds__(threads_of(NT)) void rms_backward_kernel(RmsArgs a)
         dw[c][e] += p;
       }
     }
-    s = sum_of_row<NT, sizeof(T) == 4 && NT == 512 && C == 1>(s, red, turn);
-    const float m = s * inv;
+    const float m = mean_of(sum_of_row<NT, sizeof(T) == 4 && NT == 512 && C == 1>(s, red, turn), a.inv);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float t[8], y[8], o[8];
@@ -579,7 +595,6 @@ __global__ __launch_bounds__(1024) void rms_backward_long_kernel(RmsArgs a) {
   constexpr int NT = 1024;
   __shared__ float red[2][16];
   int turn = 0;
-  const float inv = 1.0f / (float)a.cols;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* tr = static_cast<const T*>(a.x) + row * a.ld_x;
     const T* yr = static_cast<const T*>(a.dy) + row * a.ld_dy;
@@ -611,10 +626,7 @@ __global__ __launch_bounds__(1024) void rms_backward_long_kernel(RmsArgs a) {
           kt.store(static_cast<T*>(a.out) + row * a.ld_out + col, a.cols - col);
         }
       }
-      if (pass == 0) {
-        s = sum_of_row<NT>(s, red, turn);
-        s *= inv;
-      }
+      if (pass == 0) s = mean_of(sum_of_row<NT>(s, red, turn), a.inv);
     }
   }
 }
@@ -652,7 +664,7 @@ __global__ __launch_bounds__(1024) void rms_reduce_kernel(const float* partial, 
   __shared__ float sums[kReduceGroups][kReduceCols + 4];
   const int at = (threadIdx.x & 7) * 4, group = threadIdx.x >> 3;
   const int64_t i = (first + blockIdx.x) * kReduceCols + at, width = cols;
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float s[8] = {};
   if (i + 4 <= width) {
     for (int p = group; p < parts; p += kReduceGroups) {
       const f32x4a4 v = *reinterpret_cast<const f32x4a4*>(partial + p * width + i);
@@ -703,6 +715,7 @@ RmsArgs args_of(const RmsParams& p) {
   RmsArgs a{};
   a.rows = p.rows;
   a.cols = (int)p.cols;
+  a.inv = 1.0 / (double)p.cols;
   a.weight = p.weight;
   a.w_bf16 = p.w_dtype == kInBf16;
   a.eps = p.eps;
