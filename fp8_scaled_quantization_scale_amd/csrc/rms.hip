@@ -37,17 +37,18 @@ namespace fp8mi {
 namespace {
 
 // Workgroups that leave column sums: each set is 4 bytes per column, written and
-// read again, so they are no more than fill the GPU, and each takes 4 rows at
-// least, fewer where that leaves compute units without work (64 x 2560: 1 row 6.5
-// us, 2 7.8, 4 10.8; 256 x 4096: 8.8, 8.5, 10.2; 1000 x 4000 FP32: 16.7, 15.1,
-// 15.6).  Rows of up to 256 columns go 16 at a time through a workgroup, which
-// takes so many at least, and their sums are so few that twice as many sets cost
-// little (BF16, 512 or 1024 sets: 262144 x 64 41.7 or 29.6 us, 262144 x 128 44.1 or
-// 39.8, 65536 x 256 26.9 or 28.4; wider rows lose, 65536 x 1024 93 or 98).
+// read again, so they are no more than fill the GPU, and each has as many rows at
+// least as it takes at a time: 16 of up to 256 columns, 4 of up to 1024, else one.
+// There it takes 4 too, fewer where that leaves compute units without work (64 x
+// 2560: 1 row 6.5 us, 2 7.8, 4 10.8; 256 x 4096: 8.8, 8.5, 10.2).  The sums of the
+// short rows are so few that twice as many sets cost little (BF16, 512 or 1024 sets:
+// 262144 x 64 41.7 or 29.6 us, 262144 x 128 44.1 or 39.8, 65536 x 256 26.9 or 28.4;
+// wider rows lose, 65536 x 1024 93 or 98).
 constexpr int64_t kMaxPartials = 512, kMaxShortPartials = 1024;
-constexpr int64_t kShort = 256, kShortRows = 16;
+constexpr int64_t kShort = 256, kMiddle = 1024;  // columns
 constexpr int64_t rows_per_partial(int64_t rows, int64_t cols) {
-  return cols <= kShort ? kShortRows : (rows <= 128 ? 1 : (rows <= 1024 ? 2 : 4));
+  if (cols <= kShort) return 16;
+  return cols <= kMiddle || rows > 1024 ? 4 : (rows <= 128 ? 1 : 2);
 }
 
 struct RmsArgs {
@@ -758,7 +759,7 @@ hipError_t forward_cols(const RmsArgs& a, hipStream_t st) {
   if (a.cols <= 128) return forward<T, 16, 1, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= kShort) return forward<T, 16, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 512) return forward<T, 64, 1, OUT, FMT, PAST, AGAIN>(a, st);
-  if (a.cols <= 1024) return forward<T, 64, 2, OUT, FMT, PAST, AGAIN>(a, st);
+  if (a.cols <= kMiddle) return forward<T, 64, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 2048) return forward<T, 256, 1, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 4096) return forward<T, 256, 2, OUT, FMT, PAST, AGAIN>(a, st);
   if (a.cols <= 8192) return forward<T, 512, 2, OUT, FMT, PAST, AGAIN>(a, st);
@@ -853,7 +854,7 @@ hipError_t backward_cols(const RmsParams& p, hipStream_t st) {
   if (p.cols <= 128) return backward<T, 16, 1, 1, PAST>(p, st);
   if (p.cols <= kShort) return backward<T, 16, 2, 1, PAST>(p, st);
   if (p.cols <= 512) return backward<T, 64, 1, 1, PAST>(p, st);
-  if (p.cols <= 1024) return backward<T, 64, 2, 1, PAST>(p, st);
+  if (p.cols <= kMiddle) return backward<T, 64, 2, 1, PAST>(p, st);
   if (p.cols <= 2048) return backward<T, 256, 1, 2, PAST>(p, st);
   // (a row of 4096 FP32: 8192 rows 83 us by 256 threads of two chunks, 80 by 512 of
   // one; BF16 50.7 and 54.7)
