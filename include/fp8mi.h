@@ -318,7 +318,8 @@ int fp8_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int x_
  *   rstd = 1 / sqrt(sum(t^2) / cols + eps), y = t * rstd * weight.
  *   total : where t goes, the residual stream's new value and what the backward
  *           pass takes; not used without a residual.
- *   weight: [cols] of w_dtype, NULL for 1; rstd: float [rows]; eps >= 0.
+ *   weight: [cols] of w_dtype, NULL for 1; rstd: float [rows]; eps >= 0 (with 0 a
+ *   row of zeros has rstd = inf and NaN for y).
  *   The squares are summed in FP32: sum(t^2) has to stay below 2^128. */
 int fp8_rms_norm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
                          const void* residual, int64_t ld_residual, const void* weight, int w_dtype, float eps,
