@@ -13,7 +13,6 @@ using fp8mi::aligned_to;
 using fp8mi::check_matrix;
 using fp8mi::in_dtype_ok;
 using fp8mi::in_size;
-using fp8mi::span_ok;
 
 int check_routing(int dtype, int64_t tokens, int64_t experts, int64_t topk) {
   if (!in_dtype_ok(dtype)) return FP8MI_ERR_ENUM;

@@ -51,6 +51,37 @@ struct NormArgs {
   float* partial;  // [gridDim.x][2][cols]
 };
 
+// Sums over the NT threads of a row; every thread gets them.  red: two sets of
+// one word per wave, used in turn, so one barrier per sum is enough (a set is
+// written again only after the barrier of the other).
+template <int NT, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (&red)[2][N][16], int& turn) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (NT > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[turn][i][wave] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NT / 64; ++w) s += red[turn][i][w];
+      v[i] = s;
+    }
+    turn ^= 1;
+  }
+}
+
+template <typename W>
+__device__ __forceinline__ void load_param(Chunk<W>& c, const void* p, float otherwise, int col, int n) {
+  if (p) c.load(static_cast<const W*>(p) + col, n);
+  else c.fill(otherwise);
+}
+
 template <typename T, typename W, int NT, int C>
 __global__ __launch_bounds__(threads_of(NT)) void norm_forward_kernel(NormArgs a) {
   constexpr int kRows = threads_of(NT) / NT;  // rows per workgroup at a time

@@ -174,7 +174,6 @@ __device__ __forceinline__ void put_codes(const RmsArgs& a, int64_t row, int col
   if (n > 0) store8(a.q + row * a.ld_q + col, n, safe ? encode8<FMT, true>(y, s) : encode8<FMT, false>(y, s));
 }
 
-// AGAIN: t is read again by the launch that follows
 // OUT_TENSOR: the workgroup's largest |y| into its slot (one workgroup's alone:
 // the grid is no more than there are slots), beside what is there.
 __device__ __forceinline__ void put_amax(const RmsArgs& a, uint32_t most) {
@@ -188,6 +187,9 @@ __device__ __forceinline__ void put_amax(const RmsArgs& a, uint32_t most) {
   }
 }
 
+// PAST: read and written past the caches.  AGAIN: t is read again by the launch that
+// follows (COL codes), so it is written as usual; OUT_VALUES then leaves t and rstd
+// alone, for COL codes without ROW ones.
 template <typename T, int NT, int C, int OUT, int FMT, bool PAST, bool AGAIN>
 __global__ __launch_bounds__(threads_of(NT)) void rms_forward_kernel(RmsArgs a) {
   constexpr int kRows = threads_of(NT) / NT;  // rows per workgroup at a time

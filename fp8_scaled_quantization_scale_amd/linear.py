@@ -401,7 +401,7 @@ class RMSNormLinear(Linear):
 
     def __init__(self, in_features: int, out_features: int, eps: float = 1e-6, recipe=None, device=None,
                  dtype=torch.bfloat16):
-        if in_features < 16:
+        if in_features < 1:
             raise Fp8Error("in_features must be positive")
         super().__init__(in_features, out_features, recipe=recipe, device=device, dtype=dtype)
         self.eps = eps
