@@ -49,7 +49,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (BLOCK_1x128, BLOCK_128x128, CHANNEL, COL, E4M3, E5M2, GEMM_BLOCK_1x128_1x128,
                GEMM_BLOCK_1x128_128x128, GEMM_CHANNEL, GEMM_MX_1x32, GEMM_TENSOR, MX_1x32, ROW,
-               TENSOR_CURRENT, TENSOR_DELAYED, DelayedState, Fp8Error, _dense, gemm, load, quantize)
+               TENSOR_CURRENT, TENSOR_DELAYED, DelayedState, Fp8Error, _dense, _one_device, _scope, gemm, load, quantize)
 from . import norm as _norm
 
 
@@ -305,6 +305,7 @@ class Linear(torch.nn.Module):
             raise Fp8Error(f"input has {x.shape[-1]} features, the layer {self.in_features}")
         if x.dtype not in (torch.bfloat16, torch.float32) or self.weight.dtype not in (torch.bfloat16, torch.float32):
             raise Fp8Error("inputs and weights are BF16 or FP32")
+        _one_device(x, self.weight)
         load()
         lead = x.shape[:-1]
         x2d = _dense(x.reshape(-1, self.in_features))
@@ -314,7 +315,8 @@ class Linear(torch.nn.Module):
             raise Fp8Error("the token count must be a multiple of 16 when the weight needs a gradient")
         states = self._delayed_states(r, p, x.device) if isinstance(r, DelayedScaling) else None
         interval = r.interval if isinstance(r, DelayedScaling) else 1
-        y = _Fp8LinearFn.apply(x2d, self.weight.contiguous(), p, states, interval, need_dx, need_dw)
+        with _scope(x.device, None):  # (the casts and products go to the current device's stream)
+            y = _Fp8LinearFn.apply(x2d, self.weight.contiguous(), p, states, interval, need_dx, need_dw)
         return y.reshape(*lead, self.out_features)
 
     # delayed-scaling state travels with the module's state_dict
@@ -417,6 +419,7 @@ class RMSNormLinear(Linear):
         _norm._check_layer_input(x, residual, self.weight, self.in_features)
         if not self.norm_weight.is_cuda or self.norm_weight.dtype not in (torch.bfloat16, torch.float32):
             raise Fp8Error("weights are BF16 or FP32, on the GPU")
+        _one_device(x, self.weight, self.norm_weight)
         lead = x.shape[:-1]
         x2d = _norm._rows_of(x, self.in_features)
         r2d = None if residual is None else _norm._rows_of(residual, self.in_features)
@@ -427,8 +430,9 @@ class RMSNormLinear(Linear):
             raise Fp8Error("the token count must be a multiple of 16 when the weight needs a gradient")
         states = self._delayed_states(r, p, x.device) if isinstance(r, DelayedScaling) else None
         interval = r.interval if isinstance(r, DelayedScaling) else 1
-        out = _RmsNormLinearFn.apply(x2d, r2d, self.norm_weight, self.weight.contiguous(), self.eps, p, states, interval, need_dx,
-                                     need_dw)
+        with _scope(x.device, None):  # (as in Linear)
+            out = _RmsNormLinearFn.apply(x2d, r2d, self.norm_weight, self.weight.contiguous(), self.eps, p, states, interval,
+                                         need_dx, need_dw)
         if residual is None:
             return out.reshape(*lead, self.out_features)
         return out[0].reshape(*lead, self.out_features), out[1].reshape(x.shape)

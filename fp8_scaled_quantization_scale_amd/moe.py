@@ -606,5 +606,7 @@ class GroupedLinear(torch.nn.Module):
         grad = torch.is_grad_enabled()
         if grad and self.weight.requires_grad and plan.rows > _MOST_LD:
             raise Fp8Error(f"the weight's gradient takes at most {_MOST_LD} sorted rows; the plan has {plan.rows}")
-        return _GroupedLinearFn.apply(_dense(x), self.weight.contiguous(), plan, p, gather,
-                                      grad and x.requires_grad, grad and self.weight.requires_grad)
+        _one_device(x, self.weight, plan.offsets)
+        with _scope(x.device, None):  # (the weight's cast goes to the current device's stream)
+            return _GroupedLinearFn.apply(_dense(x), self.weight.contiguous(), plan, p, gather,
+                                          grad and x.requires_grad, grad and self.weight.requires_grad)
