@@ -19,16 +19,17 @@
 // registers: a 1x128 block is 16 neighbouring lanes' chunks, an MX block four
 // lanes'.  Codes with their blocks along the rows (COL) need 128 rows'
 // statistics before their first element, so a second launch reads t again, in
-// 128 x 128 tiles.  (Rows in parts of 16 to 128 MB, each with both launches, so
-// that t would still be in the Infinity Cache: 8192 x 16384 takes 411 to 289 us
-// against 280 in one part; the launches' ends cost more than the cache gives.)
+// 128 x 128 tiles.  (Rows in parts of 128, 64 or 32 MB of t, each with both launches
+// and its inputs read past the caches, so that t would still be in the Infinity
+// Cache: 8192 x 16384 takes 240, 262 or 295 us against 240 in one part; what the
+// cache gives goes to the launches' ends.)
 //
-// Measured (MI355X, BF16 with a residual): forward 8192 x 16384 182 us (5.9
-// TB/s); into 1x128 codes of both orientations 154 + 79 us (5.5 TB/s of the 1.29
-// GB that the two launches move), 8192 x 4096 42 + 20 us; backward 8192 x 4096 46
-// us (5.8 TB/s, a part of it from the Infinity Cache) and 4.7 of the weight's
-// sums, 4096 x 16384 103 us in all (5.2 TB/s).  Over 16384 columns the rows are
-// read again from the caches.
+// Measured (MI355X, BF16 with a residual): forward 8192 x 16384 183 us (5.9
+// TB/s); into 1x128 codes of both orientations 156 + 79 us (5.8 TB/s of the 1.37
+// GB that the two launches move), 8192 x 4096 42 + 19 us, under delayed scaling 60 in
+// all; backward 8192 x 4096 46 us (6.0 TB/s) and 4.7 of the weight's sums, 4096 x
+// 16384 102 us in all (5.2 TB/s).  Over 16384 columns the rows are read again from
+// the caches.
 #include "norm.hpp"
 #include "tile.hpp"
 
@@ -40,10 +41,10 @@ namespace {
 // read again, so they are no more than fill the GPU, and each has as many rows at
 // least as it takes at a time: 16 of up to 256 columns, 4 of up to 1024, else one.
 // There it takes 4 too, fewer where that leaves compute units without work (64 x
-// 2560: 1 row 6.5 us, 2 7.8, 4 10.8; 256 x 4096: 8.8, 8.5, 10.2).  The sums of the
-// short rows are so few that twice as many sets cost little (BF16, 512 or 1024 sets:
-// 262144 x 64 41.7 or 29.6 us, 262144 x 128 44.1 or 39.8, 65536 x 256 26.9 or 28.4;
-// wider rows lose, 65536 x 1024 93 or 98).
+// 2560: 1 row 6.4 us, 4 10.2; 256 x 4096: 1 8.5, 2 8.1, 4 9.6; 512 x 4096: 13.3,
+// 11.3, 11.6).  The sums of the short rows are so few that twice as many sets cost
+// little (BF16, 512 or 1024 sets: 262144 x 64 41 or 29 us, 262144 x 128 44 or 41,
+// 65536 x 256 26.9 or 28.4; wider rows lose, 65536 x 1024 94 or 100).
 constexpr int64_t kMaxPartials = 512, kMaxShortPartials = 1024;
 constexpr int64_t kShort = 256, kMiddle = 1024;  // columns
 constexpr int64_t rows_per_partial(int64_t rows, int64_t cols) {
@@ -88,10 +89,11 @@ __device__ __forceinline__ S paired_sum(const float* v) {
 // per wave, used in turn, so that one barrier is enough (a set is written again
 // only after the barrier of the other).  Within a wave by rotations (four rows to
 // a wave for NT = 16), whose latency is a fraction of the shuffles' (128 x 512
-// forward 2.9 us by shuffles, 2.7 by rotations; 8192 x 5120 backward 88.7, 84.5).
-// SHUFFLE is the backward pass over FP32 rows of up to 4096 columns, the one place
-// where shuffles measured faster (1000 x 4000 15.2 us, rotations 16.4; 8192 x 4096
-// 78.9, 81.1).
+// forward 2.9 us by shuffles, 2.6 by rotations; 8192 x 5120 backward 89.0, 85.6).
+// SHUFFLE is the backward pass over FP32 rows of 2049 to 4096 columns, the one place
+// where shuffles measured faster (1000 x 4000 15.3 us, rotations 16.3; 2000 x 4000
+// 27.4, 29.6; 4096 x 4096 48.8, 50.1; 8192 x 4096 alike), with one workgroup to a
+// compute unit: its 132 VGPRs are four too many for two.
 template <int NT, bool SHUFFLE = false>
 __device__ __forceinline__ double sum_of_row(float v, float (&red)[2][16], int& turn) {
   if constexpr (NT == 16) v = row16_total(v);
@@ -321,7 +323,8 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsArgs a) {
 // COL codes: the transposed tile, each column's blocks along its rows.  Rows
 // are staged in LDS as they were loaded; thread (cp, rq) then has 16 rows of the
 // column pair 2 cp, and the codes go back through LDS so that they
-// leave as whole 128-byte lines.
+// leave as whole 128-byte lines.  (Six waves of BF16 leave 80 VGPRs, one too few under
+// delayed scaling, which spills it; five waves without the spill take the same time.)
 // ---------------------------------------------------------------------------
 constexpr int kColThreads = 512, kColRows = kTile / (kColThreads / 64);  // rows of a wave
 
@@ -705,10 +708,10 @@ __global__ __launch_bounds__(1024) void rms_reduce_kernel(const float* partial, 
 // ---------------------------------------------------------------------------
 // Inputs that would not stay in the 256 MB Infinity Cache together are read past
 // it, and so is what the forward pass leaves of them written, but for the rows
-// that the launch for COL codes reads again: 8192 x 16384 with a residual 210 ->
-// 196 us, into codes 284 -> 246, backward 4096 x 16384 114 -> 103.  Smaller ones
+// that the launch for COL codes reads again: 8192 x 16384 with a residual 208 ->
+// 194 us, into codes 278 -> 243, backward 4096 x 16384 115 -> 102.  Smaller ones
 // may be there already from the kernel that made them: read past it, 4096 x 8192
-// into codes 43 -> 50, 3000 x 5120 FP32 backward 49 -> 54.
+// into codes 44 -> 52, 3000 x 5120 FP32 backward 49 -> 55.
 bool past_caches(const RmsParams& p) {
   const int64_t inputs = 1 + (p.residual != nullptr) + (p.dy != nullptr), es = p.x_dtype == kInBf16 ? 2 : 4;
   return p.rows > (256LL << 20) / (inputs * es * p.cols);
@@ -754,8 +757,8 @@ hipError_t forward(const RmsArgs& a, hipStream_t st) {
 }
 
 // Threads of a row, chunks of 8 columns of a thread.  Short rows by 16 lanes, four
-// of them in a wave: 262144 x 128 BF16 60.9 -> 22.5 us against a wave per row, into
-// codes 75 -> 22, backward 104 -> 40; 131072 x 256 33.9 -> 22.5, 41.6 -> 21.1, 63 -> 39.
+// of them in a wave: 262144 x 128 BF16 60 -> 23 us against a wave per row, into
+// codes 77 -> 22, backward 120 -> 41; 131072 x 256 33 -> 23, 41 -> 21, 73 -> 40.
 template <typename T, int OUT, int FMT, bool PAST, bool AGAIN>
 hipError_t forward_cols(const RmsArgs& a, hipStream_t st) {
   if (a.cols <= 128) return forward<T, 16, 1, OUT, FMT, PAST, AGAIN>(a, st);
@@ -858,8 +861,8 @@ hipError_t backward_cols(const RmsParams& p, hipStream_t st) {
   if (p.cols <= 512) return backward<T, 64, 1, 1, PAST>(p, st);
   if (p.cols <= kMiddle) return backward<T, 64, 2, 1, PAST>(p, st);
   if (p.cols <= 2048) return backward<T, 256, 1, 2, PAST>(p, st);
-  // (a row of 4096 FP32: 8192 rows 83 us by 256 threads of two chunks, 80 by 512 of
-  // one; BF16 50.7 and 54.7)
+  // (FP32, 256 threads of two chunks or 512 of one: 1000 x 4000 16.5 and 15.3 us, 2000
+  // x 4000 29.3 and 27.4, 8192 x 4096 84 and 83; BF16 8192 x 4096 52.1 and 54.0)
   if (p.cols <= 4096) return backward<T, sizeof(T) == 4 ? 512 : 256, sizeof(T) == 4 ? 1 : 2, 2, PAST>(p, st);
   if (p.cols <= 8192) return backward<T, 512, 2, 2, PAST>(p, st);
   return backward<T, 1024, 2, 0, PAST>(p, st);

@@ -26,11 +26,11 @@
 // second launch in a fixed order, over all workgroups; only integers are counted
 // with atomics.
 //
-// Measured (MI355X): forward 65536 x 256 BF16 to 8 22.6 + 5.4 us, bound by
-// instructions (605 per four tokens, 300 of them the choice; the logits' 34 MB
-// would take 7 us; choosing by marking what is taken, in the same lanes: 49 us);
-// 16384 x 64 FP32 to 4 5.7 + 4.4 us and 128 x 8 to 2 4.4 us (one launch), latency.
-// Gradient 65536 x 256 FP32 31 us (4.4 TB/s), 16384 x 64 5.2 us.
+// Measured (MI355X): forward 65536 x 256 BF16 to 8 26 + 5 us, bound by
+// instructions (718 per four tokens, 300 of them the choice, 19 us of issue; the
+// logits' 34 MB would take 6 us; choosing by marking what is taken cost 26 us more);
+// 16384 x 64 FP32 to 4 6 + 4.5 us and 128 x 8 to 2 4.4 us (one launch), latency.
+// Gradient 65536 x 256 FP32 31 us (4.3 TB/s), 16384 x 64 5.6 us.
 #include "launch.hpp"
 #include "rows.hpp"
 #include "tile.hpp"
@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kRouteMaxBlocks = 256;
 // Tokens per group of lanes up to which there is one workgroup, and one launch
-// (128 x 8: 4.8 us; of 64 tokens each with the second launch 11.4).
+// (128 x 8 4.7 us; of 64 tokens each, with the second launch, 6.2).
 constexpr int kRouteOneBlock = 4;
 
 // lanes that own a token, and the experts of a lane: the power of two that they
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteArgs a) {
 // the topk chosen experts: each lane has a choice and adds it to a row in LDS
 // that is zero otherwise, and from which the lanes take their experts' parts.
 // 4 workgroups per compute unit: what one sets up is used for more tokens (65536 x
-// 256 FP32: 44.5 us, 8 49.7, 32 71.6).
+// 256 FP32: 31 us; 2 37, 8 34, 16 37).
 constexpr int kBackThreads = 256, kBackBlocks = 4;
 
 template <typename T, int G, int V, bool EVEN>
