@@ -291,14 +291,15 @@ def _read_only(t: torch.Tensor) -> bool:
     if t.grad_fn is None:
         return False
     made_by = getattr(type((t._base if t._is_view() else t).grad_fn), "_forward_cls", None)
-    return made_by is not None and made_by.__module__.partition(".")[0] == __name__.partition(".")[0]
+    return made_by is not None and made_by.__module__.rpartition(".")[0] == __package__
 
 
 def _apart(x: torch.Tensor, residual: torch.Tensor | None) -> bool:
     """The two need gradients in memory of their own.  Autograd takes a gradient
-    over as a leaf's .grad, which later passes and users write to, where it sees no
-    other holder of the tensor; behind a view it does not see that of the other's."""
-    return residual is not None and x.requires_grad and residual.requires_grad and not (_read_only(x) or _read_only(residual))
+    over as a leaf's .grad, which later passes, hooks and users write to, where it
+    sees no other holder of the tensor; behind a view it does not see the other's.
+    Where both end in backward passes of this package, neither is written to."""
+    return residual is not None and x.requires_grad and residual.requires_grad and not (_read_only(x) and _read_only(residual))
 
 
 def _to_both(dx, need_x: bool, need_residual: bool, apart: bool):

@@ -41,21 +41,24 @@ def test_leaves(which, outputs, shape):
 
 
 @pytest.mark.parametrize("which", ["norm", "linear"])
-def test_behind_a_layer(which):
-    """x from a layer of the package, the residual a leaf: no copy is made, and the
-    gradients are those of the two by themselves."""
+@pytest.mark.parametrize("leaf", [False, True])
+def test_behind_layers(which, leaf):
+    """x from a layer of the package, the residual from another, when no copy is made,
+    or a leaf: the gradients are those of the two by themselves."""
     need_gpu()
     torch.manual_seed(3)
     layer, before = _layers()[which], linear.Linear(128, 256, recipe=linear.Float8BlockScaling(), device="cuda")
+    first = norm.RMSNorm(256, device="cuda")
     a, res = torch.randn(4, 16, 128, device="cuda").bfloat16().requires_grad_(), torch.randn(4, 16, 256, device="cuda").bfloat16().requires_grad_()
-    x = before(a)
-    assert not norm._apart(norm._rows_of(x, 256), norm._rows_of(res, 256))
-    alone = x.detach().requires_grad_()
-    dy = None
-    for xs in (x, alone):
-        y, total = layer(xs, res)
-        dy = torch.randn_like(y) if dy is None else dy
-        torch.autograd.backward([y, total], [dy, torch.ones_like(total)])
-    assert torch.equal(res.grad, 2 * alone.grad)  # (from both passes)
-    want, = torch.autograd.grad(before(a), a, alone.grad)
+    x, stream = before(a), res if leaf else first(res)
+    assert norm._apart(norm._rows_of(x, 256), norm._rows_of(stream, 256)) == leaf
+    alone = [t.detach().requires_grad_() for t in (x, stream)]
+    y, total = layer(*alone)
+    dy = torch.randn_like(y)
+    torch.autograd.backward([y, total], [dy, torch.ones_like(total)])
+    y, total = layer(x, stream)
+    torch.autograd.backward([y, total], [dy, torch.ones_like(total)])
+    want, = torch.autograd.grad(before(a), a, alone[0].grad)
     assert torch.equal(a.grad, want)
+    want = alone[1].grad if leaf else torch.autograd.grad(first(res), res, alone[1].grad)[0]
+    assert torch.equal(res.grad, want)

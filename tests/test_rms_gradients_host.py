@@ -83,9 +83,28 @@ def test_gradients_are_not_shared(how, outputs):
 def test_no_copy_where_a_backward_pass_of_the_package_reads_it():
     """(the residual stream between the package's layers costs no copy)"""
     x, res = _leaf(ROWS, COLS), _leaf(ROWS, COLS)
-    assert norm._apart(x, res) and norm._apart(x.view(-1), res) and norm._apart(x * 1.0, res)
-    made = _Made.apply(x)
-    for a, b in ((made, res), (x, made), (made.view(3, 2, COLS).reshape(ROWS, COLS), res)):
+    made, other = _Made.apply(x), _Made.apply(res)
+    view = made.view(3, 2, COLS).reshape(ROWS, COLS)
+    for a, b in ((made, other), (view, other), (other, view), (made[:2], other), (made, made)):
         assert not norm._apart(a, b)
-    assert norm._apart(made.detach().requires_grad_(), res) and norm._apart(made + res, res)
+    for a in (x, x.view(-1), x * 1.0, made + res, made.detach().requires_grad_()):
+        assert norm._apart(a, res) and norm._apart(a, x * 2.0) and norm._apart(a, other) and norm._apart(other, a)
     assert not norm._apart(x, None) and not norm._apart(x, res.detach())
+
+
+def test_a_leaf_s_hook_does_not_reach_the_other_gradient():
+    """A hook that scales a leaf's .grad as soon as it is there (an optimizer's step in
+    the backward pass) while the other gradient has yet to be read."""
+    torch.manual_seed(4)
+    x, res, w = _leaf(2, 3, COLS), _leaf(ROWS, COLS), _leaf(COLS)
+
+    def hook(t):
+        t.grad.zero_()
+
+    x.register_post_accumulate_grad_hook(hook)
+    made = _Made.apply(res)
+    y, total = norm._RMSNormFn.apply(x.reshape(ROWS, COLS), w, made, 1e-6)  # (what was made last goes first)
+    dy, dtotal = torch.randn(ROWS, COLS, dtype=torch.float64), torch.randn(ROWS, COLS, dtype=torch.float64)
+    torch.autograd.backward([y, total], [dy, dtotal])
+    want, _ = norm.rms_norm_backward(dy, total.detach(), w.detach(), (total.detach().square().mean(1) + 1e-6) ** -0.5, dtotal)
+    assert torch.equal(res.grad, want) and not x.grad.any()
