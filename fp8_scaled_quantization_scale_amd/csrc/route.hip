@@ -506,10 +506,20 @@ __global__ __launch_bounds__(kBackThreads) void route_backward_kernel(RouteArgs 
     add[at + O::expert(i)] = 0.0f;
   }
   if (a.dloss) {
+    // What all slopes have in common (all of it, with even loads) has no gradient: it
+    // is taken out before anything is rounded to its size.
     const float d = *a.dloss;
+    float least = kNegInf;  // (of their negatives the largest)
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (O::expert(i) < n) slope[i] = d * a.slope[at + O::expert(i)];
+      if (O::expert(i) < n) {
+        slope[i] = a.slope[at + O::expert(i)];
+        least = fmaxf(least, -slope[i]);
+      }
+    least = fmaxf(-lanes_fmax<G>(least), 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (O::expert(i) < n) slope[i] = d * (slope[i] - least);
   }
   const int tokens = (int)a.tokens, step = (int)gridDim.x * kGroups;  // (at most 2^30 tokens)
   Logits<T, G, V, EVEN> raw{};

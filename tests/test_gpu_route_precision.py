@@ -117,3 +117,38 @@ def test_normalized_weights_where_one_expert_has_nearly_all(experts, topk, far):
     tol = w * (c * E32 * (off.abs() + (w * off.abs()).sum(1, keepdim=True)) + (c * E32) ** 2 * dw.abs().amax(1, keepdim=True)) + 2 * DENORMAL
     bad = (got.double().gather(1, at) - w * off).abs() > tol
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}"
+
+
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("experts", [1, 2, 7, 16, 64, 256, 300, 1000])
+def test_loss_gradient_with_even_loads(experts, dt):
+    """p (s - <p, s>), s = slope dloss: what all slopes have in common has no gradient.
+    Equal slopes give zeros; slopes that differ by steps of 2^-22 of themselves (their
+    differences are exact) an error in proportion to the differences, P and ADDS as above."""
+    need_gpu()
+    l, g = _logits(300, experts, dt, -12, 2)
+    dloss = torch.tensor(0.3, device="cuda")
+    slope = torch.full((experts,), 1.7, device="cuda")
+    assert not moe.route_backward(l, None, None, slope, dloss).any()
+    over = torch.randint(0, 64, (experts,), generator=g, device="cuda").float() * 2.0 ** -22
+    slope = 1.5 + over
+    assert torch.equal(slope.double() - 1.5, over.double())
+    got = moe.route_backward(l, None, None, slope, dloss)
+    s = (slope.double() - slope.double().min()) * dloss.double()
+    p = torch.softmax(l.double(), 1)
+    ref = p * (s - (p * s).sum(1, keepdim=True))
+    size = p * (s + (p * s).sum(1, keepdim=True))
+    adds = _adds(experts)
+    tol = (2 * (2 * EXP + adds + 2) + adds + 4) * E32 * size + U[dt] * ref.abs()
+    assert ((got.double() - ref).abs() <= tol).all()
+
+
+def test_loss_gradient_of_even_routing():
+    """Each expert chosen as often: the loss has no gradient, to the bit."""
+    need_gpu()
+    l = torch.randn(64, 8, device="cuda").requires_grad_()
+    expert = (torch.arange(64, device="cuda")[:, None] + torch.arange(2, device="cuda")).remainder(8)
+    loss, counts, _ = moe.balance(l, expert)
+    assert (counts == 16).all()
+    loss.backward()
+    assert not l.grad.any()
